@@ -17,6 +17,12 @@
  *      H-head indexer re-ranks them to the final k              (misa_hier_rerank)
  *   5. the dense DSA indexer, all H heads                      (dsa_index_dense)
  *
+ * and, around the indexer, the key/value cache and the attention that reads it:
+ *   6. new keys and values, rotated, into a paged cache        (misa_cache_append)
+ *   7. attention over the selected tokens                      (misa_attend_selected)
+ *   8. attention over the whole cache, also behind a prefix
+ *      that the batch shares             (misa_attend, misa_attend_shared)
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - All array arguments are DEVICE pointers to caller-owned memory. The library
@@ -333,6 +339,147 @@ MISA_API int32_t misa_pivot_indexer(const void* q, const float* w, const void* k
                                     const int32_t* q_len, int64_t T, int32_t H, int32_t d, int64_t nseq, int64_t Lmax,
                                     int32_t G, int32_t kc, int32_t topk, int32_t* cand, int32_t* idx, float* score,
                                     void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Key/value cache and attention
+ *
+ * A cache holds one row of d elements per token and kv head, keys and values
+ * apart, in pages of `page` tokens. Token s of sequence n lies in row s % page
+ * of page table[n][s / page]; without a table sequence n is page n (the layout
+ * k [nseq][Lmax][d] of the indexer keys is such a cache, with one head and
+ * page = Lmax). The element of (page p, row r, head g, i) is at
+ *     p * page_stride + r * token_stride + g * head_stride + i
+ * in elements, the same for k and v, so token-major and head-major pages both
+ * fit; strides are positive multiples of 8 and the pointers 16-byte aligned.
+ * The struct is read on the host during the call only; k, v and table are
+ * device memory.
+ *  - d: any multiple of 16 up to 1024 to append; 64, 128 or 256 to attend.
+ *  - A sequence can address table_cols * page tokens (page without a table),
+ *    less than 2^31 - 65536.
+ *  - A table entry outside [0, npages) is no page: nothing is written there, and
+ *    its tokens are not visible.
+ */
+#define MISA_BF16 1
+#define MISA_FP16 2
+typedef struct misa_kv_cache {
+  void* k;
+  void* v;                /* NULL: a cache of keys alone (append only) */
+  int64_t npages;
+  int64_t page;           /* tokens per page */
+  int64_t page_stride;    /* in elements */
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t heads;          /* kv heads */
+  int32_t d;
+  int32_t dtype;          /* MISA_BF16 or MISA_FP16 */
+  const int32_t* table;   /* [nseq][table_cols] or NULL */
+  int64_t table_cols;
+  int64_t nseq;           /* rows of the table (without one: npages) */
+} misa_kv_cache;
+
+/*
+ * Appends N tokens to the cache, rotating their keys (and, in the same launch,
+ * their queries) by the angles of their positions.
+ *   k, v   [N][heads][d]  the new keys and values, of the cache's type; v is NULL
+ *          exactly when the cache has no values
+ *   q      [N][Hq][d]     queries of the same tokens, rotated into q_out; both may
+ *          be NULL (Hq = 0). q_out may be q itself (with the same strides).
+ *   *_ts, *_hs            token and head strides of these arrays in elements,
+ *          multiples of 8 (slices of one fused projection need no copy)
+ *   q_seq, q_tok  int32 [N]  the token's sequence and its index there
+ *   q_pos  int32 [N]      rotary position, or NULL: q_tok
+ *   cos_sin fp32 [P][rot] cosines, then sines, of the rot / 2 angles of position p
+ *   rot    rotated elements at the start of each row, a multiple of 16 up to d;
+ *          0: none (cos_sin may be NULL)
+ *   interleaved  pairs (2i, 2i + 1) instead of (i, i + rot / 2)
+ * Pair i becomes (a cos - b sin, b cos + a sin), computed in fp32 and rounded
+ * once. A token whose sequence, index, page or (rot > 0) position is out of
+ * range is skipped: neither the cache nor its q_out rows are written. No two
+ * tokens of a call may have the same (sequence, index) or share a page's row
+ * (the row would hold parts of both). Rows of other tokens keep their values.
+ * The pooled keys of an indexer cache follow with misa_pool_update.
+ * Errors: MISA_ERR_ARG (sizes, null pointers), MISA_ERR_ALIGN.
+ */
+MISA_API int32_t misa_cache_append(const misa_kv_cache* cache, const void* k, int64_t k_ts, int64_t k_hs, const void* v,
+                                   int64_t v_ts, int64_t v_hs, const void* q, int64_t q_ts, int64_t q_hs, void* q_out,
+                                   int64_t o_ts, int64_t o_hs, int32_t Hq, const int32_t* q_seq, const int32_t* q_tok,
+                                   const int32_t* q_pos, const float* cos_sin, int64_t P, int32_t rot,
+                                   int32_t interleaved, int64_t N, void* stream);
+
+/*
+ * Attention of T queries over their sequences' caches. For query t and head
+ * j (kv head g = j / (Hq / heads)), over the visible tokens
+ * q_start[t] <= s < q_len[t]:
+ *     x_s = scale * q[t][j] . k_s
+ *     x_s = cap * tanh(x_s / cap)                     if cap > 0
+ *     x_s = x_s - slopes[j] * |q_pos[t] - s|          if slopes
+ *     out[t][j] = sum_s exp(x_s - m) v_s / sum_s exp(x_s - m),   lse = log sum_s exp(x_s)
+ * A causal query at position t has q_len = t + 1; a decode step has one query
+ * per sequence; a document mask sets q_start to the document's first token, a
+ * sliding window to t + 1 - window; a bidirectional prefix raises q_len to it.
+ * Queries of one sequence next to each other share its keys.
+ *   q        [T][Hq][d] of the cache's type, strides q_ts, q_hs in elements
+ *            (multiples of 8); Hq a multiple of the cache's heads
+ *   q_seq, q_len  int32 [T];  q_start  int32 [T] or NULL (0)
+ *   q_pos    int32 [T] or NULL (q_len - 1); read with slopes only
+ *   scale    > 0;  cap  >= 0, 0: none;  slopes  fp32 [Hq] or NULL
+ *   out      [T][Hq][d] of the cache's type;  lse  fp32 [T][Hq] or NULL
+ * A query that sees nothing (empty interval, sequence out of range) gets zeros
+ * and lse = -inf. q_len is clamped to what a sequence can address, q_start to
+ * [0, q_len]. What a query does not see may hold anything, NaN included; a NaN
+ * or an infinity reaches exactly the queries that see it.
+ *   ws: misa_attend_workspace_bytes(MISA_OP_ATTEND, T, Hq, heads, d, nseq, 0)
+ * Errors: MISA_ERR_ARG, MISA_ERR_ALIGN, MISA_ERR_WORKSPACE.
+ */
+MISA_API int32_t misa_attend(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs,
+                             const int32_t* q_seq, const int32_t* q_start, const int32_t* q_len, const int32_t* q_pos,
+                             int64_t T, int32_t Hq, float scale, float cap, const float* slopes, void* out, float* lse,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Attention over selected tokens, the consumer of the indexers' output (MISA
+ * abstract; "Probleemstelling": the selected set is shared by all heads): as
+ * misa_attend, over the tokens idx[t][0 .. topk) of sequence q_seq[t]. Entries
+ * outside [0, q_len[t]) (the -1 padding) are skipped, the others count once per
+ * occurrence, in any order.
+ *   idx  int32 [T][topk]
+ *   ws: misa_attend_workspace_bytes(MISA_OP_ATTEND_SELECTED, T, Hq, heads, d, nseq, 0)
+ */
+MISA_API int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs,
+                                      const int32_t* idx, int32_t topk, const int32_t* q_seq, const int32_t* q_len,
+                                      const int32_t* q_pos, int64_t T, int32_t Hq, float scale, float cap,
+                                      const float* slopes, void* out, float* lse, void* ws, size_t ws_bytes,
+                                      void* stream);
+
+/*
+ * Attention of a batch whose sequences share long prefixes: query t sees the
+ * pre_len[pre[t]] tokens of prefix pre[t], at positions 0 .., and behind them
+ * the q_len[t] tokens of its own sequence. The keys of a prefix are read once
+ * for its queries that stand next to each other in the batch, instead of once
+ * per sequence; the two parts are joined by their log-sums.
+ *   pre        int32 [T]  prefix of each query; outside [0, npre): none
+ *   pre_len    int32 [npre]
+ *   pre_table  int32 [npre][pre_cols] pages of the prefixes in the same cache, or
+ *              NULL: prefix i is page i
+ *   q_pos      int32 [T] or NULL (pre_len + q_len - 1); read with slopes only
+ *   the rest as misa_attend (q_seq, q_len: the own part)
+ *   ws: misa_attend_workspace_bytes(MISA_OP_ATTEND_SHARED, T, Hq, heads, d, nseq, npre)
+ */
+MISA_API int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs,
+                                    const int32_t* q_seq, const int32_t* q_len, const int32_t* q_pos,
+                                    const int32_t* pre, const int32_t* pre_len, const int32_t* pre_table,
+                                    int64_t pre_cols, int64_t npre, int64_t T, int32_t Hq, float scale, float cap,
+                                    const float* slopes, void* out, float* lse, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* op codes of misa_attend_workspace_bytes */
+#define MISA_OP_ATTEND 10
+#define MISA_OP_ATTEND_SELECTED 11
+#define MISA_OP_ATTEND_SHARED 12
+
+/* Workspace bytes of one attention call (0: none needed, or sizes out of range). */
+MISA_API size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t heads, int32_t d, int64_t nseq,
+                                            int64_t npre);
 
 /*
  * Full score rows of the routed scoring step (a diagnostic of step 3 above):

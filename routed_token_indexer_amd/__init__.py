@@ -9,6 +9,7 @@ __version__ = "0.1.0"
 
 _EXPORTS = ("pool_keys", "route", "score_topk", "hier_rerank", "dsa_index_dense", "indexer", "hier_indexer",
             "debug_scores",
+            "cache_append", "attend", "attend_selected", "attend_shared", "attend_workspace_bytes",
             "workspace_bytes", "timing_begin", "timing_end", "MisaError")
 
 

@@ -30,6 +30,12 @@ OP_HIER_INDEXER = 6
 OP_BLOCK_FILTER = 7
 OP_BLOCK_INDEXER = 8
 OP_PIVOT_INDEXER = 9
+OP_ATTEND = 10
+OP_ATTEND_SELECTED = 11
+OP_ATTEND_SHARED = 12
+
+BF16 = 1
+FP16 = 2
 
 KERNEL_SCORE = 1
 KERNEL_TOPK = 2
@@ -43,6 +49,16 @@ _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+
+_F32 = ctypes.c_float
+
+
+class KvCache(ctypes.Structure):
+    """misa_kv_cache: where a cache lies and how it is paged."""
+    _fields_ = [("k", _P), ("v", _P), ("npages", _I64), ("page", _I64), ("page_stride", _I64), ("token_stride", _I64),
+                ("head_stride", _I64), ("heads", _I32), ("d", _I32), ("dtype", _I32), ("table", _P),
+                ("table_cols", _I64), ("nseq", _I64)]
+
 
 _SIGNATURES = {
     "misa_version": (_I32, []),
@@ -70,6 +86,14 @@ _SIGNATURES = {
                                   _P, _SZ, _P]),
     "misa_hier_indexer_noalloc": (_I32, [_P, _P, _P, _P, _P, _P, _I64, _I32, _I32, _I64, _I64, _I32, _I32, _I32,
                                          _I32, _P, _P, _P, _P, _P]),
+    "misa_attend_workspace_bytes": (_SZ, [_I32, _I64, _I32, _I32, _I32, _I64, _I64]),
+    "misa_cache_append": (_I32, [_P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I32, _P, _P, _P,
+                                 _P, _I64, _I32, _I32, _I64, _P]),
+    "misa_attend": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I32, _F32, _F32, _P, _P, _P, _P, _SZ, _P]),
+    "misa_attend_selected": (_I32, [_P, _P, _I64, _I64, _P, _I32, _P, _P, _P, _I64, _I32, _F32, _F32, _P, _P, _P, _P,
+                                    _SZ, _P]),
+    "misa_attend_shared": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _F32, _F32, _P,
+                                  _P, _P, _P, _SZ, _P]),
     "misa_timing_begin": (_I32, [_I32, _I32, _P]),
     "misa_timing_end": (_I32, [_P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int32)]),
 }
@@ -328,6 +352,227 @@ def hier_indexer_noalloc(q, w, k, kbar, q_seq, q_len, B: int, h: int, kc: int, t
                                            nseq, L, B, h, kc, topk, _ptr(heads), _ptr(cand), _ptr(idx), _ptr(score),
                                            _stream(stream)))
     return idx, score
+
+
+_KV_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16}
+
+
+def _rows(x: torch.Tensor, name: str, ref: torch.Tensor, n: Optional[int] = None, heads: Optional[int] = None):
+    """A [tokens, heads, d] tensor of ``ref``'s type, device and d, rows contiguous."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dtype != ref.dtype:
+        raise TypeError(f"{name}: expected {ref.dtype}, got {x.dtype}")
+    if x.device != ref.device:
+        raise ValueError(f"{name}: on {x.device}, the cache on {ref.device}")
+    shape = x.shape
+    if len(shape) != 3 or shape[2] != ref.shape[-1] or (n is not None and shape[0] != n) or \
+            (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: got shape {tuple(shape)}, expected [{'tokens' if n is None else n}, "
+                         f"{'heads' if heads is None else heads}, {ref.shape[-1]}]")
+    ts, hs, es = x.stride()
+    if es != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    # the stride of an axis of one element is never used
+    return ts if shape[0] > 1 else 8 * max(1, ts // 8), hs if shape[1] > 1 else 8 * max(1, hs // 8)
+
+
+def _vec(x: Optional[torch.Tensor], name: str, dtype, shape, device):
+    """Pointer of a contiguous tensor of this dtype and shape (None stays None)."""
+    if x is None:
+        return None
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.device != device:
+        raise ValueError(f"{name}: on {x.device}, the cache on {device}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name}: got shape {tuple(x.shape)}, expected {tuple(shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return x.data_ptr()
+
+
+def _kv_cache(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], table: Optional[torch.Tensor]):
+    """misa_kv_cache of cache tensors [pages, page, heads, d] (any strides with
+    contiguous rows), or [nseq, Lmax, d] for one head without pages."""
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache: expected a torch.Tensor")
+    if k_cache.dtype not in _KV_DTYPES:
+        raise TypeError(f"k_cache: expected bfloat16 or float16, got {k_cache.dtype}")
+    if not k_cache.is_cuda:
+        raise ValueError("k_cache: must be a device tensor")
+    if v_cache is not None:
+        if not isinstance(v_cache, torch.Tensor) or v_cache.dtype != k_cache.dtype:
+            raise TypeError(f"v_cache: expected a tensor of {k_cache.dtype}")
+        if v_cache.device != k_cache.device:
+            raise ValueError(f"v_cache: on {v_cache.device}, k_cache on {k_cache.device}")
+        if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+            raise ValueError("v_cache: must have the shape and strides of k_cache")
+    if k_cache.dim() == 3:
+        npages, page, d = k_cache.shape
+        heads = 1
+        ps, ts, es = k_cache.stride()
+        hs = 8
+    elif k_cache.dim() == 4:
+        npages, page, heads, d = k_cache.shape
+        ps, ts, hs, es = k_cache.stride()
+    else:
+        raise ValueError(f"k_cache: expected 3 or 4 dims, got shape {tuple(k_cache.shape)}")
+    if es != 1 and d > 1:
+        raise ValueError("k_cache: rows must be contiguous")
+    one = lambda n, s: s if n > 1 else 8 * max(1, s // 8)   # noqa: E731  (an axis of one element)
+    c = KvCache(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), npages, page, one(npages, ps),
+                one(page, ts), one(heads, hs), heads, d, _KV_DTYPES[k_cache.dtype], None, 0, npages)
+    if table is not None:
+        if table.dim() != 2:
+            raise ValueError(f"table: expected 2 dims, got shape {tuple(table.shape)}")
+        c.table = _vec(table, "table", torch.int32, table.shape, k_cache.device)
+        c.nseq, c.table_cols = table.shape
+    return c
+
+
+def _on(device, stream):
+    """Stream to launch on: the given one, or the current one of the tensors' device."""
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _call(device, name: str, *args):
+    """One library call with ``device`` as the current one."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args)
+    if rc != MISA_OK:
+        _check(name, rc)
+
+
+def attend_workspace_bytes(op: int, T: int, Hq: int, heads: int, d: int, nseq: int, npre: int = 0) -> int:
+    return int(lib().misa_attend_workspace_bytes(op, T, Hq, heads, d, nseq, npre))
+
+
+def cache_append(k, v, k_cache, v_cache, q_seq, q_tok, table=None, q=None, q_out=None, cos_sin=None, pos=None,
+                 interleaved=False, stream=None):
+    """Append tokens to a cache, rotated on the way; returns ``q_out``.
+
+    k, v [N, heads, d] (v None for a cache of keys alone), q [N, Hq, d] optional;
+    k_cache, v_cache [pages, page, heads, d] with ``table`` [nseq, cols] int32, or
+    rows of whole sequences ([nseq, Lmax, d] or [nseq, Lmax, heads, d]) without
+    one. Token i goes to index ``q_tok[i]`` of sequence ``q_seq[i]`` and is
+    rotated by row ``pos[i]`` (default: ``q_tok[i]``) of ``cos_sin`` [P, rot] fp32
+    (cosines, then sines; None: no rotation). ``interleaved`` pairs neighbours
+    instead of halves. Tokens out of range are skipped.
+    """
+    c = _kv_cache(k_cache, v_cache, table)
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    dev = k_cache.device
+    k_ts, k_hs = _rows(k, "k", k_cache, None, c.heads)
+    N = k.shape[0]
+    v_ts, v_hs = (0, 0) if v is None else _rows(v, "v", k_cache, N, c.heads)
+    q_ts = q_hs = o_ts = o_hs = Hq = 0
+    if q is not None:
+        q_ts, q_hs = _rows(q, "q", k_cache, N)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        o_ts, o_hs = _rows(q_out, "q_out", k_cache, N, Hq)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    P = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError(f"cos_sin: expected 2 dims, got shape {tuple(cos_sin.shape)}")
+        P, rot = cos_sin.shape
+    _call(dev, "misa_cache_append", ctypes.byref(c), k.data_ptr(), k_ts, k_hs, None if v is None else v.data_ptr(), v_ts,
+          v_hs, None if q is None else q.data_ptr(), q_ts, q_hs, None if q is None else q_out.data_ptr(), o_ts, o_hs, Hq,
+          _vec(q_seq, "q_seq", torch.int32, (N,), dev), _vec(q_tok, "q_tok", torch.int32, (N,), dev),
+          _vec(pos, "pos", torch.int32, (N,), dev),
+          None if cos_sin is None else _vec(cos_sin, "cos_sin", torch.float32, (P, rot), dev), P, rot, int(interleaved),
+          N, _on(dev, stream))
+    return q_out
+
+
+def _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale, slopes, out, lse, want_lse):
+    if v_cache is None:
+        raise ValueError("v_cache: attention needs values")
+    c = _kv_cache(k_cache, v_cache, table)
+    dev = k_cache.device
+    q_ts, q_hs = _rows(q, "q", k_cache)
+    T, Hq, d = q.shape
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    ptrs = (_vec(q_seq, "q_seq", torch.int32, (T,), dev), _vec(q_len, "q_len", torch.int32, (T,), dev),
+            _vec(q_pos, "q_pos", torch.int32, (T,), dev), _vec(slopes, "slopes", torch.float32, (Hq,), dev),
+            _vec(out, "out", k_cache.dtype, (T, Hq, d), dev), _vec(lse, "lse", torch.float32, (T, Hq), dev))
+    return c, dev, q_ts, q_hs, T, Hq, float(scale), out, lse, ptrs
+
+
+def _attend_ws(ws, op, T, Hq, c, dev, npre=0):
+    need = attend_workspace_bytes(op, T, Hq, c.heads, c.d, c.nseq, npre)
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws: on {ws.device}, the cache on {dev}")
+    return _workspace(ws, need, dev)
+
+
+def attend(q, k_cache, v_cache, q_seq, q_len, table=None, q_start=None, q_pos=None, scale=None, cap=0.0, slopes=None,
+           out=None, lse=None, want_lse=False, ws=None, stream=None):
+    """Attention of q [T, Hq, d] over the tokens [q_start, q_len) of their
+    sequences' cache (layouts as in ``cache_append``): out [T, Hq, d], lse [T, Hq]
+    (natural log; None unless wanted). ``scale`` defaults to d ** -0.5; ``cap``
+    > 0 caps the scores by cap * tanh(x / cap); ``slopes`` [Hq] subtracts
+    slope * |q_pos - s| (q_pos default: q_len - 1)."""
+    c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
+                                                                   slopes, out, lse, want_lse)
+    ws = _attend_ws(ws, OP_ATTEND, T, Hq, c, dev)
+    _call(dev, "misa_attend", ctypes.byref(c), q.data_ptr(), q_ts, q_hs, p[0],
+          _vec(q_start, "q_start", torch.int32, (T,), dev), p[1], p[2], T, Hq, scale, cap, p[3], p[4], p[5],
+          ws.data_ptr(), ws.numel(), _on(dev, stream))
+    return out, lse
+
+
+def attend_selected(q, k_cache, v_cache, idx, q_seq, q_len, table=None, q_pos=None, scale=None, cap=0.0, slopes=None,
+                    out=None, lse=None, want_lse=False, ws=None, stream=None):
+    """As ``attend``, over the tokens idx [T, topk] that an indexer selected
+    (entries outside [0, q_len) are skipped)."""
+    c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
+                                                                   slopes, out, lse, want_lse)
+    if idx.dim() != 2:
+        raise ValueError(f"idx: expected 2 dims, got shape {tuple(idx.shape)}")
+    topk = idx.shape[1]
+    ws = _attend_ws(ws, OP_ATTEND_SELECTED, T, Hq, c, dev)
+    _call(dev, "misa_attend_selected", ctypes.byref(c), q.data_ptr(), q_ts, q_hs,
+          _vec(idx, "idx", torch.int32, (T, topk), dev), topk, p[0], p[1], p[2], T, Hq, scale, cap, p[3], p[4], p[5],
+          ws.data_ptr(), ws.numel(), _on(dev, stream))
+    return out, lse
+
+
+def attend_shared(q, k_cache, v_cache, q_seq, q_len, pre, pre_len, table=None, pre_table=None, q_pos=None, scale=None,
+                  cap=0.0, slopes=None, out=None, lse=None, want_lse=False, ws=None, stream=None):
+    """As ``attend``, for sequences that share prefixes: query t sees the
+    pre_len[pre[t]] tokens of prefix pre[t] (pages pre_table [npre, cols]; without
+    a table prefix i is page i), then the q_len[t] tokens of its own sequence."""
+    c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
+                                                                   slopes, out, lse, want_lse)
+    npre = pre_len.shape[0]
+    cols = 0
+    if pre_table is not None:
+        if pre_table.dim() != 2:
+            raise ValueError(f"pre_table: expected 2 dims, got shape {tuple(pre_table.shape)}")
+        cols = pre_table.shape[1]
+    ws = _attend_ws(ws, OP_ATTEND_SHARED, T, Hq, c, dev, npre)
+    _call(dev, "misa_attend_shared", ctypes.byref(c), q.data_ptr(), q_ts, q_hs, p[0], p[1], p[2],
+          _vec(pre, "pre", torch.int32, (T,), dev), _vec(pre_len, "pre_len", torch.int32, (npre,), dev),
+          None if pre_table is None else _vec(pre_table, "pre_table", torch.int32, (npre, cols), dev), cols, npre, T, Hq,
+          scale, cap, p[3], p[4], p[5], ws.data_ptr(), ws.numel(), _on(dev, stream))
+    return out, lse
 
 
 def timing_begin(kernel: int, capacity: int = 4096, stream=None):

@@ -14,7 +14,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmisa.so")
-SOURCES = ["abi.hip", "pool.hip", "route.hip", "score.hip", "topk.hip", "topk_split.hip", "block.hip", "pivot.hip"]
+SOURCES = ["abi.hip", "pool.hip", "route.hip", "score.hip", "topk.hip", "topk_split.hip", "block.hip", "pivot.hip",
+           "append.hip", "attend.hip", "attend_d64.hip", "attend_d128.hip", "attend_d256.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "misa.h"
+#include "misa_attend.hpp"
 #include "misa_internal.hpp"
 
 namespace {
@@ -250,6 +251,95 @@ int32_t scratch_of_stream(const char* fn, hipStream_t st, void** out) {
   }
   *out = g_scratch_ptr[dev];
   return MISA_OK;
+}
+
+// ---------------------------------------------------------------- cache and attention
+// Token indices stay below this, so that a tile past the last one still fits 31 bits.
+constexpr int64_t kMaxTokens = (int64_t(1) << 31) - 65536;
+
+bool stride_ok(int64_t s) { return s > 0 && s % 8 == 0; }
+
+// Checks a cache and turns it into the kernels' view.
+int32_t check_cache(const char* fn, const misa_kv_cache* c, misa::KvView* out) {
+  if (!c) return fail(MISA_ERR_ARG, "%s: null cache", fn);
+  if (c->dtype != MISA_BF16 && c->dtype != MISA_FP16) return fail(MISA_ERR_ARG, "%s: dtype = %d", fn, c->dtype);
+  if (c->heads < 1 || c->heads > 1024) return fail(MISA_ERR_ARG, "%s: heads = %d not in [1, 1024]", fn, c->heads);
+  if (c->npages < 1 || c->npages >= (int64_t(1) << 31)) return fail(MISA_ERR_ARG, "%s: npages = %lld out of range", fn, (long long)c->npages);
+  if (c->page < 1 || c->page > kMaxTokens) return fail(MISA_ERR_ARG, "%s: page = %lld out of range", fn, (long long)c->page);
+  if (!c->k) return fail(MISA_ERR_ARG, "%s: null key cache", fn);
+  if (c->table) {
+    if (c->nseq < 1) return fail(MISA_ERR_ARG, "%s: nseq = %lld < 1", fn, (long long)c->nseq);
+    if (c->table_cols < 1 || c->table_cols > kMaxTokens / c->page)
+      return fail(MISA_ERR_ARG, "%s: table_cols = %lld out of range", fn, (long long)c->table_cols);
+  } else if (c->nseq != c->npages) {
+    return fail(MISA_ERR_ARG, "%s: without a table nseq = %lld must be npages = %lld", fn, (long long)c->nseq, (long long)c->npages);
+  }
+  if (!stride_ok(c->page_stride) || !stride_ok(c->token_stride) || !stride_ok(c->head_stride))
+    return fail(MISA_ERR_ALIGN, "%s: cache strides must be positive multiples of 8", fn);
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(MISA_ERR_ALIGN, "%s: k and v caches must be 16-byte aligned", fn);
+  if (!aligned(c->table, 4)) return fail(MISA_ERR_ALIGN, "%s: table must be 4-byte aligned", fn);
+  misa::KvView v{};
+  v.k = static_cast<uint16_t*>(c->k);
+  v.v = static_cast<uint16_t*>(c->v);
+  v.page_stride = c->page_stride;
+  v.tok_stride = c->token_stride;
+  v.head_stride = c->head_stride;
+  v.npages = c->npages;
+  v.page = (int32_t)c->page;
+  v.by_page = misa::fast_div((uint32_t)c->page);
+  v.table = c->table;
+  v.table_stride = c->table_cols;
+  v.nseq = c->nseq;
+  v.Lmax = c->table ? c->table_cols * c->page : c->page;
+  *out = v;
+  return MISA_OK;
+}
+
+// Checks shared by the attention calls; fills what they have in common.
+int32_t check_attend(const char* fn, const misa_kv_cache* c, const void* q, int64_t q_ts, int64_t q_hs,
+                     const int32_t* q_seq, const int32_t* q_len, const int32_t* q_pos, int64_t T, int32_t Hq,
+                     float scale, float cap, const float* slopes, void* out, float* lse, misa::AttendArgs* a) {
+  int32_t rc = check_cache(fn, c, &a->kv);
+  if (rc) return rc;
+  if (!(c->d == 64 || c->d == 128 || c->d == 256)) return fail(MISA_ERR_ARG, "%s: d = %d not in {64, 128, 256}", fn, c->d);
+  if (!c->v) return fail(MISA_ERR_ARG, "%s: null value cache", fn);
+  if (T < 0 || T >= (int64_t(1) << 31)) return fail(MISA_ERR_ARG, "%s: T = %lld out of range", fn, (long long)T);
+  if (Hq < 1 || Hq % c->heads || Hq > 65536) return fail(MISA_ERR_ARG, "%s: Hq = %d not a multiple of heads = %d", fn, Hq, c->heads);
+  if (!(scale > 0.f) || scale > 1e30f) return fail(MISA_ERR_ARG, "%s: scale = %g must be positive and finite", fn, scale);
+  if (!(cap >= 0.f) || cap > 1e30f) return fail(MISA_ERR_ARG, "%s: cap = %g must be finite and not negative", fn, cap);
+  if (T > 0 && (!q || !q_seq || !q_len || !out)) return fail(MISA_ERR_ARG, "%s: null pointer", fn);
+  if (!stride_ok(q_ts) || !stride_ok(q_hs)) return fail(MISA_ERR_ALIGN, "%s: q strides must be positive multiples of 8", fn);
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(MISA_ERR_ALIGN, "%s: q and out must be 16-byte aligned", fn);
+  if (!aligned(q_seq, 4) || !aligned(q_len, 4) || !aligned(q_pos, 4) || !aligned(slopes, 4) || !aligned(lse, 4))
+    return fail(MISA_ERR_ALIGN, "%s: q_seq, q_len, q_pos, slopes and lse must be 4-byte aligned", fn);
+  a->q = static_cast<const uint16_t*>(q);
+  a->q_ts = q_ts;
+  a->q_hs = q_hs;
+  a->q_seq = q_seq;
+  a->q_len = q_len;
+  a->q_pos = q_pos;
+  a->T = T;
+  a->d = c->d;
+  a->Hq = Hq;
+  a->Hkv = c->heads;
+  a->scale = scale;
+  a->cap = cap;
+  a->slopes = slopes;
+  a->out = static_cast<uint16_t*>(out);
+  a->lse = lse;
+  return MISA_OK;
+}
+
+int32_t check_attend_grid(const char* fn, const misa::AttendArgs& a) {
+  const int64_t rows = a.T * (int64_t)a.Hq;
+  if (misa::attend_blocks(a) >= (int64_t(1) << 31) || rows / 4 >= (int64_t(1) << 31))
+    return fail(MISA_ERR_ARG, "%s: grid too large", fn);
+  return MISA_OK;
+}
+
+// Rows of a workgroup's tile in each pass of a call.
+int rows_of(int64_t T, int64_t nseq, int32_t Hq, int32_t heads, bool gather) {
+  return misa::attend_rows(T, nseq, Hq / heads, gather);
 }
 
 }  // namespace
@@ -895,6 +985,180 @@ int32_t misa_pivot_indexer(const void* q, const float* w, const void* k, const i
   // each query re-ranks its group's candidates with its own dense indexer
   return score_and_select(fn, q, w, k, nullptr, H, cd, kc, q_seq, q_len, T, H, d, nseq, Lmax, topk, idx, score,
                           reinterpret_cast<float*>(p), kc, st);
+}
+
+size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t heads, int32_t d, int64_t nseq,
+                                   int64_t npre) {
+  if (T <= 0 || heads < 1 || Hq < heads || Hq % heads || !(d == 64 || d == 128 || d == 256) || nseq < 1) return 0;
+  const size_t own = misa::attend_ws_bytes(T, d, rows_of(T, nseq, Hq, heads, op == MISA_OP_ATTEND_SELECTED));
+  switch (op) {
+    case MISA_OP_ATTEND:
+    case MISA_OP_ATTEND_SELECTED:
+      return own;
+    case MISA_OP_ATTEND_SHARED: {
+      if (npre < 1) return own;
+      // the prefix pass's results in fp32, and its own workspace or the second pass's
+      const size_t pre = misa::attend_ws_bytes(T, d, rows_of(T, npre, Hq, heads, false));
+      return round_up((size_t)T * Hq * d * 4) + round_up((size_t)T * Hq * 4) + (own > pre ? own : pre);
+    }
+  }
+  return 0;
+}
+
+int32_t misa_cache_append(const misa_kv_cache* cache, const void* k, int64_t k_ts, int64_t k_hs, const void* v,
+                          int64_t v_ts, int64_t v_hs, const void* q, int64_t q_ts, int64_t q_hs, void* q_out,
+                          int64_t o_ts, int64_t o_hs, int32_t Hq, const int32_t* q_seq, const int32_t* q_tok,
+                          const int32_t* q_pos, const float* cos_sin, int64_t P, int32_t rot, int32_t interleaved,
+                          int64_t N, void* stream) {
+  const char* fn = "misa_cache_append";
+  misa::AppendArgs a{};
+  int32_t rc = check_cache(fn, cache, &a.kv);
+  if (rc) return rc;
+  const int32_t d = cache->d;
+  if (d < 16 || d > 1024 || d % 16) return fail(MISA_ERR_ARG, "%s: d = %d not a multiple of 16 in [16, 1024]", fn, d);
+  if (N < 0 || N >= (int64_t(1) << 31)) return fail(MISA_ERR_ARG, "%s: N = %lld out of range", fn, (long long)N);
+  if (Hq < 0 || Hq > 65536) return fail(MISA_ERR_ARG, "%s: Hq = %d not in [0, 65536]", fn, Hq);
+  if (rot < 0 || rot > d || rot % 16) return fail(MISA_ERR_ARG, "%s: rot = %d not a multiple of 16 in [0, d = %d]", fn, rot, d);
+  if (rot > 0 && (P < 1 || P >= (int64_t(1) << 31))) return fail(MISA_ERR_ARG, "%s: P = %lld out of range", fn, (long long)P);
+  if (!v != !cache->v) return fail(MISA_ERR_ARG, "%s: v and the value cache go together", fn);
+  if (N > 0 && (!k || !q_seq || !q_tok || (Hq > 0 && (!q || !q_out)) || (rot > 0 && !cos_sin)))
+    return fail(MISA_ERR_ARG, "%s: null pointer", fn);
+  if (!stride_ok(k_ts) || !stride_ok(k_hs) || (v && (!stride_ok(v_ts) || !stride_ok(v_hs))) ||
+      (Hq > 0 && (!stride_ok(q_ts) || !stride_ok(q_hs) || !stride_ok(o_ts) || !stride_ok(o_hs))))
+    return fail(MISA_ERR_ALIGN, "%s: strides must be positive multiples of 8", fn);
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16))
+    return fail(MISA_ERR_ALIGN, "%s: k, v, q and q_out must be 16-byte aligned", fn);
+  if (!aligned(q_seq, 4) || !aligned(q_tok, 4) || !aligned(q_pos, 4) || !aligned(cos_sin, 4))
+    return fail(MISA_ERR_ALIGN, "%s: q_seq, q_tok, q_pos and cos_sin must be 4-byte aligned", fn);
+  if (Hq > 0 && q == q_out && (q_ts != o_ts || q_hs != o_hs))
+    return fail(MISA_ERR_ARG, "%s: q_out = q needs the strides of q", fn);
+  if (N == 0) return ok();
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_ts = k_ts;
+  a.k_hs = k_hs;
+  a.v_ts = v_ts;
+  a.v_hs = v_hs;
+  a.q_ts = q_ts;
+  a.q_hs = q_hs;
+  a.o_ts = o_ts;
+  a.o_hs = o_hs;
+  a.seq = q_seq;
+  a.tok = q_tok;
+  a.pos = q_pos;
+  a.cos_sin = cos_sin;
+  a.P = P;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = cache->heads;
+  a.d = d;
+  a.rot = rot;
+  a.interleaved = interleaved != 0;
+  a.half = cache->dtype == MISA_FP16;
+  return hip_status(misa::launch_append(a, (hipStream_t)stream), fn);
+}
+
+int32_t misa_attend(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs, const int32_t* q_seq,
+                    const int32_t* q_start, const int32_t* q_len, const int32_t* q_pos, int64_t T, int32_t Hq,
+                    float scale, float cap, const float* slopes, void* out, float* lse, void* ws, size_t ws_bytes,
+                    void* stream) {
+  const char* fn = "misa_attend";
+  misa::AttendArgs a{};
+  int32_t rc = check_attend(fn, cache, q, q_ts, q_hs, q_seq, q_len, q_pos, T, Hq, scale, cap, slopes, out, lse, &a);
+  if (rc) return rc;
+  if (!aligned(q_start, 4)) return fail(MISA_ERR_ALIGN, "%s: q_start must be 4-byte aligned", fn);
+  if (T == 0) return ok();
+  rc = check_ws(fn, ws, ws_bytes, misa_attend_workspace_bytes(MISA_OP_ATTEND, T, Hq, a.Hkv, a.d, a.kv.nseq, 0));
+  if (rc) return rc;
+  a.q_start = q_start;
+  a.mode = misa::kAttendPlain;
+  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, false);
+  misa::attend_setup(a, R, ws);
+  if ((rc = check_attend_grid(fn, a))) return rc;
+  return hip_status(misa::launch_attend(a, R, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
+}
+
+int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs, const int32_t* idx,
+                             int32_t topk, const int32_t* q_seq, const int32_t* q_len, const int32_t* q_pos, int64_t T,
+                             int32_t Hq, float scale, float cap, const float* slopes, void* out, float* lse, void* ws,
+                             size_t ws_bytes, void* stream) {
+  const char* fn = "misa_attend_selected";
+  misa::AttendArgs a{};
+  int32_t rc = check_attend(fn, cache, q, q_ts, q_hs, q_seq, q_len, q_pos, T, Hq, scale, cap, slopes, out, lse, &a);
+  if (rc) return rc;
+  if (topk < 1 || topk > kMaxTokens) return fail(MISA_ERR_ARG, "%s: topk = %d out of range", fn, topk);
+  if (T == 0) return ok();
+  if (!idx) return fail(MISA_ERR_ARG, "%s: null idx", fn);
+  if (!aligned(idx, 4)) return fail(MISA_ERR_ALIGN, "%s: idx must be 4-byte aligned", fn);
+  rc = check_ws(fn, ws, ws_bytes, misa_attend_workspace_bytes(MISA_OP_ATTEND_SELECTED, T, Hq, a.Hkv, a.d, a.kv.nseq, 0));
+  if (rc) return rc;
+  a.idx = idx;
+  a.topk = topk;
+  a.mode = misa::kAttendPlain;
+  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, true);
+  misa::attend_setup(a, R, ws);
+  if ((rc = check_attend_grid(fn, a))) return rc;
+  return hip_status(misa::launch_attend(a, R, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
+}
+
+int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs, const int32_t* q_seq,
+                           const int32_t* q_len, const int32_t* q_pos, const int32_t* pre, const int32_t* pre_len,
+                           const int32_t* pre_table, int64_t pre_cols, int64_t npre, int64_t T, int32_t Hq, float scale,
+                           float cap, const float* slopes, void* out, float* lse, void* ws, size_t ws_bytes,
+                           void* stream) {
+  const char* fn = "misa_attend_shared";
+  misa::AttendArgs a{};
+  int32_t rc = check_attend(fn, cache, q, q_ts, q_hs, q_seq, q_len, q_pos, T, Hq, scale, cap, slopes, out, lse, &a);
+  if (rc) return rc;
+  if (npre < 1 || npre >= (int64_t(1) << 31)) return fail(MISA_ERR_ARG, "%s: npre = %lld out of range", fn, (long long)npre);
+  if (pre_table) {
+    if (pre_cols < 1 || pre_cols > kMaxTokens / cache->page)
+      return fail(MISA_ERR_ARG, "%s: pre_cols = %lld out of range", fn, (long long)pre_cols);
+  } else if (npre > cache->npages) {
+    return fail(MISA_ERR_ARG, "%s: without a table of prefixes npre = %lld must be at most npages", fn, (long long)npre);
+  }
+  if (T == 0) return ok();
+  if (!pre || !pre_len) return fail(MISA_ERR_ARG, "%s: null pre or pre_len", fn);
+  if (!aligned(pre, 4) || !aligned(pre_len, 4) || !aligned(pre_table, 4))
+    return fail(MISA_ERR_ALIGN, "%s: pre, pre_len and pre_table must be 4-byte aligned", fn);
+  rc = check_ws(fn, ws, ws_bytes, misa_attend_workspace_bytes(MISA_OP_ATTEND_SHARED, T, Hq, a.Hkv, a.d, a.kv.nseq, npre));
+  if (rc) return rc;
+  char* p = static_cast<char*>(ws);
+  float* part = reinterpret_cast<float*>(p);
+  p += round_up((size_t)T * Hq * a.d * 4);
+  float* part_lse = reinterpret_cast<float*>(p);
+  p += round_up((size_t)T * Hq * 4);
+  a.pre = pre;
+  a.pre_len = pre_len;
+  a.npre = npre;
+  a.pre_max = pre_table ? pre_cols * cache->page : cache->page;
+
+  // the prefixes first, for all of their queries; their results join the own parts
+  misa::AttendArgs b = a;
+  b.mode = misa::kAttendPrefix;
+  b.own_seq = q_seq;
+  b.own_nseq = a.kv.nseq;
+  b.kv.table = pre_table;
+  b.kv.table_stride = pre_cols;
+  b.kv.nseq = npre;
+  b.kv.Lmax = a.pre_max;
+  b.out = nullptr;
+  b.out32 = part;
+  b.lse = part_lse;
+  const int Rb = rows_of(T, npre, Hq, a.Hkv, false);
+  misa::attend_setup(b, Rb, p);
+  a.mode = misa::kAttendOwn;
+  a.init_out = part;
+  a.init_lse = part_lse;
+  const int Ra = rows_of(T, a.kv.nseq, Hq, a.Hkv, false);
+  misa::attend_setup(a, Ra, p);
+  if ((rc = check_attend_grid(fn, a)) || (rc = check_attend_grid(fn, b))) return rc;
+  const bool half = cache->dtype == MISA_FP16;
+  const hipError_t e = misa::launch_attend(b, Rb, half, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_status(e, fn);
+  return hip_status(misa::launch_attend(a, Ra, half, (hipStream_t)stream), fn);
 }
 
 int32_t misa_debug_scores(const void* q, const float* w, const void* k, const int32_t* heads, int32_t h,

@@ -1,0 +1,895 @@
+// Attention over a paged cache.
+//
+// A row is one (query, head) pair; its score of the visible key s is
+//   x = scale q.k_s,  then cap tanh(x / cap),  then - slope |position - s|,
+// and its result sum_s e^(x_s - m) v_s / sum_s e^(x_s - m). The sums are kept
+// against the running maximum m and rescaled when it grows, so that the keys
+// are read once. Scores, m and both sums are fp32; the weights e^(x - m) are
+// rounded to the cache's 16-bit type (to nearest) for the second product, whose
+// sums are fp32 again, while the sum of the weights adds the unrounded ones.
+//
+// A workgroup takes a tile of R rows that read one kv head (the heads of a
+// group, of one or several queries of a sequence) and a run of their keys:
+// RW waves split the rows (MR = 16 or 32 a wave), KW groups of waves split the
+// keys, NK at a time. Both products are MFMAs with the keys or the values as
+// the first operand and the queries or weights as the second one:
+//   S^T [keys x rows] = K Q^T,   O^T [d x rows] += V^T P^T.
+// A lane then holds scores of ONE row (its column), so the maximum and the sum
+// are sums over its registers and one or two lane exchanges, the rescaling is a
+// product by a lane's own factor, and the weights already lie where the second
+// product wants them: the order of the keys within a product is free, so the
+// lane's own score registers are its share of P^T, and V^T is read to match by
+// transposing LDS reads (ds_read_b64_tr_b16: 16 lanes read a 4 x 16 block of
+// 16-bit values and each gets one column).
+//
+// Keys and values go through LDS in two buffers: while one is used, the next
+// tile's rows are on their way into registers and the page ids of the tile
+// after it are looked up. The 16-byte pieces of a row are permuted by the row's
+// low bits (swizzle) so that neither the row-wise nor the transposing reads
+// meet in a bank.
+//
+// Batches of up to kPlanMax queries are planned: every workgroup sums the key
+// tiles of all segments (runs of queries of one sequence that share a row
+// tile), and the flat list of (segment, head tile, key tile) is cut into G
+// equal runs, so that a ragged batch loads all CUs evenly. A segment that a cut
+// divides leaves unfinished parts, at most two a workgroup, which a second
+// launch joins in a fixed order. Larger batches take one workgroup per row tile.
+#pragma once
+
+#include <type_traits>
+
+#include "misa_attend.hpp"
+#include "misa_common.hpp"
+
+namespace misa {
+namespace attend {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef short shortx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <bool HALF>
+__device__ __forceinline__ floatx16 mfma32(const u32x4& a, const u32x4& b, const floatx16& c) {
+  if (HALF)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <bool HALF>
+__device__ __forceinline__ floatx4 mfma16(const u32x4& a, const u32x4& b, const floatx4& c) {
+  if (HALF)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a), __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Two fp32 values in 16 bits each, to nearest, ties to even.
+template <bool HALF>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (HALF)
+    return (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)lo) |
+           (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)hi) << 16;
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  bf16x2 r;
+  r[0] = (__bf16)lo;
+  r[1] = (__bf16)hi;
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// Tile shapes. NK keys per group of waves and step; KT = KW * NK keys a step.
+template <int D, int R>
+struct Shape {
+  static constexpr int MR = R == 16 ? 16 : 32;
+  static constexpr int RW = R <= 32 ? 1 : R / 32;
+  static constexpr int KW = D == 256 ? (R <= 32 ? 2 : 1) : (R <= 32 ? 4 : (R == 64 ? 2 : 1));
+  static constexpr int NK = D == 256 ? 32 : (D == 128 ? (R == 128 ? 64 : 32) : 64);
+  static constexpr int KT = KW * NK;
+  static constexpr int threads = 64 * RW * KW;
+  static constexpr int stage_bytes = KT * D * 2 * 2;
+  // the keys' waves join their sums through LDS: rows of D + 4 floats
+  static constexpr int merge_bytes = KW > 1 ? KW * R * (D + 4) * 4 + KW * R * 8 + R * 8 : 0;
+  static constexpr int lds_bytes = 2 * stage_bytes > merge_bytes ? 2 * stage_bytes : merge_bytes;
+  // workgroups that fit a CU (160 KiB of LDS, the plan's share included)
+  static constexpr int per_cu = (lds_bytes + kPlanMax * 8 + 64) * 2 <= 160 * 1024 ? 2 : 1;
+};
+
+// 16-byte piece c of row r lies at piece c ^ swizzle(r) of its row in LDS. The
+// row-wise reads (16 or 32 rows, one piece each) and the transposing ones (four
+// consecutive rows, four pieces each) then spread over all 64 banks.
+template <int D>
+__device__ __forceinline__ int swizzle(int r) {
+  if (D == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+  return ((r & 3) << 2) | ((r >> 2) & 3);
+}
+
+// Zeros that stand in for a row without a key.
+static __device__ __align__(16) const uint32_t kZeroRow[128] = {};
+
+struct QueryInfo {
+  int seq;        // row of the table, -1: none
+  int lo, hi;     // visible tokens of that row
+  int kbase;      // position of its token 0
+  int pos;        // position of the query
+};
+
+__device__ __forceinline__ int clamp_len(int64_t v, int64_t most) { return (int)(v < 0 ? 0 : (v > most ? most : v)); }
+
+__device__ __forceinline__ QueryInfo query_info(const AttendArgs& a, int64_t t) {
+  QueryInfo r;
+  r.lo = 0;
+  r.kbase = 0;
+  const int own = a.mode == kAttendPrefix ? a.own_seq[t] : a.q_seq[t];
+  const int64_t nown = a.mode == kAttendPrefix ? a.own_nseq : a.kv.nseq;
+  const bool ok = own >= 0 && own < nown;
+  int plen = 0, pre = -1;
+  if (a.mode != kAttendPlain) {
+    pre = a.pre[t];
+    if (pre >= 0 && pre < a.npre) plen = clamp_len(a.pre_len[pre], a.pre_max);
+    else pre = -1;
+  }
+  const int len = a.q_len[t];
+  if (a.mode == kAttendPrefix) {
+    r.seq = ok ? pre : -1;
+    r.hi = r.seq >= 0 ? plen : 0;
+  } else {
+    r.seq = ok ? own : -1;
+    r.hi = ok ? clamp_len(len, a.kv.Lmax) : 0;
+    if (a.q_start) {
+      const int s = a.q_start[t];
+      r.lo = s < 0 ? 0 : (s > r.hi ? r.hi : s);
+    }
+    r.kbase = plen;
+  }
+  r.pos = a.q_pos ? a.q_pos[t] : plen + len - 1;
+  return r;
+}
+
+// Key tiles of KT keys that a segment of queries visits (at least one, so that
+// a segment without keys still writes its rows).
+__device__ __forceinline__ int tiles_of(int lo, int hi, int KT) { return hi > lo ? (hi - lo + KT - 1) / KT : 1; }
+
+// Work of a part of a segment.
+struct Part {
+  int64_t t0;      // first query
+  int nq;          // queries
+  int hh;          // kv head * head_tiles + head tile
+  int tile0, tile1;   // key tiles of it
+  int tiles;       // key tiles of the segment
+  int slot;        // unfinished parts: where they are kept
+};
+
+__device__ __forceinline__ int wave_min_of(int v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = min(v, __shfl_xor(v, off, 64));
+  return v;
+}
+__device__ __forceinline__ int wave_max_of(int v) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) v = max(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
+// Sequence and span of the visible keys of queries t0 .. t0 + nq - 1 (one sequence).
+struct Span {
+  int seq, lo, hi;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t t0, int nq) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0x7fffffff, hi = 0, seq = -1;
+  for (int i = lane; i < nq; i += 64) {
+    const QueryInfo r = query_info(a, t0 + i);
+    seq = max(seq, r.seq);
+    if (a.idx) {
+      lo = 0;
+      hi = r.hi > r.lo ? a.topk : 0;
+    } else if (r.hi > r.lo) {
+      lo = min(lo, r.lo);
+      hi = max(hi, r.hi);
+    }
+  }
+  Span s;
+  s.seq = wave_max_of(seq);
+  s.lo = wave_min_of(lo);
+  s.hi = wave_max_of(hi);
+  if (s.hi <= s.lo) s.lo = s.hi = 0;
+  return s;
+}
+
+// One score in units of log2: the scale, the cap and the bias applied.
+// tanh(y) = 1 - 2 / (1 + e^2y); below 1/8 by its series, whose first left-out
+// term is y^8 62 / 2835 < 1.4e-9 of the value.
+__device__ __forceinline__ float shaped(float acc, float scale, float cap, float inv_cap, float slope, float dist) {
+  float x = acc * scale;
+  if (cap > 0.f) {
+    const float y = x * inv_cap, y2 = y * y;
+    const float big = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * (2.f * kLog2e)));
+    const float small = y * (1.f + y2 * (-1.f / 3.f + y2 * (2.f / 15.f - y2 * (17.f / 315.f))));
+    x = cap * (fabsf(y) < 0.125f ? small : big);
+  }
+  return (x - slope * dist) * kLog2e;
+}
+
+// A finished row: sums relative to 2^m (m in units of log2) to the result and its log-sum.
+template <bool HALF, int D>
+__device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, int d0, float m, float sum, floatx4 o) {
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;   // a row without a key: zeros
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] *= inv;
+  if (a.out) {
+    u32x2 w;
+    w[0] = pack2<HALF>(o[0], o[1]);
+    w[1] = pack2<HALF>(o[2], o[3]);
+    *reinterpret_cast<u32x2*>(a.out + row * D + d0) = w;
+  } else {
+    *reinterpret_cast<floatx4*>(a.out32 + row * D + d0) = o;
+  }
+  if (d0 == 0 && a.lse) a.lse[row] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * kLn2;
+}
+
+template <bool HALF, int D, int R, bool EXTRA>
+struct Kernel {
+  using S = Shape<D, R>;
+  static constexpr int MR = S::MR, RW = S::RW, KW = S::KW, NK = S::NK, KT = S::KT, TH = S::threads;
+  static constexpr int RPI = 512 / D;              // rows a wave's load instruction covers
+  static constexpr int LPR = D / 8;                // lanes (16-byte pieces) per row
+  static constexpr int NLD = NK / RW / RPI;        // load instructions per tensor, wave and step
+  static constexpr int QF = D * MR / 512;          // query fragments: d / 16 or d / 32 products deep
+  static constexpr int OT = D / MR;                // output tiles of MR dims
+  static constexpr int ST = NK / MR;               // score tiles of MR keys
+  static constexpr int AR = MR * MR / 64;          // accumulator registers of a tile: 16 or 4
+  static_assert(NLD >= 1 && NK % MR == 0, "tile shape");
+  using Acc = typename std::conditional<MR == 32, floatx16, floatx4>::type;
+
+  __device__ static __forceinline__ Acc mma(const u32x4& x, const u32x4& y, const Acc& c) {
+    if constexpr (MR == 32) return mfma32<HALF>(x, y, c);
+    else return mfma16<HALF>(x, y, c);
+  }
+  // key (or output dim) within a tile that accumulator register j of this lane holds
+  __device__ static __forceinline__ int acc_row(int j, int lane) {
+    if constexpr (MR == 32) return 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+    else return 4 * (lane >> 4) + j;
+  }
+
+  struct Rows {     // a lane's row
+    int lo, hi;     // visible keys
+    float slope;
+    int pos;        // position - kbase
+    bool active;
+    int64_t t;
+    int head;
+  };
+
+  // The keys of one step for one group of waves: lane l looks up key l.
+  struct Look {
+    int page;       // -1: no key
+    int token;
+  };
+
+  __device__ static __forceinline__ Look look_up(const AttendArgs& a, const Span& sp, const int32_t* ids, int s, int end,
+                                                 int lo, int hi) {
+    const int lane = threadIdx.x & 63;
+    Look r;
+    r.page = -1;
+    r.token = 0;
+    s += lane;
+    if (lane < NK && s < end) {
+      int tok = s;
+      if (ids) tok = ids[s];
+      if (tok >= lo && tok < hi) {
+        const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)tok);
+        r.page = kv_page(a.kv, sp.seq, col);
+        r.token = tok;
+      }
+    }
+    return r;
+  }
+  // element offset of the row looked up; -1: none
+  __device__ static __forceinline__ int64_t row_offset(const AttendArgs& a, const Look& l, int64_t head_off) {
+    if (l.page < 0) return -1;
+    const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)l.token);
+    return (int64_t)l.page * a.kv.page_stride + (int64_t)(l.token - (int)col * a.kv.page) * a.kv.tok_stride + head_off;
+  }
+
+  __device__ static __forceinline__ void load_rows(const AttendArgs& a, int64_t off, int rw, u32x4 (&kr)[NLD],
+                                                   u32x4 (&vr)[NLD]) {
+    const int lane = threadIdx.x & 63;
+    const int lo = (int)(uint32_t)off, hi = (int)(off >> 32);
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int row = (rw * NLD + i) * RPI + lane / LPR;
+      const int64_t o = (int64_t)(uint32_t)__shfl(lo, row, 64) | (int64_t)__shfl(hi, row, 64) << 32;
+      const int c = 8 * ((lane % LPR) ^ swizzle<D>(row));
+      const uint16_t* z = reinterpret_cast<const uint16_t*>(kZeroRow);
+      kr[i] = *reinterpret_cast<const u32x4*>((o >= 0 ? a.kv.k + o : z) + c);
+      vr[i] = *reinterpret_cast<const u32x4*>((o >= 0 ? a.kv.v + o : z) + c);
+    }
+  }
+  __device__ static __forceinline__ void store_rows(uint16_t* ks, uint16_t* vs, int rw, const u32x4 (&kr)[NLD],
+                                                    const u32x4 (&vr)[NLD]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int at = (rw * NLD + i) * RPI * D + lane * 8;
+      *reinterpret_cast<u32x4*>(ks + at) = kr[i];
+      *reinterpret_cast<u32x4*>(vs + at) = vr[i];
+    }
+  }
+
+  // scores of one step: S^T tiles of this wave's rows
+  __device__ static __forceinline__ void score(const uint16_t* ks, const u32x4 (&qf)[QF], Acc (&s)[ST]) {
+    const int lane = threadIdx.x & 63;
+    const int r = lane % MR, g = lane / MR;
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+#pragma unroll
+      for (int j = 0; j < AR; ++j) s[i][j] = 0.f;
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        const int row = i * MR + r;
+        const int c = (f * (64 / MR) + g) ^ swizzle<D>(row);
+        s[i] = mma(*reinterpret_cast<const u32x4*>(ks + row * D + 8 * c), qf[f], s[i]);
+      }
+    }
+  }
+
+  // 4 values V[key0 + 0..3][dim] of this lane's output dim: 16 lanes read 4 rows of 16 dims
+  __device__ static __forceinline__ u32x2 read_tr(const uint16_t* vs, int key0, int dim0) {
+    const int lane = threadIdx.x & 63;
+    const int row = key0 + ((lane & 15) >> 2);
+    const int piece = (dim0 >> 3) + ((lane & 3) >> 1);
+    const uint16_t* p = vs + row * D + 8 * (piece ^ swizzle<D>(row)) + 4 * (lane & 1);
+    typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(uintptr_t)(
+                                         __attribute__((address_space(3))) const uint16_t*)p));
+  }
+
+  // Bits of the halves of x that hold an infinity or a NaN: ~0 or 0 each.
+  __device__ static __forceinline__ uint32_t not_finite(uint32_t x) {
+    constexpr uint32_t e = HALF ? 0x7c00u : 0x7f80u;
+    return ((x & e) == e ? 0xffffu : 0u) | ((x & (e << 16)) == (e << 16) ? 0xffff0000u : 0u);
+  }
+  __device__ static __forceinline__ bool any_not_finite(const uint16_t* vs) {
+    const int lane = threadIdx.x & 63;
+    uint32_t bad = 0;
+#pragma unroll 4
+    for (int e = lane * 8; e < NK * D; e += 512) {
+      const u32x4 x = *reinterpret_cast<const u32x4*>(vs + e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bad |= not_finite(x[i]);
+    }
+    return __any(bad != 0);
+  }
+
+  // The operand V^T of product p, output tile i.
+  __device__ static __forceinline__ u32x4 value_frag(const uint16_t* vs, int p, int i) {
+    const int lane = threadIdx.x & 63;
+    const int k0 = MR == 32 ? p * 16 + 4 * (lane >> 5) : p * 32 + 4 * (lane >> 4);
+    const int dim0 = i * MR + (MR == 32 ? (lane & 16) : 0);
+    const u32x2 x = read_tr(vs, k0, dim0), y = read_tr(vs, k0 + (MR == 32 ? 8 : 16), dim0);
+    return u32x4{x[0], x[1], y[0], y[1]};
+  }
+  // The operand P^T of product p from this lane's score registers: MR == 32: 16
+  // keys (registers 8 (p & 1) .. + 7 of tile p / 2); MR == 16: 32 keys (two tiles).
+  __device__ static __forceinline__ u32x4 weight_frag(const Acc (&s)[ST], int p) {
+    u32x4 w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (MR == 32) w[i] = pack2<HALF>(s[p / 2][8 * (p & 1) + 2 * i], s[p / 2][8 * (p & 1) + 2 * i + 1]);
+      else w[i] = pack2<HALF>(s[2 * p + i / 2][2 * (i & 1)], s[2 * p + i / 2][2 * (i & 1) + 1]);
+    }
+    return w;
+  }
+  static constexpr int NP = MR == 32 ? NK / 16 : NK / 32;
+
+  // O^T += V^T P^T over one step
+  __device__ static __forceinline__ void accumulate(const uint16_t* vs, const Acc (&s)[ST], Acc (&o)[OT]) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const u32x4 w = weight_frag(s, p);
+#pragma unroll
+      for (int i = 0; i < OT; ++i) o[i] = mma(value_frag(vs, p, i), w, o[i]);
+    }
+  }
+
+  // The same for a step of which some rows do not see every key, and whose values
+  // are not all finite: the product would carry 0 * inf = NaN into rows that do
+  // not see them. The finite values are multiplied as above; then, for +inf, -inf
+  // and NaN in turn, a product of marks counts those that each row sees.
+  __device__ static __noinline__ void accumulate_guarded(const uint16_t* vs, Acc (&s)[ST], Acc (&o)[OT], int base, int lo,
+                                                         int hi, uint64_t valid) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const u32x4 w = weight_frag(s, p);
+#pragma unroll
+      for (int i = 0; i < OT; ++i) {
+        u32x4 v = value_frag(vs, p, i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] &= ~not_finite(v[e]);
+        o[i] = mma(v, w, o[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < ST; ++i)
+#pragma unroll
+      for (int j = 0; j < AR; ++j) {
+        const int key = i * MR + acc_row(j, lane);
+        s[i][j] = base + key >= lo && base + key < hi && ((valid >> key) & 1) ? 1.f : 0.f;
+      }
+    constexpr uint32_t one = HALF ? 0x3c00u : 0x3f80u, inf = HALF ? 0x7c00u : 0x7f80u;
+#pragma unroll 1
+    for (int kind = 0; kind < 3; ++kind) {
+      const float value = kind == 0 ? __builtin_inff() : kind == 1 ? -__builtin_inff() : __builtin_nanf("");
+#pragma unroll
+      for (int i = 0; i < OT; ++i) {
+        Acc n;
+#pragma unroll
+        for (int j = 0; j < AR; ++j) n[j] = 0.f;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          u32x4 v = value_frag(vs, p, i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t mark = 0;
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              const uint32_t x = (v[e] >> h) & 0xffffu;
+              const bool is = kind == 0 ? x == inf : kind == 1 ? x == (inf | 0x8000u) : (x & 0x7fffu) > inf;
+              mark |= is ? one << h : 0u;
+            }
+            v[e] = mark;
+          }
+          n = mma(v, weight_frag(s, p), n);
+        }
+#pragma unroll
+        for (int j = 0; j < AR; ++j) o[i][j] = n[j] > 0.f ? o[i][j] + value : o[i][j];
+      }
+    }
+  }
+
+  __device__ static __forceinline__ float over_rows_max(float v) {
+    if constexpr (MR == 16) v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+  }
+  __device__ static __forceinline__ float over_rows_sum(float v) {
+    if constexpr (MR == 16) v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+  }
+
+  // Result or unfinished sums of row r (of the tile), dims d0 .. d0 + 3.
+  // m in units of log2; sum and o relative to 2^m.
+  __device__ static __forceinline__ void emit(const AttendArgs& a, const Part& p, bool whole, int64_t t, int head, int r,
+                                              int d0, float m, float sum, floatx4 o) {
+    if (!whole) {
+      *reinterpret_cast<floatx4*>(a.part_out + ((int64_t)p.slot * R + r) * D + d0) = o;
+      if (d0 == 0) {
+        a.part_ml[((int64_t)p.slot * R + r) * 2] = m;
+        a.part_ml[((int64_t)p.slot * R + r) * 2 + 1] = sum;
+      }
+      return;
+    }
+    const int64_t row = t * a.Hq + head;
+    write_row<HALF, D>(a, row, d0, m, sum, o);
+  }
+
+  __device__ static __forceinline__ void run_part(const AttendArgs& a, const Part& p, unsigned char* lds) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rw = wave % RW, kw = wave / RW;
+    const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
+    const Span sp = span_of(a, p.t0, p.nq);
+    const bool whole = p.tile0 == 0 && p.tile1 == p.tiles;
+    // p.tile1 * KT may pass the last key (and 2^31): 64 bits
+    const int begin = sp.lo + p.tile0 * KT;
+    const int end = (int)min((int64_t)sp.hi, sp.lo + (int64_t)p.tile1 * KT);
+    const int steps = end > begin ? (end - begin + KT - 1) / KT : 0;
+
+    // this lane's row
+    const int r = rw * MR + lane % MR;
+    const int qi = (int)fast_quot(a.by_gw, (uint32_t)r);
+    Rows row;
+    row.head = kvh * a.group + hb * a.gw + (r - qi * a.gw);
+    row.active = qi < p.nq && row.head < (kvh + 1) * a.group;
+    row.t = p.t0 + qi;
+    row.lo = row.hi = 0;
+    row.slope = 0.f;
+    row.pos = 0;
+    if (row.active) {
+      const QueryInfo q = query_info(a, row.t);
+      row.pos = q.pos - q.kbase;
+      if (a.idx) {
+        row.lo = 0;
+        row.hi = a.topk;
+      } else {
+        row.lo = q.lo;
+        row.hi = q.hi;
+      }
+      if (EXTRA && a.slopes) row.slope = a.slopes[row.head];
+    }
+    // visible token ids of selected tokens (one query a segment; also for waves
+    // without a row, which load for the others)
+    const int32_t* ids = nullptr;
+    int id_lo = 0, id_hi = 0x7fffffff;
+    if (a.idx) {
+      const QueryInfo q = query_info(a, p.t0);
+      ids = a.idx + p.t0 * a.topk;
+      id_lo = q.lo;
+      id_hi = q.hi;
+    }
+    // keys that every row of this wave sees, and keys that any of them sees
+    const int all_lo = wave_max_of(row.active ? row.lo : 0);
+    const int all_hi = wave_min_of(row.active ? row.hi : 0x7fffffff);
+    const int any_lo = wave_min_of(row.active ? row.lo : 0x7fffffff);
+    const int any_hi = wave_max_of(row.active ? row.hi : 0);
+
+    u32x4 qf[QF];
+    {
+      const uint16_t* src = a.q + row.t * a.q_ts + row.head * a.q_hs + 8 * (lane / MR);
+#pragma unroll
+      for (int f = 0; f < QF; ++f) {
+        if (row.active) qf[f] = *reinterpret_cast<const u32x4*>(src + f * (512 / MR));
+        else qf[f] = u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+
+    float m = -__builtin_inff(), sum = 0.f;
+    Acc o[OT];
+#pragma unroll
+    for (int i = 0; i < OT; ++i)
+#pragma unroll
+      for (int j = 0; j < AR; ++j) o[i][j] = 0.f;
+    if (a.init_out && kw == 0 && p.tile0 == 0 && row.active) {
+      const int64_t at = row.t * a.Hq + row.head;
+      const float l = a.init_lse[at];
+      if (l > -__builtin_inff() || l != l) {
+        m = l * kLog2e;
+        sum = lane < MR ? 1.f : 0.f;
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; j += 4) {
+            const floatx4 x = *reinterpret_cast<const floatx4*>(a.init_out + at * D + i * MR + acc_row(j, lane));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][j + e] = x[e];
+          }
+      }
+    }
+    const float sc = EXTRA ? 1.f : a.scale * kLog2e;
+    if (!EXTRA) m = m / sc;   // in units of the raw scores while the keys are read
+    const float inv_cap = EXTRA && a.cap > 0.f ? 1.f / a.cap : 0.f;
+
+    uint16_t* buf = reinterpret_cast<uint16_t*>(lds);
+    constexpr int GB = NK * D;             // elements of one tensor of one group's step
+    constexpr int SB = KW * 2 * GB;        // of one buffer
+    const int64_t head_off = (int64_t)kvh * a.kv.head_stride;
+    const int k0 = begin + kw * NK;
+    Look cur{-1, 0}, nxt{-1, 0};
+    u32x4 kr[NLD], vr[NLD];
+    if (steps > 0) {
+      cur = look_up(a, sp, ids, k0, end, id_lo, id_hi);
+      load_rows(a, row_offset(a, cur, head_off), rw, kr, vr);
+      if (steps > 1) nxt = look_up(a, sp, ids, k0 + KT, end, id_lo, id_hi);
+      store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
+    }
+    __syncthreads();
+    for (int it = 0; it < steps; ++it) {
+      const bool more = it + 1 < steps;
+      Look after{-1, 0};
+      if (more) {
+        load_rows(a, row_offset(a, nxt, head_off), rw, kr, vr);
+        if (it + 2 < steps) after = look_up(a, sp, ids, k0 + (it + 2) * KT, end, id_lo, id_hi);
+      }
+      const uint16_t* ks = buf + (it & 1) * SB + kw * 2 * GB;
+      const int base = k0 + it * KT;
+      const uint64_t valid = __ballot(cur.page >= 0);
+      if (base < any_hi && base + NK > any_lo && valid != 0) {
+        Acc s[ST];
+        score(ks, qf, s);
+        if constexpr (EXTRA) {
+#pragma unroll
+          for (int i = 0; i < ST; ++i)
+#pragma unroll
+            for (int j = 0; j < AR; ++j) {
+              const int key = i * MR + acc_row(j, lane);
+              float dist = 0.f;
+              if (a.slopes) {
+                const int tok = ids ? __shfl(cur.token, key, 64) : base + key;
+                dist = fabsf((float)(row.pos - tok));
+              }
+              s[i][j] = shaped(s[i][j], a.scale, a.cap, inv_cap, row.slope, dist);
+            }
+        }
+        constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK & 63)) - 1;
+        if (!(valid == kAll && base >= all_lo && base + NK <= all_hi)) {
+#pragma unroll
+          for (int i = 0; i < ST; ++i)
+#pragma unroll
+            for (int j = 0; j < AR; ++j) {
+              const int key = i * MR + acc_row(j, lane);
+              const bool see = base + key >= row.lo && base + key < row.hi && ((valid >> key) & 1);
+              s[i][j] = see ? s[i][j] : -__builtin_inff();
+            }
+        }
+        float mx = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j) mx = fmaxf(mx, s[i][j]);
+        mx = over_rows_max(mx);
+        const float mn = fmaxf(m, mx);
+        const float ref = mn == -__builtin_inff() ? 0.f : mn;
+        if (__any(mn > m)) {
+          const float alpha = __builtin_amdgcn_exp2f((m - ref) * sc);
+          sum *= alpha;
+#pragma unroll
+          for (int i = 0; i < OT; ++i)
+#pragma unroll
+            for (int j = 0; j < AR; ++j) o[i][j] *= alpha;
+          m = mn;
+        }
+        const float off = ref * sc;
+        float add = 0.f;
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j) {
+            s[i][j] = __builtin_amdgcn_exp2f(s[i][j] * sc - off);
+            add += s[i][j];
+          }
+        sum += add;
+        // keys of this step that some query of the part sees and some row of this wave does not
+        if ((base < all_lo || min(base + NK, end) > all_hi) && any_not_finite(ks + GB)) {
+          Acc sv[ST], oc[OT];   // copies: the registers of the usual path have no address
+#pragma unroll
+          for (int i = 0; i < ST; ++i) sv[i] = s[i];
+#pragma unroll
+          for (int i = 0; i < OT; ++i) oc[i] = o[i];
+          accumulate_guarded(ks + GB, sv, oc, base, row.lo, row.hi, valid);
+#pragma unroll
+          for (int i = 0; i < OT; ++i) o[i] = oc[i];
+        } else {
+          accumulate(ks + GB, s, o);
+        }
+      }
+      cur = nxt;
+      nxt = after;
+      if (more) {
+        uint16_t* to = buf + ((it + 1) & 1) * SB + kw * 2 * GB;
+        store_rows(to, to + GB, rw, kr, vr);
+      }
+      __syncthreads();
+    }
+
+    m *= sc;
+    sum = over_rows_sum(sum);
+    if constexpr (KW == 1) {
+      if (row.active) {
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; j += 4)
+            emit(a, p, whole, row.t, row.head, r, i * MR + acc_row(j, lane), m, sum,
+                 floatx4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
+      }
+    } else {
+      // join the groups of waves: maxima and sums first, then the scaled outputs
+      float* ob = reinterpret_cast<float*>(lds);             // [KW][R][D + 4]
+      float* ml = ob + KW * R * (D + 4);                     // [KW][R][2]
+      float* fin = ml + KW * R * 2;                          // [R][2]
+      if (lane < MR) {
+        ml[(kw * R + r) * 2] = m;
+        ml[(kw * R + r) * 2 + 1] = sum;
+      }
+      __syncthreads();
+      float M = -__builtin_inff(), total = 0.f;
+#pragma unroll
+      for (int i = 0; i < KW; ++i) M = fmaxf(M, ml[(i * R + r) * 2]);
+      const float ref = M == -__builtin_inff() ? 0.f : M;
+#pragma unroll
+      for (int i = 0; i < KW; ++i)
+        total += ml[(i * R + r) * 2 + 1] * __builtin_amdgcn_exp2f(ml[(i * R + r) * 2] - ref);
+      const float w = __builtin_amdgcn_exp2f(m - ref);
+      if (kw == 0 && lane < MR) {
+        fin[r * 2] = M;
+        fin[r * 2 + 1] = total;
+      }
+#pragma unroll
+      for (int i = 0; i < OT; ++i)
+#pragma unroll
+        for (int j = 0; j < AR; j += 4)
+          *reinterpret_cast<floatx4*>(ob + (kw * R + r) * (D + 4) + i * MR + acc_row(j, lane)) =
+              floatx4{o[i][j] * w, o[i][j + 1] * w, o[i][j + 2] * w, o[i][j + 3] * w};
+      __syncthreads();
+      for (int e = threadIdx.x; e < R * (D / 4); e += TH) {
+        const int rr = e / (D / 4), d0 = (e % (D / 4)) * 4;
+        const int q = (int)fast_quot(a.by_gw, (uint32_t)rr);
+        const int head = kvh * a.group + hb * a.gw + (rr - q * a.gw);
+        if (q >= p.nq || head >= (kvh + 1) * a.group) continue;
+        floatx4 x = *reinterpret_cast<const floatx4*>(ob + rr * (D + 4) + d0);
+#pragma unroll
+        for (int i = 1; i < KW; ++i) x += *reinterpret_cast<const floatx4*>(ob + (i * R + rr) * (D + 4) + d0);
+        emit(a, p, whole, p.t0 + q, head, rr, d0, fin[rr * 2], fin[rr * 2 + 1], x);
+      }
+      __syncthreads();   // the next part's first rows go to the same memory
+    }
+  }
+
+  // Queries from t0 on that belong to t0's sequence and row tile.
+  __device__ static __forceinline__ int run_length(const AttendArgs& a, int64_t t0) {
+    const int lane = threadIdx.x & 63;
+    int64_t end = (t0 / a.qt + 1) * a.qt;
+    if (end > a.T) end = a.T;
+    const int n = (int)(end - t0);
+    if (n <= 1) return n;
+    const int seq = query_info(a, t0).seq;
+    for (int i = 0; i < n; i += 64) {
+      const bool other = i + lane < n && query_info(a, t0 + i + lane).seq != seq;
+      const uint64_t b = __ballot(other);
+      if (b) return __builtin_amdgcn_readfirstlane(i + (int)__builtin_ctzll(b));
+    }
+    return n;
+  }
+
+  // Key tiles before each query's segment: cum[t] for t < T, and their sum.
+  __device__ static __forceinline__ int64_t make_plan(const AttendArgs& a, int64_t* cum) {
+    const int T = (int)a.T, tid = threadIdx.x;
+    constexpr int PER = kPlanMax / TH;       // queries a thread sums
+    int64_t w[PER];
+    int64_t mine = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int t = tid * PER + i;
+      w[i] = 0;
+      if (t < T) {
+        const QueryInfo q = query_info(a, t);
+        const bool starts = t % a.qt == 0 || query_info(a, t - 1).seq != q.seq;
+        if (starts) {
+          int lo = 0x7fffffff, hi = 0;
+          const int last = min(T, (t / a.qt + 1) * a.qt);
+          for (int u = t; u < last; ++u) {
+            const QueryInfo z = query_info(a, u);
+            if (z.seq != q.seq) break;
+            if (a.idx) {
+              lo = 0;
+              hi = z.hi > z.lo ? a.topk : 0;
+            } else if (z.hi > z.lo) {
+              lo = min(lo, z.lo);
+              hi = max(hi, z.hi);
+            }
+          }
+          w[i] = tiles_of(lo, hi, KT);
+        }
+      }
+      mine += w[i];
+    }
+    // prefix sum over the threads
+    __shared__ int64_t wsum[TH / 64];
+    const int lane = tid & 63;
+    int64_t inc = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int64_t v = __shfl_up(inc, off, 64);
+      if (lane >= off) inc += v;
+    }
+    if (lane == 63) wsum[tid >> 6] = inc;
+    __syncthreads();
+    int64_t before = inc - mine, total = 0;
+#pragma unroll
+    for (int i = 0; i < TH / 64; ++i) {
+      if (i < (tid >> 6)) before += wsum[i];
+      total += wsum[i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int t = tid * PER + i;
+      if (t < T) cum[t] = before;
+      before += w[i];
+    }
+    __syncthreads();
+    return total;
+  }
+
+  __device__ static __forceinline__ void body(const AttendArgs& a, unsigned char* lds, int64_t* cum) {
+    // units of work [u, u1): queries of this workgroup's row tile, or key tiles of the plan
+    int64_t total = 0, u, u1;
+    int hh = 0;
+    if (a.planned) {
+      total = make_plan(a, cum);
+      const int64_t units = total * a.NH;
+      u = blockIdx.x * units / a.G;
+      u1 = ((int64_t)blockIdx.x + 1) * units / a.G;
+      if (blockIdx.x == 0) publish_plan(a, cum, total);
+    } else {
+      // one workgroup per row tile, the last queries (the longest of a causal prompt) first
+      const int64_t ntiles = (a.T + a.qt - 1) / a.qt;
+      const int64_t tile = ntiles - 1 - (int64_t)(blockIdx.x / (unsigned)a.NH);
+      hh = blockIdx.x % (unsigned)a.NH;
+      u = tile * a.qt;
+      u1 = min(a.T, u + a.qt);
+    }
+    while (u < u1) {
+      Part p;
+      if (a.planned) {
+        // the last query whose segment starts at or before unit u
+        int lo = 0, hi = (int)a.T - 1;
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (cum[mid] * a.NH <= u) lo = mid;
+          else hi = mid - 1;
+        }
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        p.t0 = lo;
+        p.nq = run_length(a, lo);
+        const int next = lo + p.nq;
+        p.tiles = (int)((next < (int)a.T ? cum[next] : total) - cum[lo]);
+        const int64_t in = u - cum[lo] * a.NH;
+        p.hh = (int)(in / p.tiles);
+        p.tile0 = (int)(in - (int64_t)p.hh * p.tiles);
+        const int64_t left = u1 - u;
+        p.tile1 = left < p.tiles - p.tile0 ? p.tile0 + (int)left : p.tiles;
+        p.slot = (int)(2 * blockIdx.x + (p.tile0 > 0 ? 0 : 1));
+        u += p.tile1 - p.tile0;
+      } else {
+        p.t0 = u;
+        p.nq = run_length(a, u);
+        p.hh = hh;
+        p.tile0 = 0;
+        p.tiles = p.tile1 = 0x7fffffff;
+        p.slot = 0;
+        u += p.nq;
+      }
+      run_part(a, p, lds);
+    }
+  }
+
+  // What the join needs: every query takes the entry of its segment.
+  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int64_t* cum, int64_t total) {
+    for (int t = threadIdx.x; t < (int)a.T; t += TH) {
+      int t0 = t, next = t + 1;
+      const int seq = query_info(a, t).seq;
+      while (t0 % a.qt != 0 && query_info(a, t0 - 1).seq == seq) --t0;
+      while (next < (int)a.T && next % a.qt != 0 && query_info(a, next).seq == seq) ++next;
+      PlanEntry e;
+      e.first = cum[t0];
+      e.tiles = (int32_t)((next < (int)a.T ? cum[next] : total) - cum[t0]);
+      e.t0 = t0;
+      a.plan[t] = e;
+    }
+    if (threadIdx.x == 0) *a.plan_total = total;
+  }
+};
+
+template <bool HALF, int D, int R, bool EXTRA>
+__global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shape<D, R>::threads / 256 > 0
+                                                          ? Shape<D, R>::per_cu * Shape<D, R>::threads / 256
+                                                          : 1)) void attend_kernel(AttendArgs a) {
+  __shared__ __align__(16) unsigned char lds[Shape<D, R>::lds_bytes];
+  __shared__ int64_t cum[kPlanMax];
+  Kernel<HALF, D, R, EXTRA>::body(a, lds, cum);
+}
+
+template <bool HALF, int D, int R>
+hipError_t launch_shape(const AttendArgs& a, unsigned blocks, hipStream_t st) {
+  const dim3 grid(blocks), block(Shape<D, R>::threads);
+  if (a.cap > 0.f || a.slopes)
+    hipLaunchKernelGGL((attend_kernel<HALF, D, R, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<HALF, D, R, false>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_dim(const AttendArgs& a, int R, bool half, unsigned blocks, hipStream_t st) {
+  switch (R) {
+    case 16: return half ? launch_shape<true, D, 16>(a, blocks, st) : launch_shape<false, D, 16>(a, blocks, st);
+    case 32: return half ? launch_shape<true, D, 32>(a, blocks, st) : launch_shape<false, D, 32>(a, blocks, st);
+    case 64: return half ? launch_shape<true, D, 64>(a, blocks, st) : launch_shape<false, D, 64>(a, blocks, st);
+    case 128: return half ? launch_shape<true, D, 128>(a, blocks, st) : launch_shape<false, D, 128>(a, blocks, st);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace attend
+}  // namespace misa
