@@ -332,14 +332,14 @@ int32_t check_attend(const char* fn, const misa_kv_cache* c, const void* q, int6
 
 int32_t check_attend_grid(const char* fn, const misa::AttendArgs& a) {
   const int64_t rows = a.T * (int64_t)a.Hq;
-  if (misa::attend_blocks(a) >= (int64_t(1) << 31) || rows / 4 >= (int64_t(1) << 31))
+  if (misa::attend_blocks(a) >= (int64_t(1) << 31) || (a.planned && rows >= (int64_t(1) << 31)))
     return fail(MISA_ERR_ARG, "%s: grid too large", fn);
   return MISA_OK;
 }
 
 // Rows of a workgroup's tile in each pass of a call.
-int rows_of(int64_t T, int64_t nseq, int32_t Hq, int32_t heads, bool gather) {
-  return misa::attend_rows(T, nseq, Hq / heads, gather);
+int rows_of(int64_t T, int64_t nseq, int32_t Hq, int32_t heads, bool single) {
+  return misa::attend_rows(T, nseq, Hq / heads, single);
 }
 
 }  // namespace
@@ -990,7 +990,8 @@ int32_t misa_pivot_indexer(const void* q, const float* w, const void* k, const i
 size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t heads, int32_t d, int64_t nseq,
                                    int64_t npre) {
   if (T <= 0 || heads < 1 || Hq < heads || Hq % heads || !(d == 64 || d == 128 || d == 256) || nseq < 1) return 0;
-  const size_t own = misa::attend_ws_bytes(T, d, rows_of(T, nseq, Hq, heads, op == MISA_OP_ATTEND_SELECTED));
+  const bool single = op == MISA_OP_ATTEND_SELECTED || T <= nseq;
+  const size_t own = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, nseq, Hq, heads, single), single, !single);
   switch (op) {
     case MISA_OP_ATTEND:
     case MISA_OP_ATTEND_SELECTED:
@@ -998,7 +999,7 @@ size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t he
     case MISA_OP_ATTEND_SHARED: {
       if (npre < 1) return own;
       // the prefix pass's results in fp32, and its own workspace or the second pass's
-      const size_t pre = misa::attend_ws_bytes(T, d, rows_of(T, npre, Hq, heads, false));
+      const size_t pre = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, npre, Hq, heads, T <= npre), T <= npre, false);
       return round_up((size_t)T * Hq * d * 4) + round_up((size_t)T * Hq * 4) + (own > pre ? own : pre);
     }
   }
@@ -1074,8 +1075,9 @@ int32_t misa_attend(const misa_kv_cache* cache, const void* q, int64_t q_ts, int
   if (rc) return rc;
   a.q_start = q_start;
   a.mode = misa::kAttendPlain;
-  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, false);
-  misa::attend_setup(a, R, ws);
+  const bool single = T <= a.kv.nseq;
+  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, single);
+  misa::attend_setup(a, R, single, !single, ws);
   if ((rc = check_attend_grid(fn, a))) return rc;
   return hip_status(misa::launch_attend(a, R, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
 }
@@ -1098,7 +1100,7 @@ int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q, int64_t 
   a.topk = topk;
   a.mode = misa::kAttendPlain;
   const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, true);
-  misa::attend_setup(a, R, ws);
+  misa::attend_setup(a, R, true, false, ws);
   if ((rc = check_attend_grid(fn, a))) return rc;
   return hip_status(misa::launch_attend(a, R, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
 }
@@ -1147,13 +1149,14 @@ int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_
   b.out = nullptr;
   b.out32 = part;
   b.lse = part_lse;
-  const int Rb = rows_of(T, npre, Hq, a.Hkv, false);
-  misa::attend_setup(b, Rb, p);
+  const int Rb = rows_of(T, npre, Hq, a.Hkv, T <= npre);
+  misa::attend_setup(b, Rb, T <= npre, false, p);
   a.mode = misa::kAttendOwn;
   a.init_out = part;
   a.init_lse = part_lse;
-  const int Ra = rows_of(T, a.kv.nseq, Hq, a.Hkv, false);
-  misa::attend_setup(a, Ra, p);
+  const bool single = T <= a.kv.nseq;
+  const int Ra = rows_of(T, a.kv.nseq, Hq, a.Hkv, single);
+  misa::attend_setup(a, Ra, single, !single, p);
   if ((rc = check_attend_grid(fn, a)) || (rc = check_attend_grid(fn, b))) return rc;
   const bool half = cache->dtype == MISA_FP16;
   const hipError_t e = misa::launch_attend(b, Rb, half, (hipStream_t)stream);

@@ -92,7 +92,7 @@ struct Shape {
   static constexpr int merge_bytes = KW > 1 ? KW * R * (D + 4) * 4 + KW * R * 8 + R * 8 : 0;
   static constexpr int lds_bytes = 2 * stage_bytes > merge_bytes ? 2 * stage_bytes : merge_bytes;
   // workgroups that fit a CU (160 KiB of LDS, the plan's share included)
-  static constexpr int per_cu = (lds_bytes + kPlanMax * 8 + 64) * 2 <= 160 * 1024 ? 2 : 1;
+  static constexpr int per_cu = D < 256 && (lds_bytes + kPlanMax * 8 + 64) * 2 <= 160 * 1024 ? 2 : 1;
 };
 
 // 16-byte piece c of row r lies at piece c ^ swizzle(r) of its row in LDS. The
@@ -150,13 +150,27 @@ __device__ __forceinline__ QueryInfo query_info(const AttendArgs& a, int64_t t) 
 // a segment without keys still writes its rows).
 __device__ __forceinline__ int tiles_of(int lo, int hi, int KT) { return hi > lo ? (hi - lo + KT - 1) / KT : 1; }
 
+// Values that are the same in all lanes, as scalars.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  return (int64_t)(uint32_t)uniform((int)(uint32_t)v) | (int64_t)uniform((int)(v >> 32)) << 32;
+}
+
+// The launch's arguments, read anew: what was loaded from them before need not
+// stay in scalar registers.
+typedef const __attribute__((address_space(4))) AttendArgs* ArgPtr;
+__device__ __forceinline__ const AttendArgs& fresh(ArgPtr p) {
+  asm volatile("" : "+s"(p));
+  return *(const AttendArgs*)p;
+}
+
 // Work of a part of a segment.
 struct Part {
   int64_t t0;      // first query
   int nq;          // queries
   int hh;          // kv head * head_tiles + head tile
   int tile0, tile1;   // key tiles of it
-  int tiles;       // key tiles of the segment
+  bool whole;      // all of the segment's
   int slot;        // unfinished parts: where they are kept
 };
 
@@ -173,42 +187,45 @@ __device__ __forceinline__ int wave_max_of(int v) {
 
 // Sequence and span of the visible keys of queries t0 .. t0 + nq - 1 (one sequence).
 struct Span {
-  int seq, lo, hi;
+  int seq, lo, hi;   // keys that any of them sees lie in [lo, hi)
+  int some;          // keys that all of them see
 };
 __device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t t0, int nq) {
   const int lane = threadIdx.x & 63;
-  int lo = 0x7fffffff, hi = 0, seq = -1;
+  int lo = 0x7fffffff, hi = 0, seq = -1, all_lo = 0, all_hi = 0x7fffffff;
   for (int i = lane; i < nq; i += 64) {
-    const QueryInfo r = query_info(a, t0 + i);
+    QueryInfo r = query_info(a, t0 + i);
     seq = max(seq, r.seq);
     if (a.idx) {
-      lo = 0;
-      hi = r.hi > r.lo ? a.topk : 0;
-    } else if (r.hi > r.lo) {
+      r.hi = r.hi > r.lo ? a.topk : 0;
+      r.lo = 0;
+    }
+    if (r.hi > r.lo) {
       lo = min(lo, r.lo);
       hi = max(hi, r.hi);
     }
+    all_lo = max(all_lo, r.lo);
+    all_hi = min(all_hi, r.hi);
   }
   Span s;
-  s.seq = wave_max_of(seq);
-  s.lo = wave_min_of(lo);
-  s.hi = wave_max_of(hi);
+  s.seq = uniform(wave_max_of(seq));
+  s.lo = uniform(wave_min_of(lo));
+  s.hi = uniform(wave_max_of(hi));
   if (s.hi <= s.lo) s.lo = s.hi = 0;
+  s.some = uniform(wave_min_of(all_hi) - wave_max_of(all_lo));
   return s;
 }
 
-// One score in units of log2: the scale, the cap and the bias applied.
-// tanh(y) = 1 - 2 / (1 + e^2y); below 1/8 by its series, whose first left-out
-// term is y^8 62 / 2835 < 1.4e-9 of the value.
-__device__ __forceinline__ float shaped(float acc, float scale, float cap, float inv_cap, float slope, float dist) {
-  float x = acc * scale;
-  if (cap > 0.f) {
-    const float y = x * inv_cap, y2 = y * y;
-    const float big = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * (2.f * kLog2e)));
-    const float small = y * (1.f + y2 * (-1.f / 3.f + y2 * (2.f / 15.f - y2 * (17.f / 315.f))));
-    x = cap * (fabsf(y) < 0.125f ? small : big);
-  }
-  return (x - slope * dist) * kLog2e;
+// Caps up to this one take tanh(y) = 1 - 2 / (1 + e^2y) as it stands: exp2, the
+// sum and the reciprocal lose at most 8 half steps of fp32 of one, times the cap
+// (3e-5 of a score at the limit). Larger ones take the series
+// y (1 - y^2 / 3 + 2 y^4 / 15 - 17 y^6 / 315) below 1/8, where the difference
+// would cancel; its first left-out term is 62 y^8 / 2835 < 1.4e-9 of the value.
+constexpr float kPlainCap = 256.f;
+
+__device__ __forceinline__ float tanh_small(float y) {
+  const float y2 = y * y;
+  return y * (1.f + y2 * (-1.f / 3.f + y2 * (2.f / 15.f - y2 * (17.f / 315.f))));
 }
 
 // A finished row: sums relative to 2^m (m in units of log2) to the result and its log-sum.
@@ -228,7 +245,7 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, int 
   if (d0 == 0 && a.lse) a.lse[row] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * kLn2;
 }
 
-template <bool HALF, int D, int R, bool EXTRA>
+template <bool HALF, int D, int R, bool EXTRA, bool GUARD>
 struct Kernel {
   using S = Shape<D, R>;
   static constexpr int MR = S::MR, RW = S::RW, KW = S::KW, NK = S::NK, KT = S::KT, TH = S::threads;
@@ -261,35 +278,42 @@ struct Kernel {
     int head;
   };
 
-  // The keys of one step for one group of waves: lane l looks up key l.
-  struct Look {
-    int page;       // -1: no key
-    int token;
+  // The keys of one step for one group of waves: lane l looks up key l, in three
+  // steps of the loop: its token (the key's number, or a selected id), the table
+  // entry of its page, and its row. A load is issued in one step and used in the
+  // next, so none is waited for.
+  struct Keys {
+    int token;      // -1: none
+    int page;
   };
-
-  __device__ static __forceinline__ Look look_up(const AttendArgs& a, const Span& sp, const int32_t* ids, int s, int end,
-                                                 int lo, int hi) {
+  // token of the lane's key s + lane (not before `end`; selected ids still unchecked)
+  __device__ static __forceinline__ int token_of(const int32_t* ids, int s, int end) {
     const int lane = threadIdx.x & 63;
-    Look r;
-    r.page = -1;
-    r.token = 0;
-    s += lane;
-    if (lane < NK && s < end) {
-      int tok = s;
-      if (ids) tok = ids[s];
-      if (tok >= lo && tok < hi) {
-        const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)tok);
-        r.page = kv_page(a.kv, sp.seq, col);
-        r.token = tok;
-      }
-    }
-    return r;
+    const int at = s + lane;
+    const bool in = lane < NK && at < end;
+    if (!ids) return in ? at : -1;
+    const int id = ids[min(at, end - 1)];
+    return in ? id : -1;
   }
-  // element offset of the row looked up; -1: none
-  __device__ static __forceinline__ int64_t row_offset(const AttendArgs& a, const Look& l, int64_t head_off) {
-    if (l.page < 0) return -1;
-    const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)l.token);
-    return (int64_t)l.page * a.kv.page_stride + (int64_t)(l.token - (int)col * a.kv.page) * a.kv.tok_stride + head_off;
+  __device__ static __forceinline__ Keys page_of(const AttendArgs& a, const Span& sp, int token, int lo, int hi) {
+    Keys k;
+    k.token = token >= lo && token < hi ? token : -1;
+    if (!a.kv.table) {
+      k.page = sp.seq;
+    } else {
+      const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)max(k.token, 0));
+      k.page = a.kv.table[(int64_t)sp.seq * a.kv.table_stride + col];
+    }
+    return k;
+  }
+  __device__ static __forceinline__ bool is_key(const AttendArgs& a, const Keys& k) {
+    return k.token >= 0 && k.page >= 0 && k.page < a.kv.npages;
+  }
+  // element offset of the row; -1: none
+  __device__ static __forceinline__ int64_t row_offset(const AttendArgs& a, const Keys& k, int64_t head_off) {
+    const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)max(k.token, 0));
+    const int64_t at = (int64_t)k.page * a.kv.page_stride + (int64_t)(k.token - (int)col * a.kv.page) * a.kv.tok_stride + head_off;
+    return is_key(a, k) ? at : -1;
   }
 
   __device__ static __forceinline__ void load_rows(const AttendArgs& a, int64_t off, int rw, u32x4 (&kr)[NLD],
@@ -322,16 +346,17 @@ struct Kernel {
     const int lane = threadIdx.x & 63;
     const int r = lane % MR, g = lane / MR;
 #pragma unroll
-    for (int i = 0; i < ST; ++i) {
+    for (int i = 0; i < ST; ++i)
 #pragma unroll
       for (int j = 0; j < AR; ++j) s[i][j] = 0.f;
 #pragma unroll
-      for (int f = 0; f < QF; ++f) {
+    for (int f = 0; f < QF; ++f)
+#pragma unroll
+      for (int i = 0; i < ST; ++i) {
         const int row = i * MR + r;
         const int c = (f * (64 / MR) + g) ^ swizzle<D>(row);
         s[i] = mma(*reinterpret_cast<const u32x4*>(ks + row * D + 8 * c), qf[f], s[i]);
       }
-    }
   }
 
   // 4 values V[key0 + 0..3][dim] of this lane's output dim: 16 lanes read 4 rows of 16 dims
@@ -345,21 +370,10 @@ struct Kernel {
                                          __attribute__((address_space(3))) const uint16_t*)p));
   }
 
-  // Bits of the halves of x that hold an infinity or a NaN: ~0 or 0 each.
-  __device__ static __forceinline__ uint32_t not_finite(uint32_t x) {
+  // The halves of x without infinities and NaNs.
+  __device__ static __forceinline__ uint32_t finite_only(uint32_t x) {
     constexpr uint32_t e = HALF ? 0x7c00u : 0x7f80u;
-    return ((x & e) == e ? 0xffffu : 0u) | ((x & (e << 16)) == (e << 16) ? 0xffff0000u : 0u);
-  }
-  __device__ static __forceinline__ bool any_not_finite(const uint16_t* vs) {
-    const int lane = threadIdx.x & 63;
-    uint32_t bad = 0;
-#pragma unroll 4
-    for (int e = lane * 8; e < NK * D; e += 512) {
-      const u32x4 x = *reinterpret_cast<const u32x4*>(vs + e);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) bad |= not_finite(x[i]);
-    }
-    return __any(bad != 0);
+    return x & (((x & e) == e ? 0u : 0xffffu) | ((x & (e << 16)) == (e << 16) ? 0u : 0xffff0000u));
   }
 
   // The operand V^T of product p, output tile i.
@@ -397,7 +411,7 @@ struct Kernel {
   // are not all finite: the product would carry 0 * inf = NaN into rows that do
   // not see them. The finite values are multiplied as above; then, for +inf, -inf
   // and NaN in turn, a product of marks counts those that each row sees.
-  __device__ static __noinline__ void accumulate_guarded(const uint16_t* vs, Acc (&s)[ST], Acc (&o)[OT], int base, int lo,
+  __device__ static __forceinline__ void accumulate_guarded(const uint16_t* vs, Acc (&s)[ST], Acc (&o)[OT], int base, int lo,
                                                          int hi, uint64_t valid) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -407,7 +421,7 @@ struct Kernel {
       for (int i = 0; i < OT; ++i) {
         u32x4 v = value_frag(vs, p, i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] &= ~not_finite(v[e]);
+        for (int e = 0; e < 4; ++e) v[e] = finite_only(v[e]);
         o[i] = mma(v, w, o[i]);
       }
     }
@@ -449,6 +463,70 @@ struct Kernel {
     }
   }
 
+  // Cap and bias; the scores leave in units of log2.
+  __device__ static __forceinline__ void shape(const AttendArgs& a, Acc (&s)[ST], const Rows& row, const int32_t* ids, int base,
+                                               int token) {
+    const int lane = threadIdx.x & 63;
+    if (a.cap > 0.f && a.cap <= kPlainCap) {
+      const float c = a.scale / a.cap * (2.f * kLog2e), cap2 = a.cap * kLog2e;
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+#pragma unroll
+        for (int j = 0; j < AR; ++j)
+          s[i][j] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[i][j] * c));
+    } else if (a.cap > 0.f) {
+      const float c = a.scale / a.cap, cap2 = a.cap * kLog2e;
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+#pragma unroll
+        for (int j = 0; j < AR; ++j) {
+          const float y = s[i][j] * c;
+          const float big = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * (2.f * kLog2e)));
+          s[i][j] = cap2 * (fabsf(y) < 0.125f ? tanh_small(y) : big);
+        }
+    } else {
+      const float c = a.scale * kLog2e;
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+#pragma unroll
+        for (int j = 0; j < AR; ++j) s[i][j] *= c;
+    }
+    if (!a.slopes) return;
+    const float slope = row.slope * kLog2e;
+    if (ids) {
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+#pragma unroll
+        for (int j = 0; j < AR; ++j)
+          s[i][j] -= slope * fabsf((float)(row.pos - __shfl(token, i * MR + acc_row(j, lane), 64)));
+    } else {
+      // distances of consecutive keys; exact in fp32 up to 2^24
+      const float first = (float)(row.pos - base - acc_row(0, lane));
+      const bool far = row.pos >= (1 << 23) || row.pos < -(1 << 23) || base >= (1 << 23);
+#pragma unroll
+      for (int i = 0; i < ST; ++i)
+#pragma unroll
+        for (int j = 0; j < AR; ++j) {
+          const int key = i * MR + acc_row(j, 0);
+          s[i][j] -= slope * fabsf(far ? (float)(row.pos - base - acc_row(0, lane) - key) : first - (float)key);
+        }
+    }
+  }
+
+  // Bits from b on of 64.
+  __device__ static __forceinline__ uint64_t bits_from(int b) { return b >= 64 ? 0 : ~0ull << (b > 0 ? b : 0); }
+  // -inf for the scores of keys whose bit in `see` is not set.
+  __device__ static __forceinline__ void hide(uint64_t see, Acc (&s)[ST]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < ST; ++i) {
+      const uint32_t w = (uint32_t)(see >> (i * MR)) >> acc_row(0, lane);
+#pragma unroll
+      for (int j = 0; j < AR; ++j)
+        s[i][j] = w >> acc_row(j, 0) & 1 ? s[i][j] : -__builtin_inff();
+    }
+  }
+
   __device__ static __forceinline__ float over_rows_max(float v) {
     if constexpr (MR == 16) v = fmaxf(v, __shfl_xor(v, 16, 64));
     return fmaxf(v, __shfl_xor(v, 32, 64));
@@ -460,9 +538,9 @@ struct Kernel {
 
   // Result or unfinished sums of row r (of the tile), dims d0 .. d0 + 3.
   // m in units of log2; sum and o relative to 2^m.
-  __device__ static __forceinline__ void emit(const AttendArgs& a, const Part& p, bool whole, int64_t t, int head, int r,
+  __device__ static __forceinline__ void emit(const AttendArgs& a, const Part& p, int64_t t, int head, int r,
                                               int d0, float m, float sum, floatx4 o) {
-    if (!whole) {
+    if (!p.whole) {
       *reinterpret_cast<floatx4*>(a.part_out + ((int64_t)p.slot * R + r) * D + d0) = o;
       if (d0 == 0) {
         a.part_ml[((int64_t)p.slot * R + r) * 2] = m;
@@ -474,13 +552,17 @@ struct Kernel {
     write_row<HALF, D>(a, row, d0, m, sum, o);
   }
 
-  __device__ static __forceinline__ void run_part(const AttendArgs& a, const Part& p, unsigned char* lds) {
+  // One part. A product with a value that is not finite leaves a NaN also in rows
+  // that do not see it (0 * inf). Where the queries of a part do not see the same
+  // keys (odd is not null) and anything comes out infinite or NaN, *odd is set
+  // and the guarded form computes the workgroup's parts again.
+  __device__ static __forceinline__ void run_part(ArgPtr ap, const Part& p, unsigned char* lds, int* odd) {
+    const AttendArgs& a = fresh(ap);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = wave % RW, kw = wave / RW;
     const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
     const Span sp = span_of(a, p.t0, p.nq);
-    const bool whole = p.tile0 == 0 && p.tile1 == p.tiles;
     // p.tile1 * KT may pass the last key (and 2^31): 64 bits
     const int begin = sp.lo + p.tile0 * KT;
     const int end = (int)min((int64_t)sp.hi, sp.lo + (int64_t)p.tile1 * KT);
@@ -515,14 +597,14 @@ struct Kernel {
     if (a.idx) {
       const QueryInfo q = query_info(a, p.t0);
       ids = a.idx + p.t0 * a.topk;
-      id_lo = q.lo;
-      id_hi = q.hi;
+      id_lo = uniform(q.lo);
+      id_hi = uniform(q.hi);
     }
     // keys that every row of this wave sees, and keys that any of them sees
-    const int all_lo = wave_max_of(row.active ? row.lo : 0);
-    const int all_hi = wave_min_of(row.active ? row.hi : 0x7fffffff);
-    const int any_lo = wave_min_of(row.active ? row.lo : 0x7fffffff);
-    const int any_hi = wave_max_of(row.active ? row.hi : 0);
+    const int all_lo = uniform(wave_max_of(row.active ? row.lo : 0));
+    const int all_hi = uniform(wave_min_of(row.active ? row.hi : 0x7fffffff));
+    const int any_lo = uniform(wave_min_of(row.active ? row.lo : 0x7fffffff));
+    const int any_hi = uniform(wave_max_of(row.active ? row.hi : 0));
 
     u32x4 qf[QF];
     {
@@ -558,61 +640,50 @@ struct Kernel {
     }
     const float sc = EXTRA ? 1.f : a.scale * kLog2e;
     if (!EXTRA) m = m / sc;   // in units of the raw scores while the keys are read
-    const float inv_cap = EXTRA && a.cap > 0.f ? 1.f / a.cap : 0.f;
 
     uint16_t* buf = reinterpret_cast<uint16_t*>(lds);
     constexpr int GB = NK * D;             // elements of one tensor of one group's step
     constexpr int SB = KW * 2 * GB;        // of one buffer
     const int64_t head_off = (int64_t)kvh * a.kv.head_stride;
     const int k0 = begin + kw * NK;
-    Look cur{-1, 0}, nxt{-1, 0};
     u32x4 kr[NLD], vr[NLD];
+    Keys cur, nxt;
+    int far = -1;
+    cur.token = nxt.token = -1;
+    cur.page = nxt.page = 0;
     if (steps > 0) {
-      cur = look_up(a, sp, ids, k0, end, id_lo, id_hi);
+      cur = page_of(a, sp, token_of(ids, k0, end), id_lo, id_hi);
+      nxt = page_of(a, sp, token_of(ids, k0 + KT, end), id_lo, id_hi);
+      far = token_of(ids, k0 + 2 * KT, end);
       load_rows(a, row_offset(a, cur, head_off), rw, kr, vr);
-      if (steps > 1) nxt = look_up(a, sp, ids, k0 + KT, end, id_lo, id_hi);
       store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
     }
+    // the loop's first products wait for these loads here, not for its own
+#pragma unroll
+    for (int f = 0; f < QF; ++f) asm volatile("" : "+v"(qf[f]));
     __syncthreads();
     for (int it = 0; it < steps; ++it) {
       const bool more = it + 1 < steps;
-      Look after{-1, 0};
+      Keys after;
+      after.token = -1;
+      after.page = 0;
       if (more) {
-        load_rows(a, row_offset(a, nxt, head_off), rw, kr, vr);
-        if (it + 2 < steps) after = look_up(a, sp, ids, k0 + (it + 2) * KT, end, id_lo, id_hi);
+        const int64_t off = row_offset(a, nxt, head_off);
+        after = page_of(a, sp, far, id_lo, id_hi);
+        far = token_of(ids, k0 + (it + 3) * KT, end);
+        load_rows(a, off, rw, kr, vr);
       }
       const uint16_t* ks = buf + (it & 1) * SB + kw * 2 * GB;
       const int base = k0 + it * KT;
-      const uint64_t valid = __ballot(cur.page >= 0);
+      const uint64_t valid = __ballot(is_key(a, cur));
       if (base < any_hi && base + NK > any_lo && valid != 0) {
         Acc s[ST];
         score(ks, qf, s);
-        if constexpr (EXTRA) {
-#pragma unroll
-          for (int i = 0; i < ST; ++i)
-#pragma unroll
-            for (int j = 0; j < AR; ++j) {
-              const int key = i * MR + acc_row(j, lane);
-              float dist = 0.f;
-              if (a.slopes) {
-                const int tok = ids ? __shfl(cur.token, key, 64) : base + key;
-                dist = fabsf((float)(row.pos - tok));
-              }
-              s[i][j] = shaped(s[i][j], a.scale, a.cap, inv_cap, row.slope, dist);
-            }
-        }
+        if constexpr (EXTRA) shape(a, s, row, ids, base, cur.token);
         constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK & 63)) - 1;
-        if (!(valid == kAll && base >= all_lo && base + NK <= all_hi)) {
-#pragma unroll
-          for (int i = 0; i < ST; ++i)
-#pragma unroll
-            for (int j = 0; j < AR; ++j) {
-              const int key = i * MR + acc_row(j, lane);
-              const bool see = base + key >= row.lo && base + key < row.hi && ((valid >> key) & 1);
-              s[i][j] = see ? s[i][j] : -__builtin_inff();
-            }
-        }
-        float mx = -__builtin_inff();
+        if (!(valid == kAll && base >= all_lo && base + NK <= all_hi))
+          hide(valid & bits_from(row.lo - base) & ~bits_from(row.hi - base), s);
+        float mx = s[0][0];
 #pragma unroll
         for (int i = 0; i < ST; ++i)
 #pragma unroll
@@ -639,19 +710,8 @@ struct Kernel {
             add += s[i][j];
           }
         sum += add;
-        // keys of this step that some query of the part sees and some row of this wave does not
-        if ((base < all_lo || min(base + NK, end) > all_hi) && any_not_finite(ks + GB)) {
-          Acc sv[ST], oc[OT];   // copies: the registers of the usual path have no address
-#pragma unroll
-          for (int i = 0; i < ST; ++i) sv[i] = s[i];
-#pragma unroll
-          for (int i = 0; i < OT; ++i) oc[i] = o[i];
-          accumulate_guarded(ks + GB, sv, oc, base, row.lo, row.hi, valid);
-#pragma unroll
-          for (int i = 0; i < OT; ++i) o[i] = oc[i];
-        } else {
-          accumulate(ks + GB, s, o);
-        }
+        if constexpr (GUARD) accumulate_guarded(ks + GB, s, o, base, row.lo, row.hi, valid);
+        else accumulate(ks + GB, s, o);
       }
       cur = nxt;
       nxt = after;
@@ -661,8 +721,25 @@ struct Kernel {
       }
       __syncthreads();
     }
+    finish(fresh(ap), p, sp, lds, odd, row, r, kw, rw, m * sc, sum, o);
+  }
 
-    m *= sc;
+  // The end of a part: joins the groups of waves and writes the rows.
+  __device__ static __forceinline__ void finish(const AttendArgs& a, const Part& p, const Span& sp, unsigned char* lds,
+                                                int* odd, const Rows& row, int r, int kw, int rw, float m, float sum,
+                                                Acc (&o)[OT]) {
+    const int lane = threadIdx.x & 63;
+    const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
+    if constexpr (!GUARD) {
+      if (odd && sp.some < sp.hi - sp.lo) {
+        float z = 0.f;
+#pragma unroll
+        for (int i = 0; i < OT; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j) z = __builtin_fmaf(o[i][j], 0.f, z);
+        if (z != z) *odd = 1;
+      }
+    }
     sum = over_rows_sum(sum);
     if constexpr (KW == 1) {
       if (row.active) {
@@ -670,7 +747,7 @@ struct Kernel {
         for (int i = 0; i < OT; ++i)
 #pragma unroll
           for (int j = 0; j < AR; j += 4)
-            emit(a, p, whole, row.t, row.head, r, i * MR + acc_row(j, lane), m, sum,
+            emit(a, p, row.t, row.head, r, i * MR + acc_row(j, lane), m, sum,
                  floatx4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
       }
     } else {
@@ -710,7 +787,7 @@ struct Kernel {
         floatx4 x = *reinterpret_cast<const floatx4*>(ob + rr * (D + 4) + d0);
 #pragma unroll
         for (int i = 1; i < KW; ++i) x += *reinterpret_cast<const floatx4*>(ob + (i * R + rr) * (D + 4) + d0);
-        emit(a, p, whole, p.t0 + q, head, rr, d0, fin[rr * 2], fin[rr * 2 + 1], x);
+        emit(a, p, p.t0 + q, head, rr, d0, fin[rr * 2], fin[rr * 2 + 1], x);
       }
       __syncthreads();   // the next part's first rows go to the same memory
     }
@@ -791,44 +868,56 @@ struct Kernel {
     return total;
   }
 
-  __device__ static __forceinline__ void body(const AttendArgs& a, unsigned char* lds, int64_t* cum) {
+  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int64_t* cum, int* odd) {
+    const AttendArgs& a = fresh(ap);
+    const bool mixed = a.odd != nullptr;
+    if (GUARD) {
+      if (!a.odd[blockIdx.x]) return;
+    } else if (mixed) {
+      if (threadIdx.x == 0) *odd = 0;
+      __syncthreads();
+    }
     // units of work [u, u1): queries of this workgroup's row tile, or key tiles of the plan
+    const int NH = a.NH, T = (int)a.T;
+    const bool planned = a.planned;
     int64_t total = 0, u, u1;
     int hh = 0;
-    if (a.planned) {
-      total = make_plan(a, cum);
-      const int64_t units = total * a.NH;
+    if (planned) {
+      total = uniform(make_plan(a, cum));
+      const int64_t units = total * NH;
       u = blockIdx.x * units / a.G;
       u1 = ((int64_t)blockIdx.x + 1) * units / a.G;
-      if (blockIdx.x == 0) publish_plan(a, cum, total);
+      if (blockIdx.x == 0 && !GUARD) publish_plan(a, cum, total);
     } else {
       // one workgroup per row tile, the last queries (the longest of a causal prompt) first
-      const int64_t ntiles = (a.T + a.qt - 1) / a.qt;
-      const int64_t tile = ntiles - 1 - (int64_t)(blockIdx.x / (unsigned)a.NH);
-      hh = blockIdx.x % (unsigned)a.NH;
-      u = tile * a.qt;
-      u1 = min(a.T, u + a.qt);
+      const unsigned ntiles = (unsigned)((T + a.qt - 1) / a.qt);
+      const unsigned tile = ntiles - 1 - blockIdx.x / (unsigned)NH;
+      hh = blockIdx.x % (unsigned)NH;
+      u = (int64_t)tile * a.qt;
+      u1 = min((int64_t)T, u + a.qt);
     }
     while (u < u1) {
       Part p;
-      if (a.planned) {
+      if (planned) {
         // the last query whose segment starts at or before unit u
-        int lo = 0, hi = (int)a.T - 1;
+        int lo = 0, hi = T - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (cum[mid] * a.NH <= u) lo = mid;
+          if (cum[mid] * NH <= u) lo = mid;
           else hi = mid - 1;
         }
-        lo = __builtin_amdgcn_readfirstlane(lo);
+        lo = uniform(lo);
+        const int64_t first = uniform(cum[lo]);
         p.t0 = lo;
         p.nq = run_length(a, lo);
         const int next = lo + p.nq;
-        p.tiles = (int)((next < (int)a.T ? cum[next] : total) - cum[lo]);
-        const int64_t in = u - cum[lo] * a.NH;
-        p.hh = (int)(in / p.tiles);
-        p.tile0 = (int)(in - (int64_t)p.hh * p.tiles);
+        const int tiles = (int)((next < T ? uniform(cum[next]) : total) - first);
+        const int64_t in = u - first * NH;
+        p.hh = (int)(in / tiles);
+        p.tile0 = (int)(in - (int64_t)p.hh * tiles);
         const int64_t left = u1 - u;
-        p.tile1 = left < p.tiles - p.tile0 ? p.tile0 + (int)left : p.tiles;
+        p.tile1 = left < tiles - p.tile0 ? p.tile0 + (int)left : tiles;
+        p.whole = p.tile0 == 0 && p.tile1 == tiles;
         p.slot = (int)(2 * blockIdx.x + (p.tile0 > 0 ? 0 : 1));
         u += p.tile1 - p.tile0;
       } else {
@@ -836,11 +925,16 @@ struct Kernel {
         p.nq = run_length(a, u);
         p.hh = hh;
         p.tile0 = 0;
-        p.tiles = p.tile1 = 0x7fffffff;
+        p.tile1 = 0x7fffffff;
+        p.whole = true;
         p.slot = 0;
         u += p.nq;
       }
-      run_part(a, p, lds);
+      run_part(ap, p, lds, mixed ? odd : nullptr);
+    }
+    if (!GUARD && mixed) {
+      __syncthreads();
+      if (threadIdx.x == 0) fresh(ap).odd[blockIdx.x] = *odd;
     }
   }
 
@@ -861,22 +955,26 @@ struct Kernel {
   }
 };
 
-template <bool HALF, int D, int R, bool EXTRA>
+template <bool HALF, int D, int R, bool EXTRA, bool GUARD>
 __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shape<D, R>::threads / 256 > 0
                                                           ? Shape<D, R>::per_cu * Shape<D, R>::threads / 256
-                                                          : 1)) void attend_kernel(AttendArgs a) {
+                                                          : 1)) void attend_kernel(AttendArgs) {
   __shared__ __align__(16) unsigned char lds[Shape<D, R>::lds_bytes];
   __shared__ int64_t cum[kPlanMax];
-  Kernel<HALF, D, R, EXTRA>::body(a, lds, cum);
+  __shared__ int odd;
+  // the arguments are read where they lie (see fresh)
+  Kernel<HALF, D, R, EXTRA, GUARD>::body((ArgPtr)__builtin_amdgcn_kernarg_segment_ptr(), lds, cum, &odd);
 }
 
 template <bool HALF, int D, int R>
 hipError_t launch_shape(const AttendArgs& a, unsigned blocks, hipStream_t st) {
   const dim3 grid(blocks), block(Shape<D, R>::threads);
   if (a.cap > 0.f || a.slopes)
-    hipLaunchKernelGGL((attend_kernel<HALF, D, R, true>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, false>), grid, block, 0, st, a);
   else
-    hipLaunchKernelGGL((attend_kernel<HALF, D, R, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((attend_kernel<HALF, D, R, false, false>), grid, block, 0, st, a);
+  // workgroups that met values that are not finite where not all rows see them
+  if (a.odd) hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, true>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

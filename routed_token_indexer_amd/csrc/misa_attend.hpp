@@ -55,6 +55,9 @@ struct AttendArgs {
   float* lse;               // [T][Hq] or null
   const float* init_out;    // [T][Hq][d] and [T][Hq]: a finished part to join, or null
   const float* init_lse;
+  // one word a workgroup, set if its parts have to be computed again by the
+  // guarded form; null where all rows of a part see the same keys
+  int32_t* odd;
   // planned batches
   int32_t planned;
   int32_t G;                // workgroups
@@ -65,13 +68,17 @@ struct AttendArgs {
 };
 
 // Rows (query, head) of a workgroup's tile for a batch: 16, 32, 64 or 128.
-int attend_rows(int64_t T, int64_t nseq, int group, bool gather);
+// single: a row tile takes one query (selected tokens are each query's own; in a
+// decode step no two queries share a sequence).
+int attend_rows(int64_t T, int64_t nseq, int group, bool single);
 bool attend_planned(int64_t T);
 // Workgroups of a planned launch, and its workspace.
 int attend_groups(int d, int R);
-size_t attend_ws_bytes(int64_t T, int d, int R);
+size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, bool mixed);
 // Fills the fields that depend on the tile and carves the workspace.
-void attend_setup(AttendArgs& a, int R, void* ws);
+// mixed: queries of one part may see different keys (several queries a row tile,
+// intervals of their own).
+void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws);
 int64_t attend_blocks(const AttendArgs& a);
 hipError_t launch_attend(const AttendArgs& a, int R, bool half, hipStream_t st);
 

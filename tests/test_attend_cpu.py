@@ -147,7 +147,7 @@ def test_workspaces(B):
         assert w(op, 0, 64, 8, 128, 4) == 0
         # bounded by the workgroups of a launch, not by the batch or its lengths
         assert 0 < w(op, 4, 64, 8, 128, 4) < 64 << 20
-        assert w(op, 100000, 64, 8, 128, 4) == 0
+        assert w(op, 100000, 64, 8, 128, 4) < 1 << 20
         assert w(op, 4, 64, 7, 128, 4) == 0 and w(op, 4, 64, 8, 96, 4) == 0
     assert w(B.OP_ATTEND_SHARED, 64, 64, 8, 128, 64, 1) > 64 * 64 * 128 * 4
     assert w(99, 4, 64, 8, 128, 4) == 0
