@@ -291,6 +291,23 @@ int32_t check_cache(const char* fn, const misa_kv_cache* c, misa::KvView* out) {
   v.table_stride = c->table_cols;
   v.nseq = c->nseq;
   v.Lmax = c->table ? c->table_cols * c->page : c->page;
+  // rows in 32 bits: bytes if all of them lie within 4 GiB, else the largest unit
+  // that divides both strides (axes of one element have none)
+  const uint64_t ps = c->npages > 1 ? (uint64_t)c->page_stride : 0, ts = c->page > 1 ? (uint64_t)c->token_stride : 0;
+  const __uint128_t span = (__uint128_t)(c->npages - 1) * ps + (__uint128_t)(c->page - 1) * ts;
+  const __uint128_t bytes = (span + (__uint128_t)(c->heads - 1) * (uint64_t)c->head_stride + (uint64_t)(c->d > 0 ? c->d : 0)) * 2;
+  if (bytes <= 0xffff0000u) {
+    v.bytes = (uint32_t)bytes;
+    v.page_units = (uint32_t)(ps * 2);
+    v.tok_units = (uint32_t)(ts * 2);
+  } else {
+    const int shift = ps | ts ? __builtin_ctzll(ps | ts) : 3;
+    v.unit_shift = (uint32_t)(shift < 31 ? shift : 31);
+    if (bytes >> 62 || (span >> v.unit_shift) >= 0xffff0000u)
+      return fail(MISA_ERR_ARG, "%s: a cache of %lld pages with these strides is too large", fn, (long long)c->npages);
+    v.page_units = (uint32_t)(ps >> v.unit_shift);
+    v.tok_units = (uint32_t)(ts >> v.unit_shift);
+  }
   *out = v;
   return MISA_OK;
 }
@@ -332,14 +349,21 @@ int32_t check_attend(const char* fn, const misa_kv_cache* c, const void* q, int6
 
 int32_t check_attend_grid(const char* fn, const misa::AttendArgs& a) {
   const int64_t rows = a.T * (int64_t)a.Hq;
-  if (misa::attend_blocks(a) >= (int64_t(1) << 31) || (a.planned && rows >= (int64_t(1) << 31)))
+  if (misa::attend_blocks(a) >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31))
     return fail(MISA_ERR_ARG, "%s: grid too large", fn);
   return MISA_OK;
 }
 
+// One pass and the join of its parts.
+int32_t run_attend(const char* fn, const misa::AttendArgs& a, int R, bool half, hipStream_t st) {
+  hipError_t e = misa::launch_attend(a, R, half, st);
+  if (e == hipSuccess) e = misa::launch_attend_join(a, R, nullptr, 0, a.out, a.lse, half, st);
+  return hip_status(e, fn);
+}
+
 // Rows of a workgroup's tile in each pass of a call.
-int rows_of(int64_t T, int64_t nseq, int32_t Hq, int32_t heads, bool single) {
-  return misa::attend_rows(T, nseq, Hq / heads, single);
+int rows_of(int64_t T, int64_t nseq, int32_t Hq, int32_t heads, int32_t d, bool single) {
+  return misa::attend_rows(T, nseq, Hq / heads, d, single);
 }
 
 }  // namespace
@@ -991,16 +1015,16 @@ size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t he
                                    int64_t npre) {
   if (T <= 0 || heads < 1 || Hq < heads || Hq % heads || !(d == 64 || d == 128 || d == 256) || nseq < 1) return 0;
   const bool single = op == MISA_OP_ATTEND_SELECTED || T <= nseq;
-  const size_t own = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, nseq, Hq, heads, single), single, !single);
+  const size_t own = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, nseq, Hq, heads, d, single), single, !single);
   switch (op) {
     case MISA_OP_ATTEND:
     case MISA_OP_ATTEND_SELECTED:
       return own;
     case MISA_OP_ATTEND_SHARED: {
       if (npre < 1) return own;
-      // the prefix pass's results in fp32, and its own workspace or the second pass's
-      const size_t pre = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, npre, Hq, heads, T <= npre), T <= npre, false);
-      return round_up((size_t)T * Hq * d * 4) + round_up((size_t)T * Hq * 4) + (own > pre ? own : pre);
+      // each pass's whole rows in fp32 and its own workspace
+      const size_t pre = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, npre, Hq, heads, d, T <= npre), T <= npre, false);
+      return 2 * (round_up((size_t)T * Hq * d * 4) + round_up((size_t)T * Hq * 4)) + own + pre;
     }
   }
   return 0;
@@ -1076,10 +1100,10 @@ int32_t misa_attend(const misa_kv_cache* cache, const void* q, int64_t q_ts, int
   a.q_start = q_start;
   a.mode = misa::kAttendPlain;
   const bool single = T <= a.kv.nseq;
-  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, single);
+  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, single);
   misa::attend_setup(a, R, single, !single, ws);
   if ((rc = check_attend_grid(fn, a))) return rc;
-  return hip_status(misa::launch_attend(a, R, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
+  return run_attend(fn, a, R, cache->dtype == MISA_FP16, (hipStream_t)stream);
 }
 
 int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs, const int32_t* idx,
@@ -1099,10 +1123,10 @@ int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q, int64_t 
   a.idx = idx;
   a.topk = topk;
   a.mode = misa::kAttendPlain;
-  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, true);
+  const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, true);
   misa::attend_setup(a, R, true, false, ws);
   if ((rc = check_attend_grid(fn, a))) return rc;
-  return hip_status(misa::launch_attend(a, R, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
+  return run_attend(fn, a, R, cache->dtype == MISA_FP16, (hipStream_t)stream);
 }
 
 int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs, const int32_t* q_seq,
@@ -1128,16 +1152,20 @@ int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_
   rc = check_ws(fn, ws, ws_bytes, misa_attend_workspace_bytes(MISA_OP_ATTEND_SHARED, T, Hq, a.Hkv, a.d, a.kv.nseq, npre));
   if (rc) return rc;
   char* p = static_cast<char*>(ws);
-  float* part = reinterpret_cast<float*>(p);
-  p += round_up((size_t)T * Hq * a.d * 4);
-  float* part_lse = reinterpret_cast<float*>(p);
-  p += round_up((size_t)T * Hq * 4);
+  float* rows[2];
+  float* lses[2];
+  for (int i = 0; i < 2; ++i) {
+    rows[i] = reinterpret_cast<float*>(p);
+    p += round_up((size_t)T * Hq * a.d * 4);
+    lses[i] = reinterpret_cast<float*>(p);
+    p += round_up((size_t)T * Hq * 4);
+  }
   a.pre = pre;
   a.pre_len = pre_len;
   a.npre = npre;
   a.pre_max = pre_table ? pre_cols * cache->page : cache->page;
 
-  // the prefixes first, for all of their queries; their results join the own parts
+  // the prefixes for all of their queries, the own parts, and the join of both
   misa::AttendArgs b = a;
   b.mode = misa::kAttendPrefix;
   b.own_seq = q_seq;
@@ -1147,21 +1175,25 @@ int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_
   b.kv.nseq = npre;
   b.kv.Lmax = a.pre_max;
   b.out = nullptr;
-  b.out32 = part;
-  b.lse = part_lse;
-  const int Rb = rows_of(T, npre, Hq, a.Hkv, T <= npre);
+  b.out32 = rows[0];
+  b.lse = lses[0];
+  const int Rb = rows_of(T, npre, Hq, a.Hkv, a.d, T <= npre);
   misa::attend_setup(b, Rb, T <= npre, false, p);
+  p += misa::attend_ws_bytes(T, Hq, a.Hkv, a.d, Rb, T <= npre, false);
   a.mode = misa::kAttendOwn;
-  a.init_out = part;
-  a.init_lse = part_lse;
+  a.out = nullptr;
+  a.out32 = rows[1];
+  a.lse = lses[1];
   const bool single = T <= a.kv.nseq;
-  const int Ra = rows_of(T, a.kv.nseq, Hq, a.Hkv, single);
+  const int Ra = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, single);
   misa::attend_setup(a, Ra, single, !single, p);
   if ((rc = check_attend_grid(fn, a)) || (rc = check_attend_grid(fn, b))) return rc;
   const bool half = cache->dtype == MISA_FP16;
-  const hipError_t e = misa::launch_attend(b, Rb, half, (hipStream_t)stream);
-  if (e != hipSuccess) return hip_status(e, fn);
-  return hip_status(misa::launch_attend(a, Ra, half, (hipStream_t)stream), fn);
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = misa::launch_attend(b, Rb, half, st);
+  if (e == hipSuccess) e = misa::launch_attend(a, Ra, half, st);
+  if (e == hipSuccess) e = misa::launch_attend_join(b, Rb, &a, Ra, static_cast<uint16_t*>(out), lse, half, st);
+  return hip_status(e, fn);
 }
 
 int32_t misa_debug_scores(const void* q, const float* w, const void* k, const int32_t* heads, int32_t h,

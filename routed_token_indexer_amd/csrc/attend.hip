@@ -9,86 +9,152 @@ using attend::Shape;
 
 constexpr int kCUs = 256;
 
+// What the join reads of a pass.
+struct Pass {
+  const PlanEntry* plan;    // null: every row is whole
+  const int64_t* plan_total;
+  const float* part_out;
+  const float* part_ml;
+  const float* whole_out;   // [T][Hq][D] and [T][Hq], for rows that are whole
+  const float* whole_lse;
+  int32_t G, R, NH, group, head_tiles, gw;
+};
+Pass pass_of(const AttendArgs& a, int R) {
+  Pass p;
+  p.plan = a.planned ? a.plan : nullptr;
+  p.plan_total = a.plan_total;
+  p.part_out = a.part_out;
+  p.part_ml = a.part_ml;
+  p.whole_out = a.out32;
+  p.whole_lse = a.lse;
+  p.G = a.G;
+  p.R = R;
+  p.NH = a.NH;
+  p.group = a.group;
+  p.head_tiles = a.head_tiles;
+  p.gw = a.gw;
+  return p;
+}
+
+// Workgroup i of a planned pass takes units [i units / G, (i + 1) units / G).
+struct Parts {
+  int64_t units, u0;   // units of the pass; the row's first
+  int i0, i1;          // workgroups that share the row
+  int r;               // its row of their tiles
+};
+__device__ __forceinline__ Parts parts_of(const Pass& p, int64_t t, int head) {
+  Parts x;
+  const PlanEntry e = p.plan[t];
+  const int in = head % p.group;
+  const int hh = head / p.group * p.head_tiles + in / p.gw;
+  x.units = *p.plan_total * p.NH;
+  x.u0 = e.first * p.NH + (int64_t)hh * e.tiles;
+  x.r = (int)(t - e.t0) * p.gw + in % p.gw;
+  x.i0 = (int)(((x.u0 + 1) * p.G - 1) / x.units);
+  x.i1 = (int)(((x.u0 + e.tiles) * p.G - 1) / x.units);
+  return x;
+}
+
 // One row's parts: out = sum_i 2^(m_i - M) o_i over the same of the sums. A
 // workgroup takes one row; D / 4 lanes add up every (1024 / D)-th part, and the
-// groups' sums are added in a fixed order. A row that one workgroup of the
-// attention finished by itself is left alone.
-template <bool HALF, int D>
-__global__ __launch_bounds__(256) void attend_join_kernel(AttendArgs a, int R) {
+// groups' sums are added in a fixed order. TWO passes over different keys give
+// their parts, or a whole row each (one part with m = lse and a sum of one). With
+// one pass a row that one workgroup of the attention finished is left alone.
+template <bool HALF, int D, bool TWO>
+__global__ __launch_bounds__(256) void attend_join_kernel(Pass pa, Pass pb, int Hq, uint16_t* out, float* lse) {
   constexpr int LPR = D / 4, GR = 256 / LPR;
   __shared__ float weight[256];
   __shared__ float wsum[4], wmax[4];
   __shared__ floatx4 acc[256];
   const int64_t row = blockIdx.x;
   const int tid = threadIdx.x;
-  const int64_t t = row / a.Hq;
-  const int head = (int)(row - t * a.Hq);
-  const PlanEntry e = a.plan[t];
-  const int64_t units = *a.plan_total * a.NH, G = a.G;
-  const int in = head % a.group;
-  const int hh = head / a.group * a.head_tiles + in / a.gw;
-  const int r = (int)(t - e.t0) * a.gw + in % a.gw;
-  const int64_t u0 = e.first * a.NH + (int64_t)hh * e.tiles, u1 = u0 + e.tiles;
-  // workgroup i takes units [i units / G, (i + 1) units / G)
-  const int i0 = (int)(((u0 + 1) * G - 1) / units), i1 = (int)((u1 * G - 1) / units);
-  if (i0 == i1) return;
+  const int64_t t = row / Hq;
+  const int head = (int)(row - t * Hq);
   float M = -__builtin_inff(), sum = 0.f;
   floatx4 o = {0.f, 0.f, 0.f, 0.f};
   const int g = tid / LPR, d0 = (tid % LPR) * 4;
-  for (int base = i0; base <= i1; base += 256) {
-    // maxima and sums of up to 256 parts
-    const int i = base + tid;
-    float m = -__builtin_inff(), s = 0.f;
-    if (i <= i1) {
-      const int64_t b = i * units / G;
-      if (b != ((int64_t)i + 1) * units / G) {
-        const float* ml = a.part_ml + ((2 * (int64_t)i + (b > u0 ? 0 : 1)) * R + r) * 2;
-        m = ml[0];
-        s = ml[1];
+#pragma unroll
+  for (int which = 0; which < (TWO ? 2 : 1); ++which) {
+    const Pass& p = which ? pb : pa;
+    Parts x;
+    x.i0 = x.i1 = 0;
+    if (p.plan) x = parts_of(p, t, head);
+    if (x.i0 == x.i1) {
+      if (!TWO) return;
+      const float l = p.whole_lse[row];
+      if (l == -__builtin_inff()) continue;
+      const float m = l * attend::kLog2e;
+      const float top = fmaxf(M, m);
+      const float old = __builtin_amdgcn_exp2f(M - top), w = l == l ? __builtin_amdgcn_exp2f(m - top) : l;
+      sum = sum * old + w;
+      const floatx4 y = *reinterpret_cast<const floatx4*>(p.whole_out + row * D + d0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = o[j] * old + (g == 0 ? y[j] * w : 0.f);
+      M = top;
+      continue;
+    }
+    const int64_t G = p.G;
+    for (int base = x.i0; base <= x.i1; base += 256) {
+      // maxima and sums of up to 256 parts
+      const int i = base + tid;
+      float m = -__builtin_inff(), s = 0.f;
+      if (i <= x.i1) {
+        const int64_t b = i * x.units / G;
+        if (b != ((int64_t)i + 1) * x.units / G) {
+          const float* ml = p.part_ml + ((2 * (int64_t)i + (b > x.u0 ? 0 : 1)) * p.R + x.r) * 2;
+          m = ml[0];
+          s = ml[1];
+        }
       }
-    }
-    float wm = m;
+      float wm = m;
 #pragma unroll
-    for (int off = 32; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor(wm, off, 64));
-    if ((tid & 63) == 0) wmax[tid >> 6] = wm;
-    __syncthreads();
-    const float top = fmaxf(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), M);
-    const float ref = top == -__builtin_inff() ? 0.f : top;
-    const float w = __builtin_amdgcn_exp2f(m - ref);
-    weight[tid] = w;
-    s = wave_sum(s * w);
-    if ((tid & 63) == 0) wsum[tid >> 6] = s;
-    const float old = __builtin_amdgcn_exp2f(M - ref);
-    M = top;
-    __syncthreads();
-    sum = sum * old + wsum[0] + wsum[1] + wsum[2] + wsum[3];
+      for (int off = 32; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor(wm, off, 64));
+      if ((tid & 63) == 0) wmax[tid >> 6] = wm;
+      __syncthreads();
+      const float top = fmaxf(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), M);
+      const float ref = top == -__builtin_inff() ? 0.f : top;
+      const float w = __builtin_amdgcn_exp2f(m - ref);
+      weight[tid] = w;
+      s = wave_sum(s * w);
+      if ((tid & 63) == 0) wsum[tid >> 6] = s;
+      const float old = __builtin_amdgcn_exp2f(M - ref);
+      M = top;
+      __syncthreads();
+      sum = sum * old + wsum[0] + wsum[1] + wsum[2] + wsum[3];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] *= old;
-    const int n = min(256, i1 - base + 1);
-#pragma unroll 4
-    for (int k = g; k < n; k += GR) {
-      const float wk = weight[k];
+      for (int j = 0; j < 4; ++j) o[j] *= old;
+      const int n = min(256, x.i1 - base + 1);
       // only the row's first part can be its workgroup's second (see Part::slot)
-      const int64_t slot = 2 * ((int64_t)base + k) + (base + k == i0 && i0 * units / G <= u0 ? 1 : 0);
-      if (wk == 0.f) continue;   // no part, or one without a key
-      const floatx4 x = *reinterpret_cast<const floatx4*>(a.part_out + (slot * R + r) * D + d0);
+      const int second = base == x.i0 && x.i0 * x.units / G <= x.u0 ? 0 : -1;
+#pragma unroll 4
+      for (int k = g; k < n; k += GR) {
+        const float wk = weight[k];
+        if (wk == 0.f) continue;   // no part, or one without a key
+        const int64_t slot = 2 * ((int64_t)base + k) + (k == second ? 1 : 0);
+        const floatx4 y = *reinterpret_cast<const floatx4*>(p.part_out + (slot * p.R + x.r) * D + d0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] += x[j] * wk;
+        for (int j = 0; j < 4; ++j) o[j] += y[j] * wk;
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   acc[tid] = o;
   __syncthreads();
   if (g > 0) return;
 #pragma unroll
   for (int k = 1; k < GR; ++k) o += acc[k * LPR + tid];
+  AttendArgs a{};
+  a.out = out;
+  a.lse = lse;
   attend::write_row<HALF, D>(a, row, d0, M, sum, o);
 }
 
 template <int D>
 int per_cu(int R) {
   switch (R) {
-    case 16: return Shape<D, 16>::per_cu;
+    case 16:
+      if constexpr (D < 256) return Shape<D, 16>::per_cu;
+      break;
     case 32: return Shape<D, 32>::per_cu;
     case 64: return Shape<D, 64>::per_cu;
   }
@@ -99,10 +165,10 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-int attend_rows(int64_t T, int64_t nseq, int group, bool single) {
+int attend_rows(int64_t T, int64_t nseq, int group, int d, bool single) {
   const int64_t each = single ? 1 : (T + nseq - 1) / nseq;
   const int64_t rows = each * group;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  return rows <= 16 && d < 256 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
 bool attend_planned(int64_t T) { return T <= kPlanMax; }
@@ -172,9 +238,19 @@ hipError_t launch_attend(const AttendArgs& a, int R, bool half, hipStream_t st) 
   if (a.d == 64) e = launch_attend_d64(a, R, half, blocks, st);
   if (a.d == 128) e = launch_attend_d128(a, R, half, blocks, st);
   if (a.d == 256) e = launch_attend_d256(a, R, half, blocks, st);
-  if (e != hipSuccess || !a.planned) return e;
+  return e;
+}
+
+hipError_t launch_attend_join(const AttendArgs& a, int Ra, const AttendArgs* b, int Rb, uint16_t* out, float* lse,
+                              bool half, hipStream_t st) {
+  if (!b && !a.planned) return hipSuccess;
+  const Pass pa = pass_of(a, Ra), pb = b ? pass_of(*b, Rb) : pa;
   const dim3 grid((unsigned)(a.T * a.Hq));
-#define MISA_JOIN(HALF_, D_) hipLaunchKernelGGL((attend_join_kernel<HALF_, D_>), grid, dim3(256), 0, st, a, R)
+#define MISA_JOIN(HALF_, D_)                                                                                     \
+  do {                                                                                                           \
+    if (b) hipLaunchKernelGGL((attend_join_kernel<HALF_, D_, true>), grid, dim3(256), 0, st, pa, pb, a.Hq, out, lse);  \
+    else hipLaunchKernelGGL((attend_join_kernel<HALF_, D_, false>), grid, dim3(256), 0, st, pa, pb, a.Hq, out, lse);   \
+  } while (0)
   if (a.d == 64) { if (half) MISA_JOIN(true, 64); else MISA_JOIN(false, 64); }
   if (a.d == 128) { if (half) MISA_JOIN(true, 128); else MISA_JOIN(false, 128); }
   if (a.d == 256) { if (half) MISA_JOIN(true, 256); else MISA_JOIN(false, 256); }

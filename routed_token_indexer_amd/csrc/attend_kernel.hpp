@@ -22,9 +22,9 @@
 // transposing LDS reads (ds_read_b64_tr_b16: 16 lanes read a 4 x 16 block of
 // 16-bit values and each gets one column).
 //
-// Keys and values go through LDS in two buffers: while one is used, the next
-// tile's rows are on their way into registers and the page ids of the tile
-// after it are looked up. The 16-byte pieces of a row are permuted by the row's
+// Keys and values go through LDS: while one tile is used, the next one's rows
+// are on their way into registers and the page ids of the tile after it are
+// looked up. The 16-byte pieces of a row are permuted by the row's
 // low bits (swizzle) so that neither the row-wise nor the transposing reads
 // meet in a bank.
 //
@@ -79,20 +79,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 // Tile shapes. NK keys per group of waves and step; KT = KW * NK keys a step.
+// With RW = 1 a wave's keys are its own: one LDS buffer and no barrier in the
+// loop. Otherwise the RW waves of a group share them, in two buffers.
 template <int D, int R>
 struct Shape {
-  static constexpr int MR = R == 16 ? 16 : 32;
-  static constexpr int RW = R <= 32 ? 1 : R / 32;
-  static constexpr int KW = D == 256 ? (R <= 32 ? 2 : 1) : (R <= 32 ? 4 : (R == 64 ? 2 : 1));
+  static_assert(D < 256 || R > 16, "head dimension 256 takes tiles of 32 rows and more");
+  static constexpr int MR = R == 16 || (D == 256 && R == 32) ? 16 : 32;
+  static constexpr int RW = R / MR;
+  static constexpr int KW = RW >= 4 ? 1 : 4 / RW;
   static constexpr int NK = D == 256 ? 32 : (D == 128 ? (R == 128 ? 64 : 32) : 64);
   static constexpr int KT = KW * NK;
   static constexpr int threads = 64 * RW * KW;
+  static constexpr int buffers = RW == 1 ? 1 : 2;
   static constexpr int stage_bytes = KT * D * 2 * 2;
   // the keys' waves join their sums through LDS: rows of D + 4 floats
   static constexpr int merge_bytes = KW > 1 ? KW * R * (D + 4) * 4 + KW * R * 8 + R * 8 : 0;
-  static constexpr int lds_bytes = 2 * stage_bytes > merge_bytes ? 2 * stage_bytes : merge_bytes;
-  // workgroups that fit a CU (160 KiB of LDS, the plan's share included)
-  static constexpr int per_cu = D < 256 && (lds_bytes + kPlanMax * 8 + 64) * 2 <= 160 * 1024 ? 2 : 1;
+  static constexpr int lds_bytes = buffers * stage_bytes > merge_bytes ? buffers * stage_bytes : merge_bytes;
+  // workgroups that fit a CU (160 KiB of LDS, the plan's share included, and 512
+  // registers a SIMD)
+  static constexpr int per_cu = D < 256 && (lds_bytes + kPlanMax * 20 + 64) * 2 <= 160 * 1024 ? 2 : 1;
 };
 
 // 16-byte piece c of row r lies at piece c ^ swizzle(r) of its row in LDS. The
@@ -106,6 +111,9 @@ __device__ __forceinline__ int swizzle(int r) {
 
 // Zeros that stand in for a row without a key.
 static __device__ __align__(16) const uint32_t kZeroRow[128] = {};
+
+// A row unit that stands for no key: beyond every buffer view, its pieces included.
+constexpr uint32_t kNoRow = 0xffff8000u;
 
 struct QueryInfo {
   int seq;        // row of the table, -1: none
@@ -185,21 +193,41 @@ __device__ __forceinline__ int wave_max_of(int v) {
   return v;
 }
 
+// Sequence and interval of the queries of a planned batch, in LDS.
+struct Interval {
+  int seq, lo, hi;
+};
+__device__ __forceinline__ Interval interval_of(const AttendArgs& a, const Interval* known, int64_t t) {
+  if (known) return known[t];
+  const QueryInfo q = query_info(a, t);
+  return Interval{q.seq, q.lo, q.hi};
+}
+
 // Sequence and span of the visible keys of queries t0 .. t0 + nq - 1 (one sequence).
 struct Span {
   int seq, lo, hi;   // keys that any of them sees lie in [lo, hi)
   int some;          // keys that all of them see
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t t0, int nq) {
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const Interval* known, int64_t t0, int nq) {
   const int lane = threadIdx.x & 63;
+  Span s;
+  if (nq == 1) {
+    const Interval r = interval_of(a, known, t0);
+    s.seq = uniform(r.seq);
+    s.lo = uniform(r.lo);
+    s.hi = uniform(r.hi);
+    if (a.idx) {
+      s.hi = s.hi > s.lo ? a.topk : 0;
+      s.lo = 0;
+    }
+    if (s.hi <= s.lo) s.lo = s.hi = 0;
+    s.some = s.hi - s.lo;
+    return s;
+  }
   int lo = 0x7fffffff, hi = 0, seq = -1, all_lo = 0, all_hi = 0x7fffffff;
   for (int i = lane; i < nq; i += 64) {
-    QueryInfo r = query_info(a, t0 + i);
+    const Interval r = interval_of(a, known, t0 + i);
     seq = max(seq, r.seq);
-    if (a.idx) {
-      r.hi = r.hi > r.lo ? a.topk : 0;
-      r.lo = 0;
-    }
     if (r.hi > r.lo) {
       lo = min(lo, r.lo);
       hi = max(hi, r.hi);
@@ -207,7 +235,6 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t t0, int nq)
     all_lo = max(all_lo, r.lo);
     all_hi = min(all_hi, r.hi);
   }
-  Span s;
   s.seq = uniform(wave_max_of(seq));
   s.lo = uniform(wave_min_of(lo));
   s.hi = uniform(wave_max_of(hi));
@@ -216,17 +243,15 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, int64_t t0, int nq)
   return s;
 }
 
-// Caps up to this one take tanh(y) = 1 - 2 / (1 + e^2y) as it stands: exp2, the
-// sum and the reciprocal lose at most 8 half steps of fp32 of one, times the cap
-// (3e-5 of a score at the limit). Larger ones take the series
-// y (1 - y^2 / 3 + 2 y^4 / 15 - 17 y^6 / 315) below 1/8, where the difference
-// would cancel; its first left-out term is 62 y^8 / 2835 < 1.4e-9 of the value.
-constexpr float kPlainCap = 256.f;
+// tanh(y) for |y| <= 1/2 as y times a polynomial in y^2, fitted to 2.8e-8 of the
+// value; c4 .. c0 are its coefficients.
+constexpr float kTanh[5] = {1.f, -0.33333072066307f, 0.13324829936f, -0.05298925563693f, 0.017141323536634f};
 
-__device__ __forceinline__ float tanh_small(float y) {
-  const float y2 = y * y;
-  return y * (1.f + y2 * (-1.f / 3.f + y2 * (2.f / 15.f - y2 * (17.f / 315.f))));
-}
+// Caps up to this one take 1 - 2 / (1 + e^2y) beyond |y| = 1/2 and, in a tile that
+// has such scores, for the others too: exp2, the sum and the reciprocal lose at
+// most 9 half steps of fp32 of one, times the cap (1.4e-4 of a score at the
+// limit, 3e-5 at 50). Larger caps choose for each score.
+constexpr float kPlainCap = 256.f;
 
 // A finished row: sums relative to 2^m (m in units of log2) to the result and its log-sum.
 template <bool HALF, int D>
@@ -283,10 +308,11 @@ struct Kernel {
   // entry of its page, and its row. A load is issued in one step and used in the
   // next, so none is waited for.
   struct Keys {
-    int token;      // -1: none
+    int token;        // -1: none
+    int within;       // its row of the page
     int page;
   };
-  // token of the lane's key s + lane (not before `end`; selected ids still unchecked)
+  // token of the lane's key s + lane (before `end`; selected ids still unchecked)
   __device__ static __forceinline__ int token_of(const int32_t* ids, int s, int end) {
     const int lane = threadIdx.x & 63;
     const int at = s + lane;
@@ -295,39 +321,65 @@ struct Kernel {
     const int id = ids[min(at, end - 1)];
     return in ? id : -1;
   }
-  __device__ static __forceinline__ Keys page_of(const AttendArgs& a, const Span& sp, int token, int lo, int hi) {
+  __device__ static __forceinline__ Keys page_of(const KvView& kv, const int32_t* table, int seq, int token, int lo, int hi) {
     Keys k;
     k.token = token >= lo && token < hi ? token : -1;
-    if (!a.kv.table) {
-      k.page = sp.seq;
-    } else {
-      const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)max(k.token, 0));
-      k.page = a.kv.table[(int64_t)sp.seq * a.kv.table_stride + col];
-    }
+    const uint32_t t = (uint32_t)max(k.token, 0);
+    const uint32_t col = fast_quot(kv.by_page, t);
+    k.within = (int)(t - col * (uint32_t)kv.page);
+    k.page = table ? table[col] : seq;
     return k;
   }
-  __device__ static __forceinline__ bool is_key(const AttendArgs& a, const Keys& k) {
-    return k.token >= 0 && k.page >= 0 && k.page < a.kv.npages;
-  }
-  // element offset of the row; -1: none
-  __device__ static __forceinline__ int64_t row_offset(const AttendArgs& a, const Keys& k, int64_t head_off) {
-    const uint32_t col = fast_quot(a.kv.by_page, (uint32_t)max(k.token, 0));
-    const int64_t at = (int64_t)k.page * a.kv.page_stride + (int64_t)(k.token - (int)col * a.kv.page) * a.kv.tok_stride + head_off;
-    return is_key(a, k) ? at : -1;
+  // where the row lies, in the view's units; kNoRow: no key
+  __device__ static __forceinline__ uint32_t row_unit(const KvView& kv, const Keys& k) {
+    const uint32_t at = (uint32_t)k.page * kv.page_units + (uint32_t)k.within * kv.tok_units;
+    return k.token >= 0 && (uint32_t)k.page < (uint32_t)kv.npages ? at : kNoRow;
   }
 
-  __device__ static __forceinline__ void load_rows(const AttendArgs& a, int64_t off, int rw, u32x4 (&kr)[NLD],
-                                                   u32x4 (&vr)[NLD]) {
+  // Bases of one kv head's rows. Caches of less than 4 GiB (to the last row) are
+  // read through buffer views with 32-bit byte offsets, whose range check gives
+  // zeros for kNoRow; others by 64-bit addresses, with zeros kept for such rows.
+  struct Bases {
+    const uint16_t *k, *v;
+    __amdgpu_buffer_rsrc_t kb, vb;
+    uint32_t shift;   // 64-bit addresses: log2 of a unit's elements; 0: byte offsets
+  };
+  __device__ static __forceinline__ Bases bases_of(const KvView& kv, int kvh) {
+    const int64_t off = (int64_t)kvh * kv.head_stride;
+    Bases b;
+    b.k = kv.k + off;
+    b.v = kv.v + off;
+    b.shift = kv.unit_shift;
+    const uint32_t bytes = kv.unit_shift ? 0u : (uint32_t)(kv.bytes - off * 2);
+    b.kb = buffer_view(b.k, bytes);
+    b.vb = buffer_view(b.v, bytes);
+    return b;
+  }
+  __device__ static __forceinline__ u32x4 buffer_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+  }
+
+  __device__ static __forceinline__ void load_rows(const Bases& b, uint32_t unit, int rw, u32x4 (&kr)[NLD], u32x4 (&vr)[NLD]) {
     const int lane = threadIdx.x & 63;
-    const int lo = (int)(uint32_t)off, hi = (int)(off >> 32);
+    if (b.shift == 0) {
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-      const int row = (rw * NLD + i) * RPI + lane / LPR;
-      const int64_t o = (int64_t)(uint32_t)__shfl(lo, row, 64) | (int64_t)__shfl(hi, row, 64) << 32;
-      const int c = 8 * ((lane % LPR) ^ swizzle<D>(row));
-      const uint16_t* z = reinterpret_cast<const uint16_t*>(kZeroRow);
-      kr[i] = *reinterpret_cast<const u32x4*>((o >= 0 ? a.kv.k + o : z) + c);
-      vr[i] = *reinterpret_cast<const u32x4*>((o >= 0 ? a.kv.v + o : z) + c);
+      for (int i = 0; i < NLD; ++i) {
+        const int row = (rw * NLD + i) * RPI + lane / LPR;
+        const uint32_t at = (uint32_t)__shfl((int)unit, row, 64) + 16 * ((lane % LPR) ^ swizzle<D>(row));
+        kr[i] = buffer_row(b.kb, at);
+        vr[i] = buffer_row(b.vb, at);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NLD; ++i) {
+        const int row = (rw * NLD + i) * RPI + lane / LPR;
+        const uint32_t u = (uint32_t)__shfl((int)unit, row, 64);
+        const int c = 8 * ((lane % LPR) ^ swizzle<D>(row));
+        const uint16_t* z = reinterpret_cast<const uint16_t*>(kZeroRow);
+        const uint64_t at = (uint64_t)u << b.shift;
+        kr[i] = *reinterpret_cast<const u32x4*>((u != kNoRow ? b.k + at : z) + c);
+        vr[i] = *reinterpret_cast<const u32x4*>((u != kNoRow ? b.v + at : z) + c);
+      }
     }
   }
   __device__ static __forceinline__ void store_rows(uint16_t* ks, uint16_t* vs, int rw, const u32x4 (&kr)[NLD],
@@ -338,6 +390,17 @@ struct Kernel {
       const int at = (rw * NLD + i) * RPI * D + lane * 8;
       *reinterpret_cast<u32x4*>(ks + at) = kr[i];
       *reinterpret_cast<u32x4*>(vs + at) = vr[i];
+    }
+  }
+
+  // Orders the LDS accesses of the waves that share rows: a barrier, or, within
+  // one wave (whose LDS instructions run in order), the compiler's alone.
+  __device__ static __forceinline__ void sync_rows() {
+    if constexpr (RW > 1) {
+      __syncthreads();
+    } else {
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
     }
   }
 
@@ -467,23 +530,44 @@ struct Kernel {
   __device__ static __forceinline__ void shape(const AttendArgs& a, Acc (&s)[ST], const Rows& row, const int32_t* ids, int base,
                                                int token) {
     const int lane = threadIdx.x & 63;
-    if (a.cap > 0.f && a.cap <= kPlainCap) {
-      const float c = a.scale / a.cap * (2.f * kLog2e), cap2 = a.cap * kLog2e;
-#pragma unroll
-      for (int i = 0; i < ST; ++i)
-#pragma unroll
-        for (int j = 0; j < AR; ++j)
-          s[i][j] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[i][j] * c));
-    } else if (a.cap > 0.f) {
+    if (a.cap > 0.f) {
       const float c = a.scale / a.cap, cap2 = a.cap * kLog2e;
+      float big = 0.f;
 #pragma unroll
       for (int i = 0; i < ST; ++i)
 #pragma unroll
-        for (int j = 0; j < AR; ++j) {
-          const float y = s[i][j] * c;
-          const float big = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * (2.f * kLog2e)));
-          s[i][j] = cap2 * (fabsf(y) < 0.125f ? tanh_small(y) : big);
-        }
+        for (int j = 0; j < AR; ++j) big = fmaxf(big, fabsf(s[i][j]));
+      const float g = cap2 * c, c2 = c * c;
+      const float k0 = g * kTanh[0], k1 = g * kTanh[1] * c2, k2 = g * kTanh[2] * c2 * c2, k3 = g * kTanh[3] * c2 * c2 * c2,
+                  k4 = g * kTanh[4] * c2 * c2 * c2 * c2;
+      // coefficients of powers of the raw score stay normal numbers for |c| in this range
+      const bool mild = c > 1e-4f && c < 1e4f;
+      if (mild && !__any(!(big * c <= 0.5f))) {
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j) {
+            const float x = s[i][j], z = x * x;
+            s[i][j] = x * (k0 + z * (k1 + z * (k2 + z * (k3 + z * k4))));
+          }
+      } else if (a.cap <= kPlainCap) {
+        const float e = c * (2.f * kLog2e);
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j)
+            s[i][j] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[i][j] * e));
+      } else {
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j) {
+            const float y = s[i][j] * c, z = y * y;
+            const float far = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * (2.f * kLog2e)));
+            const float near = y * (kTanh[0] + z * (kTanh[1] + z * (kTanh[2] + z * (kTanh[3] + z * kTanh[4]))));
+            s[i][j] = cap2 * (fabsf(y) < 0.5f ? near : far);
+          }
+      }
     } else {
       const float c = a.scale * kLog2e;
 #pragma unroll
@@ -500,16 +584,19 @@ struct Kernel {
         for (int j = 0; j < AR; ++j)
           s[i][j] -= slope * fabsf((float)(row.pos - __shfl(token, i * MR + acc_row(j, lane), 64)));
     } else {
-      // distances of consecutive keys; exact in fp32 up to 2^24
-      const float first = (float)(row.pos - base - acc_row(0, lane));
-      const bool far = row.pos >= (1 << 23) || row.pos < -(1 << 23) || base >= (1 << 23);
+      const int first = row.pos - base - acc_row(0, lane);
+      if (__any(first > (1 << 23) || first < -(1 << 23))) {
 #pragma unroll
-      for (int i = 0; i < ST; ++i)
+        for (int i = 0; i < ST; ++i)
 #pragma unroll
-        for (int j = 0; j < AR; ++j) {
-          const int key = i * MR + acc_row(j, 0);
-          s[i][j] -= slope * fabsf(far ? (float)(row.pos - base - acc_row(0, lane) - key) : first - (float)key);
-        }
+          for (int j = 0; j < AR; ++j) s[i][j] -= slope * fabsf((float)(first - (i * MR + acc_row(j, 0))));
+      } else {   // differences that fp32 holds exactly
+        const float f = (float)first;
+#pragma unroll
+        for (int i = 0; i < ST; ++i)
+#pragma unroll
+          for (int j = 0; j < AR; ++j) s[i][j] -= slope * fabsf(f - (float)(i * MR + acc_row(j, 0)));
+      }
     }
   }
 
@@ -556,13 +643,14 @@ struct Kernel {
   // that do not see it (0 * inf). Where the queries of a part do not see the same
   // keys (odd is not null) and anything comes out infinite or NaN, *odd is set
   // and the guarded form computes the workgroup's parts again.
-  __device__ static __forceinline__ void run_part(ArgPtr ap, const Part& p, unsigned char* lds, int* odd) {
+  __device__ static __forceinline__ void run_part(ArgPtr ap, const Part& p, unsigned char* lds, const Interval* known,
+                                                  int* odd) {
     const AttendArgs& a = fresh(ap);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = wave % RW, kw = wave / RW;
     const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
-    const Span sp = span_of(a, p.t0, p.nq);
+    const Span sp = span_of(a, known, p.t0, p.nq);
     // p.tile1 * KT may pass the last key (and 2^31): 64 bits
     const int begin = sp.lo + p.tile0 * KT;
     const int end = (int)min((int64_t)sp.hi, sp.lo + (int64_t)p.tile1 * KT);
@@ -579,23 +667,21 @@ struct Kernel {
     row.slope = 0.f;
     row.pos = 0;
     if (row.active) {
-      const QueryInfo q = query_info(a, row.t);
-      row.pos = q.pos - q.kbase;
-      if (a.idx) {
-        row.lo = 0;
-        row.hi = a.topk;
-      } else {
-        row.lo = q.lo;
-        row.hi = q.hi;
+      const Interval q = interval_of(a, known, row.t);
+      row.lo = a.idx ? 0 : q.lo;
+      row.hi = a.idx ? a.topk : q.hi;
+      if (EXTRA && a.slopes) {
+        const QueryInfo z = query_info(a, row.t);
+        row.slope = a.slopes[row.head];
+        row.pos = z.pos - z.kbase;
       }
-      if (EXTRA && a.slopes) row.slope = a.slopes[row.head];
     }
     // visible token ids of selected tokens (one query a segment; also for waves
     // without a row, which load for the others)
     const int32_t* ids = nullptr;
     int id_lo = 0, id_hi = 0x7fffffff;
     if (a.idx) {
-      const QueryInfo q = query_info(a, p.t0);
+      const Interval q = interval_of(a, known, p.t0);
       ids = a.idx + p.t0 * a.topk;
       id_lo = uniform(q.lo);
       id_hi = uniform(q.hi);
@@ -622,64 +708,57 @@ struct Kernel {
     for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int j = 0; j < AR; ++j) o[i][j] = 0.f;
-    if (a.init_out && kw == 0 && p.tile0 == 0 && row.active) {
-      const int64_t at = row.t * a.Hq + row.head;
-      const float l = a.init_lse[at];
-      if (l > -__builtin_inff() || l != l) {
-        m = l * kLog2e;
-        sum = lane < MR ? 1.f : 0.f;
-#pragma unroll
-        for (int i = 0; i < OT; ++i)
-#pragma unroll
-          for (int j = 0; j < AR; j += 4) {
-            const floatx4 x = *reinterpret_cast<const floatx4*>(a.init_out + at * D + i * MR + acc_row(j, lane));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][j + e] = x[e];
-          }
-      }
-    }
     const float sc = EXTRA ? 1.f : a.scale * kLog2e;
-    if (!EXTRA) m = m / sc;   // in units of the raw scores while the keys are read
 
     uint16_t* buf = reinterpret_cast<uint16_t*>(lds);
     constexpr int GB = NK * D;             // elements of one tensor of one group's step
     constexpr int SB = KW * 2 * GB;        // of one buffer
-    const int64_t head_off = (int64_t)kvh * a.kv.head_stride;
+    const Bases bases = bases_of(a.kv, kvh);
+    const int32_t* table = a.kv.table ? a.kv.table + (int64_t)max(sp.seq, 0) * a.kv.table_stride : nullptr;
     const int k0 = begin + kw * NK;
+    // steps of this wave: its own where no other shares its keys
+    const int mine = RW > 1 ? steps : (end > k0 ? (end - k0 + KT - 1) / KT : 0);
     u32x4 kr[NLD], vr[NLD];
-    Keys cur, nxt;
-    int far = -1;
-    cur.token = nxt.token = -1;
-    cur.page = nxt.page = 0;
-    if (steps > 0) {
-      cur = page_of(a, sp, token_of(ids, k0, end), id_lo, id_hi);
-      nxt = page_of(a, sp, token_of(ids, k0 + KT, end), id_lo, id_hi);
+    Keys nxt;
+    nxt.token = -1;
+    nxt.within = nxt.page = 0;
+    int far = -1, cur_token = -1;
+    uint64_t valid = 0;
+    if (mine > 0) {
+      const Keys cur = page_of(a.kv, table, sp.seq, token_of(ids, k0, end), id_lo, id_hi);
+      nxt = page_of(a.kv, table, sp.seq, token_of(ids, k0 + KT, end), id_lo, id_hi);
       far = token_of(ids, k0 + 2 * KT, end);
-      load_rows(a, row_offset(a, cur, head_off), rw, kr, vr);
+      const uint32_t unit = row_unit(a.kv, cur);
+      load_rows(bases, unit, rw, kr, vr);
+      valid = __ballot(unit != kNoRow);
+      cur_token = cur.token;
       store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
     }
     // the loop's first products wait for these loads here, not for its own
 #pragma unroll
     for (int f = 0; f < QF; ++f) asm volatile("" : "+v"(qf[f]));
-    __syncthreads();
-    for (int it = 0; it < steps; ++it) {
-      const bool more = it + 1 < steps;
-      Keys after;
-      after.token = -1;
-      after.page = 0;
+    // the maximum is followed lazily: the reference m moves when a row's maximum
+    // passes it by more than 2^8, so that rescaling is rare after the first step
+    const float slack = 8.f / sc;
+    sync_rows();
+    for (int it = 0; it < mine; ++it) {
+      const bool more = it + 1 < mine;
+      uint64_t next_valid = 0;
+      int next_token = -1;
       if (more) {
-        const int64_t off = row_offset(a, nxt, head_off);
-        after = page_of(a, sp, far, id_lo, id_hi);
+        const uint32_t unit = row_unit(a.kv, nxt);
+        next_valid = __ballot(unit != kNoRow);
+        next_token = nxt.token;
+        nxt = page_of(a.kv, table, sp.seq, far, id_lo, id_hi);
         far = token_of(ids, k0 + (it + 3) * KT, end);
-        load_rows(a, off, rw, kr, vr);
+        load_rows(bases, unit, rw, kr, vr);
       }
-      const uint16_t* ks = buf + (it & 1) * SB + kw * 2 * GB;
+      const uint16_t* ks = buf + (S::buffers > 1 ? (it & 1) * SB : 0) + kw * 2 * GB;
       const int base = k0 + it * KT;
-      const uint64_t valid = __ballot(is_key(a, cur));
       if (base < any_hi && base + NK > any_lo && valid != 0) {
         Acc s[ST];
         score(ks, qf, s);
-        if constexpr (EXTRA) shape(a, s, row, ids, base, cur.token);
+        if constexpr (EXTRA) shape(a, s, row, ids, base, cur_token);
         constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK & 63)) - 1;
         if (!(valid == kAll && base >= all_lo && base + NK <= all_hi))
           hide(valid & bits_from(row.lo - base) & ~bits_from(row.hi - base), s);
@@ -689,10 +768,9 @@ struct Kernel {
 #pragma unroll
           for (int j = 0; j < AR; ++j) mx = fmaxf(mx, s[i][j]);
         mx = over_rows_max(mx);
-        const float mn = fmaxf(m, mx);
-        const float ref = mn == -__builtin_inff() ? 0.f : mn;
-        if (__any(mn > m)) {
-          const float alpha = __builtin_amdgcn_exp2f((m - ref) * sc);
+        if (__any(mx > m + slack)) {
+          const float mn = fmaxf(m, mx);
+          const float alpha = __builtin_amdgcn_exp2f((m - (mn == -__builtin_inff() ? 0.f : mn)) * sc);
           sum *= alpha;
 #pragma unroll
           for (int i = 0; i < OT; ++i)
@@ -700,26 +778,27 @@ struct Kernel {
             for (int j = 0; j < AR; ++j) o[i][j] *= alpha;
           m = mn;
         }
-        const float off = ref * sc;
-        float add = 0.f;
+        const float off = (m == -__builtin_inff() ? 0.f : m) * sc;
+        float add[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < ST; ++i)
 #pragma unroll
           for (int j = 0; j < AR; ++j) {
             s[i][j] = __builtin_amdgcn_exp2f(s[i][j] * sc - off);
-            add += s[i][j];
+            add[j & 1] += s[i][j];
           }
-        sum += add;
+        sum += add[0] + add[1];
         if constexpr (GUARD) accumulate_guarded(ks + GB, s, o, base, row.lo, row.hi, valid);
         else accumulate(ks + GB, s, o);
       }
-      cur = nxt;
-      nxt = after;
+      valid = next_valid;
+      cur_token = next_token;
+      if (S::buffers == 1) sync_rows();   // this wave has read what it now overwrites
       if (more) {
-        uint16_t* to = buf + ((it + 1) & 1) * SB + kw * 2 * GB;
+        uint16_t* to = buf + (S::buffers > 1 ? ((it + 1) & 1) * SB : 0) + kw * 2 * GB;
         store_rows(to, to + GB, rw, kr, vr);
       }
-      __syncthreads();
+      sync_rows();
     }
     finish(fresh(ap), p, sp, lds, odd, row, r, kw, rw, m * sc, sum, o);
   }
@@ -755,6 +834,7 @@ struct Kernel {
       float* ob = reinterpret_cast<float*>(lds);             // [KW][R][D + 4]
       float* ml = ob + KW * R * (D + 4);                     // [KW][R][2]
       float* fin = ml + KW * R * 2;                          // [R][2]
+      __syncthreads();   // every wave is done with its rows
       if (lane < MR) {
         ml[(kw * R + r) * 2] = m;
         ml[(kw * R + r) * 2 + 1] = sum;
@@ -794,24 +874,27 @@ struct Kernel {
   }
 
   // Queries from t0 on that belong to t0's sequence and row tile.
-  __device__ static __forceinline__ int run_length(const AttendArgs& a, int64_t t0) {
+  __device__ static __forceinline__ int run_length(const AttendArgs& a, const Interval* known, int64_t t0) {
     const int lane = threadIdx.x & 63;
     int64_t end = (t0 / a.qt + 1) * a.qt;
     if (end > a.T) end = a.T;
     const int n = (int)(end - t0);
     if (n <= 1) return n;
-    const int seq = query_info(a, t0).seq;
+    const int seq = interval_of(a, known, t0).seq;
     for (int i = 0; i < n; i += 64) {
-      const bool other = i + lane < n && query_info(a, t0 + i + lane).seq != seq;
+      const bool other = i + lane < n && interval_of(a, known, t0 + i + lane).seq != seq;
       const uint64_t b = __ballot(other);
       if (b) return __builtin_amdgcn_readfirstlane(i + (int)__builtin_ctzll(b));
     }
     return n;
   }
 
-  // Key tiles before each query's segment: cum[t] for t < T, and their sum.
-  __device__ static __forceinline__ int64_t make_plan(const AttendArgs& a, int64_t* cum) {
+  // Key tiles before each query's segment: cum[t] for t < T, and their sum; the
+  // queries' intervals.
+  __device__ static __forceinline__ int64_t make_plan(const AttendArgs& a, int64_t* cum, Interval* known) {
     const int T = (int)a.T, tid = threadIdx.x;
+    for (int t = tid; t < T; t += TH) known[t] = interval_of(a, nullptr, t);
+    __syncthreads();
     constexpr int PER = kPlanMax / TH;       // queries a thread sums
     int64_t w[PER];
     int64_t mine = 0;
@@ -820,21 +903,20 @@ struct Kernel {
       const int t = tid * PER + i;
       w[i] = 0;
       if (t < T) {
-        const QueryInfo q = query_info(a, t);
-        const bool starts = t % a.qt == 0 || query_info(a, t - 1).seq != q.seq;
-        if (starts) {
+        const int seq = known[t].seq;
+        if (t % a.qt == 0 || known[t - 1].seq != seq) {
           int lo = 0x7fffffff, hi = 0;
           const int last = min(T, (t / a.qt + 1) * a.qt);
-          for (int u = t; u < last; ++u) {
-            const QueryInfo z = query_info(a, u);
-            if (z.seq != q.seq) break;
-            if (a.idx) {
-              lo = 0;
-              hi = z.hi > z.lo ? a.topk : 0;
-            } else if (z.hi > z.lo) {
+          for (int u = t; u < last && known[u].seq == seq; ++u) {
+            const Interval z = known[u];
+            if (z.hi > z.lo) {
               lo = min(lo, z.lo);
               hi = max(hi, z.hi);
             }
+          }
+          if (a.idx && hi > lo) {
+            lo = 0;
+            hi = a.topk;
           }
           w[i] = tiles_of(lo, hi, KT);
         }
@@ -868,7 +950,7 @@ struct Kernel {
     return total;
   }
 
-  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int64_t* cum, int* odd) {
+  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int64_t* cum, Interval* intervals, int* odd) {
     const AttendArgs& a = fresh(ap);
     const bool mixed = a.odd != nullptr;
     if (GUARD) {
@@ -883,11 +965,11 @@ struct Kernel {
     int64_t total = 0, u, u1;
     int hh = 0;
     if (planned) {
-      total = uniform(make_plan(a, cum));
+      total = uniform(make_plan(a, cum, intervals));
       const int64_t units = total * NH;
       u = blockIdx.x * units / a.G;
       u1 = ((int64_t)blockIdx.x + 1) * units / a.G;
-      if (blockIdx.x == 0 && !GUARD) publish_plan(a, cum, total);
+      if (blockIdx.x == 0 && !GUARD) publish_plan(a, cum, intervals, total);
     } else {
       // one workgroup per row tile, the last queries (the longest of a causal prompt) first
       const unsigned ntiles = (unsigned)((T + a.qt - 1) / a.qt);
@@ -909,7 +991,7 @@ struct Kernel {
         lo = uniform(lo);
         const int64_t first = uniform(cum[lo]);
         p.t0 = lo;
-        p.nq = run_length(a, lo);
+        p.nq = run_length(a, intervals, lo);
         const int next = lo + p.nq;
         const int tiles = (int)((next < T ? uniform(cum[next]) : total) - first);
         const int64_t in = u - first * NH;
@@ -922,7 +1004,7 @@ struct Kernel {
         u += p.tile1 - p.tile0;
       } else {
         p.t0 = u;
-        p.nq = run_length(a, u);
+        p.nq = run_length(a, nullptr, u);
         p.hh = hh;
         p.tile0 = 0;
         p.tile1 = 0x7fffffff;
@@ -930,7 +1012,7 @@ struct Kernel {
         p.slot = 0;
         u += p.nq;
       }
-      run_part(ap, p, lds, mixed ? odd : nullptr);
+      run_part(ap, p, lds, planned ? intervals : nullptr, mixed ? odd : nullptr);
     }
     if (!GUARD && mixed) {
       __syncthreads();
@@ -939,12 +1021,13 @@ struct Kernel {
   }
 
   // What the join needs: every query takes the entry of its segment.
-  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int64_t* cum, int64_t total) {
+  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int64_t* cum, const Interval* known,
+                                                     int64_t total) {
     for (int t = threadIdx.x; t < (int)a.T; t += TH) {
       int t0 = t, next = t + 1;
-      const int seq = query_info(a, t).seq;
-      while (t0 % a.qt != 0 && query_info(a, t0 - 1).seq == seq) --t0;
-      while (next < (int)a.T && next % a.qt != 0 && query_info(a, next).seq == seq) ++next;
+      const int seq = known[t].seq;
+      while (t0 % a.qt != 0 && known[t0 - 1].seq == seq) --t0;
+      while (next < (int)a.T && next % a.qt != 0 && known[next].seq == seq) ++next;
       PlanEntry e;
       e.first = cum[t0];
       e.tiles = (int32_t)((next < (int)a.T ? cum[next] : total) - cum[t0]);
@@ -961,9 +1044,10 @@ __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shap
                                                           : 1)) void attend_kernel(AttendArgs) {
   __shared__ __align__(16) unsigned char lds[Shape<D, R>::lds_bytes];
   __shared__ int64_t cum[kPlanMax];
+  __shared__ Interval intervals[kPlanMax];
   __shared__ int odd;
   // the arguments are read where they lie (see fresh)
-  Kernel<HALF, D, R, EXTRA, GUARD>::body((ArgPtr)__builtin_amdgcn_kernarg_segment_ptr(), lds, cum, &odd);
+  Kernel<HALF, D, R, EXTRA, GUARD>::body((ArgPtr)__builtin_amdgcn_kernarg_segment_ptr(), lds, cum, intervals, &odd);
 }
 
 template <bool HALF, int D, int R>
@@ -981,7 +1065,9 @@ hipError_t launch_shape(const AttendArgs& a, unsigned blocks, hipStream_t st) {
 template <int D>
 hipError_t launch_dim(const AttendArgs& a, int R, bool half, unsigned blocks, hipStream_t st) {
   switch (R) {
-    case 16: return half ? launch_shape<true, D, 16>(a, blocks, st) : launch_shape<false, D, 16>(a, blocks, st);
+    case 16:
+      if constexpr (D < 256) return half ? launch_shape<true, D, 16>(a, blocks, st) : launch_shape<false, D, 16>(a, blocks, st);
+      break;
     case 32: return half ? launch_shape<true, D, 32>(a, blocks, st) : launch_shape<false, D, 32>(a, blocks, st);
     case 64: return half ? launch_shape<true, D, 64>(a, blocks, st) : launch_shape<false, D, 64>(a, blocks, st);
     case 128: return half ? launch_shape<true, D, 128>(a, blocks, st) : launch_shape<false, D, 128>(a, blocks, st);

@@ -53,8 +53,6 @@ struct AttendArgs {
   uint16_t* out;            // [T][Hq][d]; null: out32
   float* out32;
   float* lse;               // [T][Hq] or null
-  const float* init_out;    // [T][Hq][d] and [T][Hq]: a finished part to join, or null
-  const float* init_lse;
   // one word a workgroup, set if its parts have to be computed again by the
   // guarded form; null where all rows of a part see the same keys
   int32_t* odd;
@@ -70,7 +68,7 @@ struct AttendArgs {
 // Rows (query, head) of a workgroup's tile for a batch: 16, 32, 64 or 128.
 // single: a row tile takes one query (selected tokens are each query's own; in a
 // decode step no two queries share a sequence).
-int attend_rows(int64_t T, int64_t nseq, int group, bool single);
+int attend_rows(int64_t T, int64_t nseq, int group, int d, bool single);
 bool attend_planned(int64_t T);
 // Workgroups of a planned launch, and its workspace.
 int attend_groups(int d, int R);
@@ -80,7 +78,13 @@ size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, 
 // intervals of their own).
 void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws);
 int64_t attend_blocks(const AttendArgs& a);
+// The rows of one pass; those that it leaves in parts want a join.
 hipError_t launch_attend(const AttendArgs& a, int R, bool half, hipStream_t st);
+// Joins the parts of planned passes: of one (b null; rows that are whole are
+// left alone), or of two over different keys of the same rows, into out and lse
+// (both passes' whole rows in their out32 and lse).
+hipError_t launch_attend_join(const AttendArgs& a, int Ra, const AttendArgs* b, int Rb, uint16_t* out, float* lse,
+                              bool half, hipStream_t st);
 
 // Per head dimension, in translation units of their own.
 hipError_t launch_attend_d64(const AttendArgs& a, int R, bool half, unsigned blocks, hipStream_t st);

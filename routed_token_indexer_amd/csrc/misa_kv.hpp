@@ -39,6 +39,13 @@ struct KvView {
   int64_t table_stride;
   int64_t nseq;
   int64_t Lmax;             // tokens a sequence can address: cols * page, or page
+  // Row (page p, row r) of a head lies p * page_units + r * tok_units units behind
+  // the head's first one, in 32 bits: bytes where the cache ends before 4 GiB
+  // (unit_shift 0; bytes: its extent), else 2^unit_shift elements.
+  uint32_t page_units;
+  uint32_t tok_units;
+  uint32_t unit_shift;
+  uint32_t bytes;
 };
 
 // Page of token s of sequence seq (seq, s in range); -1 if the table holds no page of the cache.
