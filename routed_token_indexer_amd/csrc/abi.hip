@@ -1014,8 +1014,8 @@ int32_t misa_pivot_indexer(const void* q, const float* w, const void* k, const i
 size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t heads, int32_t d, int64_t nseq,
                                    int64_t npre) {
   if (T <= 0 || heads < 1 || Hq < heads || Hq % heads || !(d == 64 || d == 128 || d == 256) || nseq < 1) return 0;
-  const bool single = op == MISA_OP_ATTEND_SELECTED || T <= nseq;
-  const size_t own = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, nseq, Hq, heads, d, single), single, !single);
+  const bool gather = op == MISA_OP_ATTEND_SELECTED, single = gather || T <= nseq;
+  const size_t own = misa::attend_ws_bytes(T, Hq, heads, d, rows_of(T, nseq, Hq, heads, d, single), single, !gather);
   switch (op) {
     case MISA_OP_ATTEND:
     case MISA_OP_ATTEND_SELECTED:
@@ -1101,7 +1101,7 @@ int32_t misa_attend(const misa_kv_cache* cache, const void* q, int64_t q_ts, int
   a.mode = misa::kAttendPlain;
   const bool single = T <= a.kv.nseq;
   const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, single);
-  misa::attend_setup(a, R, single, !single, ws);
+  misa::attend_setup(a, R, single, !single || q_start, ws);
   if ((rc = check_attend_grid(fn, a))) return rc;
   return run_attend(fn, a, R, cache->dtype == MISA_FP16, (hipStream_t)stream);
 }

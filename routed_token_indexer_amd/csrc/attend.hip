@@ -149,6 +149,19 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Pass pa, Pass pb, int 
   attend::write_row<HALF, D>(a, row, d0, M, sum, o);
 }
 
+// Rows a wave loads at a time where several waves share them, 0 elsewhere.
+template <int D, int R>
+constexpr int shared_rows() { return Shape<D, R>::RW > 1 ? Shape<D, R>::WR : 0; }
+template <int D>
+int shared_rows_of(int R) {
+  switch (R) {
+    case 32: return shared_rows<D, 32>();
+    case 64: return shared_rows<D, 64>();
+    case 128: return shared_rows<D, 128>();
+  }
+  return 0;
+}
+
 template <int D>
 int per_cu(int R) {
   switch (R) {
@@ -194,7 +207,7 @@ static int64_t blocks_of(int64_t T, int heads, int d, int R, const Tile& t) {
 size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, bool mixed) {
   const Tile t = tile_of(Hq / heads, R, single);
   size_t b = 0;
-  if (mixed && t.qt > 1) b += up((size_t)blocks_of(T, heads, d, R, t) * 4);
+  if (mixed) b += up((size_t)blocks_of(T, heads, d, R, t) * 4);
   if (!attend_planned(T)) return b;
   const size_t slots = 2 * (size_t)attend_groups(d, R);
   return b + up(slots * R * d * 4) + up(slots * R * 8) + up((size_t)T * sizeof(PlanEntry)) + 256;
@@ -209,11 +222,15 @@ void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws) {
   a.qt = t.qt;
   a.NH = a.Hkv * a.head_tiles;
   a.by_gw = fast_div((uint32_t)a.gw);
+  // pages that hold whole groups of a wave's rows take the kernels that look a
+  // page up once a group (a row cache is one page a sequence)
+  const int wr = d == 64 ? shared_rows_of<64>(R) : d == 128 ? shared_rows_of<128>(R) : shared_rows_of<256>(R);
+  a.align = wr && !a.idx && (!a.kv.table || a.kv.page % wr == 0) ? wr : 1;
   a.planned = attend_planned(a.T);
   a.G = a.planned ? attend_groups(d, R) : 0;
   a.odd = nullptr;
   char* p = static_cast<char*>(ws);
-  if (mixed && t.qt > 1) {
+  if (mixed) {
     a.odd = reinterpret_cast<int32_t*>(p);
     p += up((size_t)blocks_of(a.T, a.Hkv, d, R, t) * 4);
   }

@@ -89,6 +89,7 @@ struct Shape {
   static constexpr int KW = RW >= 4 ? 1 : 4 / RW;
   static constexpr int NK = D == 256 ? 32 : (D == 128 ? (R == 128 ? 64 : 32) : 64);
   static constexpr int KT = KW * NK;
+  static constexpr int WR = NK / RW;     // rows of a step that each wave loads
   static constexpr int threads = 64 * RW * KW;
   static constexpr int buffers = RW == 1 ? 1 : 2;
   static constexpr int stage_bytes = KT * D * 2 * 2;
@@ -222,6 +223,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Interval* kno
     }
     if (s.hi <= s.lo) s.lo = s.hi = 0;
     s.some = s.hi - s.lo;
+    s.lo &= -a.align;
     return s;
   }
   int lo = 0x7fffffff, hi = 0, seq = -1, all_lo = 0, all_hi = 0x7fffffff;
@@ -240,6 +242,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Interval* kno
   s.hi = uniform(wave_max_of(hi));
   if (s.hi <= s.lo) s.lo = s.hi = 0;
   s.some = uniform(wave_min_of(all_hi) - wave_max_of(all_lo));
+  s.lo &= -a.align;
   return s;
 }
 
@@ -270,10 +273,10 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, int 
   if (d0 == 0 && a.lse) a.lse[row] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * kLn2;
 }
 
-template <bool HALF, int D, int R, bool EXTRA, bool GUARD>
+template <bool HALF, int D, int R, bool EXTRA, bool ALIGNED, bool GUARD>
 struct Kernel {
   using S = Shape<D, R>;
-  static constexpr int MR = S::MR, RW = S::RW, KW = S::KW, NK = S::NK, KT = S::KT, TH = S::threads;
+  static constexpr int MR = S::MR, RW = S::RW, KW = S::KW, NK = S::NK, KT = S::KT, WR = S::WR, TH = S::threads;
   static constexpr int RPI = 512 / D;              // rows a wave's load instruction covers
   static constexpr int LPR = D / 8;                // lanes (16-byte pieces) per row
   static constexpr int NLD = NK / RW / RPI;        // load instructions per tensor, wave and step
@@ -359,28 +362,70 @@ struct Kernel {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
   }
 
-  __device__ static __forceinline__ void load_rows(const Bases& b, uint32_t unit, int rw, u32x4 (&kr)[NLD], u32x4 (&vr)[NLD]) {
+  // Loads of this wave's rows: instruction i covers rows i * RPI + lane / LPR of
+  // its WR, whose units are given.
+  __device__ static __forceinline__ void load_units(const Bases& b, const uint32_t (&unit)[NLD], int rw, u32x4 (&kr)[NLD],
+                                                    u32x4 (&vr)[NLD]) {
     const int lane = threadIdx.x & 63;
     if (b.shift == 0) {
 #pragma unroll
       for (int i = 0; i < NLD; ++i) {
-        const int row = (rw * NLD + i) * RPI + lane / LPR;
-        const uint32_t at = (uint32_t)__shfl((int)unit, row, 64) + 16 * ((lane % LPR) ^ swizzle<D>(row));
+        const uint32_t at = unit[i] + 16 * ((lane % LPR) ^ swizzle<D>(rw * WR + i * RPI + lane / LPR));
         kr[i] = buffer_row(b.kb, at);
         vr[i] = buffer_row(b.vb, at);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NLD; ++i) {
-        const int row = (rw * NLD + i) * RPI + lane / LPR;
-        const uint32_t u = (uint32_t)__shfl((int)unit, row, 64);
-        const int c = 8 * ((lane % LPR) ^ swizzle<D>(row));
+        const int c = 8 * ((lane % LPR) ^ swizzle<D>(rw * WR + i * RPI + lane / LPR));
         const uint16_t* z = reinterpret_cast<const uint16_t*>(kZeroRow);
-        const uint64_t at = (uint64_t)u << b.shift;
-        kr[i] = *reinterpret_cast<const u32x4*>((u != kNoRow ? b.k + at : z) + c);
-        vr[i] = *reinterpret_cast<const u32x4*>((u != kNoRow ? b.v + at : z) + c);
+        const uint64_t at = (uint64_t)unit[i] << b.shift;
+        kr[i] = *reinterpret_cast<const u32x4*>((unit[i] != kNoRow ? b.k + at : z) + c);
+        vr[i] = *reinterpret_cast<const u32x4*>((unit[i] != kNoRow ? b.v + at : z) + c);
       }
     }
+  }
+  __device__ static __forceinline__ void load_rows(const Bases& b, uint32_t unit, int rw, u32x4 (&kr)[NLD], u32x4 (&vr)[NLD]) {
+    const int lane = threadIdx.x & 63;
+    uint32_t u[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) u[i] = (uint32_t)__shfl((int)unit, rw * WR + i * RPI + lane / LPR, 64);
+    load_units(b, u, rw, kr, vr);
+  }
+
+  // Aligned pages: a step's keys start at a multiple of WR, which divides the
+  // page, so that each wave's WR rows lie in one page. Lane j looks up the page of
+  // wave j's rows (every wave has to know which of them are keys); a wave's own
+  // page is then a scalar, and its rows follow each other.
+  __device__ static __forceinline__ int page_entry(const KvView& kv, const int32_t* table, int seq, int base, int end) {
+    const int lane = threadIdx.x & 63;
+    const int s = min(base + (lane & (RW - 1)) * WR, end - 1);
+    return table ? table[fast_quot(kv.by_page, (uint32_t)s)] : seq;
+  }
+  __device__ static __forceinline__ uint64_t load_aligned(const KvView& kv, const Bases& b, int entry, int base, int end, int rw,
+                                                          u32x4 (&kr)[NLD], u32x4 (&vr)[NLD]) {
+    const int lane = threadIdx.x & 63;
+    const bool ok = (uint32_t)entry < (uint32_t)kv.npages && base + (lane & (RW - 1)) * WR < end;
+    const uint32_t bits = (uint32_t)__ballot(ok) & ((1u << RW) - 1);
+    const int s0 = base + rw * WR;
+    const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, rw);
+    const uint32_t within = (uint32_t)s0 - fast_quot(kv.by_page, (uint32_t)s0) * (uint32_t)kv.page;
+    const uint32_t first = page * kv.page_units + within * kv.tok_units;
+    const int rows = (bits >> rw & 1) ? end - s0 : 0;
+    uint32_t u[NLD];
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int r = i * RPI + lane / LPR;
+      u[i] = r < rows ? first + (uint32_t)r * kv.tok_units : kNoRow;
+    }
+    load_units(b, u, rw, kr, vr);
+    uint64_t valid = ~0ull;
+    if (bits != (1u << RW) - 1) {
+      valid = 0;
+#pragma unroll
+      for (int j = 0; j < RW; ++j) valid |= (bits >> j & 1) ? ((WR == 64 ? 0ull : 1ull << (WR & 63)) - 1) << (j * WR) : 0;
+    }
+    return NK == 64 ? valid : valid & ((1ull << (NK & 63)) - 1);
   }
   __device__ static __forceinline__ void store_rows(uint16_t* ks, uint16_t* vs, int rw, const u32x4 (&kr)[NLD],
                                                     const u32x4 (&vr)[NLD]) {
@@ -724,7 +769,14 @@ struct Kernel {
     nxt.within = nxt.page = 0;
     int far = -1, cur_token = -1;
     uint64_t valid = 0;
-    if (mine > 0) {
+    int entry = 0;
+    if (ALIGNED) {
+      if (mine > 0) {
+        valid = load_aligned(a.kv, bases, page_entry(a.kv, table, sp.seq, k0, end), k0, end, rw, kr, vr);
+        entry = page_entry(a.kv, table, sp.seq, k0 + KT, end);
+        store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
+      }
+    } else if (mine > 0) {
       const Keys cur = page_of(a.kv, table, sp.seq, token_of(ids, k0, end), id_lo, id_hi);
       nxt = page_of(a.kv, table, sp.seq, token_of(ids, k0 + KT, end), id_lo, id_hi);
       far = token_of(ids, k0 + 2 * KT, end);
@@ -745,7 +797,13 @@ struct Kernel {
       const bool more = it + 1 < mine;
       uint64_t next_valid = 0;
       int next_token = -1;
-      if (more) {
+      if (ALIGNED) {
+        if (more) {
+          const int now = entry;
+          entry = page_entry(a.kv, table, sp.seq, k0 + (it + 2) * KT, end);
+          next_valid = load_aligned(a.kv, bases, now, k0 + (it + 1) * KT, end, rw, kr, vr);
+        }
+      } else if (more) {
         const uint32_t unit = row_unit(a.kv, nxt);
         next_valid = __ballot(unit != kNoRow);
         next_token = nxt.token;
@@ -918,7 +976,7 @@ struct Kernel {
             lo = 0;
             hi = a.topk;
           }
-          w[i] = tiles_of(lo, hi, KT);
+          w[i] = tiles_of(lo & -a.align, hi, KT);
         }
       }
       mine += w[i];
@@ -1038,7 +1096,7 @@ struct Kernel {
   }
 };
 
-template <bool HALF, int D, int R, bool EXTRA, bool GUARD>
+template <bool HALF, int D, int R, bool EXTRA, bool ALIGNED, bool GUARD>
 __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shape<D, R>::threads / 256 > 0
                                                           ? Shape<D, R>::per_cu * Shape<D, R>::threads / 256
                                                           : 1)) void attend_kernel(AttendArgs) {
@@ -1047,18 +1105,29 @@ __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shap
   __shared__ Interval intervals[kPlanMax];
   __shared__ int odd;
   // the arguments are read where they lie (see fresh)
-  Kernel<HALF, D, R, EXTRA, GUARD>::body((ArgPtr)__builtin_amdgcn_kernarg_segment_ptr(), lds, cum, intervals, &odd);
+  Kernel<HALF, D, R, EXTRA, ALIGNED, GUARD>::body((ArgPtr)__builtin_amdgcn_kernarg_segment_ptr(), lds, cum, intervals, &odd);
 }
 
 template <bool HALF, int D, int R>
 hipError_t launch_shape(const AttendArgs& a, unsigned blocks, hipStream_t st) {
   const dim3 grid(blocks), block(Shape<D, R>::threads);
-  if (a.cap > 0.f || a.slopes)
-    hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, false>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((attend_kernel<HALF, D, R, false, false>), grid, block, 0, st, a);
+  const bool extra = a.cap > 0.f || a.slopes;
+  if constexpr (Shape<D, R>::RW > 1) {
+    if (a.align > 1) {
+      if (extra)
+        hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, true, false>), grid, block, 0, st, a);
+      else
+        hipLaunchKernelGGL((attend_kernel<HALF, D, R, false, true, false>), grid, block, 0, st, a);
+    }
+  }
+  if (a.align == 1) {
+    if (extra)
+      hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, false, false>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((attend_kernel<HALF, D, R, false, false, false>), grid, block, 0, st, a);
+  }
   // workgroups that met values that are not finite where not all rows see them
-  if (a.odd) hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, true>), grid, block, 0, st, a);
+  if (a.odd) hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, false, true>), grid, block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -47,6 +47,7 @@ struct AttendArgs {
   int32_t qt;               // queries of a row tile: R / gw
   int32_t NH;               // Hkv * head_tiles
   FastDiv by_gw;
+  int32_t align;            // a part's keys start at a multiple of this (1 or Shape::WR)
   float scale;
   float cap;                // 0: none
   const float* slopes;      // [Hq] or null
@@ -74,8 +75,8 @@ bool attend_planned(int64_t T);
 int attend_groups(int d, int R);
 size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, bool mixed);
 // Fills the fields that depend on the tile and carves the workspace.
-// mixed: queries of one part may see different keys (several queries a row tile,
-// intervals of their own).
+// mixed: rows of one part may see different keys, or not all keys of its steps
+// (several queries a row tile, intervals that start behind a sequence's first key).
 void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws);
 int64_t attend_blocks(const AttendArgs& a);
 // The rows of one pass; those that it leaves in parts want a join.
