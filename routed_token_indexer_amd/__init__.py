@@ -16,5 +16,6 @@ _EXPORTS = ("pool_keys", "route", "score_topk", "hier_rerank", "dsa_index_dense"
 def __getattr__(name):
     if name in _EXPORTS:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)   # found directly from now on
+        return value
     raise AttributeError(name)

@@ -358,10 +358,11 @@ _KV_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16}
 
 
 def _rows(x: torch.Tensor, name: str, ref: torch.Tensor, n: Optional[int] = None, heads: Optional[int] = None):
-    """A [tokens, heads, d] tensor of ``ref``'s type, device and d, rows contiguous."""
+    """Token and head strides of a [tokens, heads, d] tensor of ``ref``'s type,
+    device and d, rows contiguous."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if x.dtype != ref.dtype:
+    if x.dtype is not ref.dtype:
         raise TypeError(f"{name}: expected {ref.dtype}, got {x.dtype}")
     if x.device != ref.device:
         raise ValueError(f"{name}: on {x.device}, the cache on {ref.device}")
@@ -373,25 +374,29 @@ def _rows(x: torch.Tensor, name: str, ref: torch.Tensor, n: Optional[int] = None
     ts, hs, es = x.stride()
     if es != 1 and shape[2] > 1:
         raise ValueError(f"{name}: rows must be contiguous")
-    # the stride of an axis of one element is never used
-    return ts if shape[0] > 1 else 8 * max(1, ts // 8), hs if shape[1] > 1 else 8 * max(1, hs // 8)
+    return _stride(shape[0], ts), _stride(shape[1], hs)
 
 
-def _vec(x: Optional[torch.Tensor], name: str, dtype, shape, device):
+def _stride(n: int, s: int) -> int:
+    """Stride of an axis of n elements; one of a single element is never used and passes the library's check."""
+    return s if n > 1 else 8
+
+
+def _vec(x: Optional[torch.Tensor], name: str, dtype, shape: tuple, device):
     """Pointer of a contiguous tensor of this dtype and shape (None stays None)."""
     if x is None:
         return None
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if x.dtype != dtype:
+    if x.dtype is dtype and x.shape == shape and x.device == device and x.is_contiguous():
+        return x.data_ptr()
+    if x.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
+    if x.shape != shape:
+        raise ValueError(f"{name}: got shape {tuple(x.shape)}, expected {tuple(shape)}")
     if x.device != device:
         raise ValueError(f"{name}: on {x.device}, the cache on {device}")
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name}: got shape {tuple(x.shape)}, expected {tuple(shape)}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return x.data_ptr()
+    raise ValueError(f"{name}: must be contiguous")
 
 
 def _kv_cache(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], table: Optional[torch.Tensor]):
@@ -399,49 +404,57 @@ def _kv_cache(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor], table: Opt
     contiguous rows), or [nseq, Lmax, d] for one head without pages."""
     if not isinstance(k_cache, torch.Tensor):
         raise TypeError("k_cache: expected a torch.Tensor")
-    if k_cache.dtype not in _KV_DTYPES:
+    dtype = _KV_DTYPES.get(k_cache.dtype)
+    if dtype is None:
         raise TypeError(f"k_cache: expected bfloat16 or float16, got {k_cache.dtype}")
     if not k_cache.is_cuda:
         raise ValueError("k_cache: must be a device tensor")
+    shape, strides = k_cache.shape, k_cache.stride()
+    v = None
     if v_cache is not None:
-        if not isinstance(v_cache, torch.Tensor) or v_cache.dtype != k_cache.dtype:
+        if not isinstance(v_cache, torch.Tensor) or v_cache.dtype is not k_cache.dtype:
             raise TypeError(f"v_cache: expected a tensor of {k_cache.dtype}")
         if v_cache.device != k_cache.device:
             raise ValueError(f"v_cache: on {v_cache.device}, k_cache on {k_cache.device}")
-        if v_cache.shape != k_cache.shape or v_cache.stride() != k_cache.stride():
+        if v_cache.shape != shape or v_cache.stride() != strides:
             raise ValueError("v_cache: must have the shape and strides of k_cache")
-    if k_cache.dim() == 3:
-        npages, page, d = k_cache.shape
+        v = v_cache.data_ptr()
+    if len(shape) == 4:
+        npages, page, heads, d = shape
+        ps, ts, hs, es = strides
+    elif len(shape) == 3:
+        npages, page, d = shape
         heads = 1
-        ps, ts, es = k_cache.stride()
+        ps, ts, es = strides
         hs = 8
-    elif k_cache.dim() == 4:
-        npages, page, heads, d = k_cache.shape
-        ps, ts, hs, es = k_cache.stride()
     else:
-        raise ValueError(f"k_cache: expected 3 or 4 dims, got shape {tuple(k_cache.shape)}")
+        raise ValueError(f"k_cache: expected 3 or 4 dims, got shape {tuple(shape)}")
     if es != 1 and d > 1:
         raise ValueError("k_cache: rows must be contiguous")
-    one = lambda n, s: s if n > 1 else 8 * max(1, s // 8)   # noqa: E731  (an axis of one element)
-    c = KvCache(k_cache.data_ptr(), None if v_cache is None else v_cache.data_ptr(), npages, page, one(npages, ps),
-                one(page, ts), one(heads, hs), heads, d, _KV_DTYPES[k_cache.dtype], None, 0, npages)
+    nseq, cols, pages = npages, 0, None
     if table is not None:
         if table.dim() != 2:
             raise ValueError(f"table: expected 2 dims, got shape {tuple(table.shape)}")
-        c.table = _vec(table, "table", torch.int32, table.shape, k_cache.device)
-        c.nseq, c.table_cols = table.shape
-    return c
+        nseq, cols = table.shape
+        pages = _vec(table, "table", torch.int32, table.shape, k_cache.device)
+    return KvCache(k_cache.data_ptr(), v, npages, page, _stride(npages, ps), _stride(page, ts), _stride(heads, hs), heads,
+                   d, dtype, pages, cols, nseq)
 
 
 def _on(device, stream):
     """Stream to launch on: the given one, or the current one of the tensors' device."""
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+_functions = {}
 
 
 def _call(device, name: str, *args):
     """One library call with ``device`` as the current one."""
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == device.index:
         rc = fn(*args)
     else:
         with torch.cuda.device(device):

@@ -55,94 +55,124 @@ __device__ __forceinline__ Parts parts_of(const Pass& p, int64_t t, int head) {
   return x;
 }
 
-// One row's parts: out = sum_i 2^(m_i - M) o_i over the same of the sums. A
-// workgroup takes one row; D / 4 lanes add up every (1024 / D)-th part, and the
-// groups' sums are added in a fixed order. TWO passes over different keys give
-// their parts, or a whole row each (one part with m = lse and a sum of one). With
-// one pass a row that one workgroup of the attention finished is left alone.
-template <bool HALF, int D, bool TWO>
-__global__ __launch_bounds__(256) void attend_join_kernel(Pass pa, Pass pb, int Hq, uint16_t* out, float* lse) {
-  constexpr int LPR = D / 4, GR = 256 / LPR;
-  __shared__ float weight[256];
-  __shared__ float wsum[4], wmax[4];
-  __shared__ floatx4 acc[256];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
+// One row's parts: out = sum_i 2^(m_i - M) o_i over the same of the sums. WPR waves
+// take one row, each every WPR-th chunk of its parts; in a wave D / 4 lanes add up
+// every (256 / D)-th part, eight at a time. The sums of lanes and waves are added
+// in a fixed order. The outputs of a chunk of parts are
+// requested together with their maxima and sums: the launch is bound by its
+// dependent loads (plan, parts). TWO passes over different keys give their parts,
+// or a whole row each (one part with m = lse and a sum of one). With one pass a
+// row that one workgroup of the attention finished is left alone.
+template <bool HALF, int D, bool TWO, int WPR>
+__global__ __launch_bounds__(256) void attend_join_kernel(Pass pa, Pass pb, int64_t rows, int Hq, uint16_t* out, float* lse) {
+  constexpr int LPR = D / 4, GR = 64 / LPR, PER = 8, CH = PER * GR;
+  __shared__ float wave_ml[4][2];
+  __shared__ floatx4 wave_o[4][LPR];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * (4 / WPR) + wave / WPR;
+  const int part = wave % WPR;
+  if (row >= rows) return;
+  const int lane = threadIdx.x & 63;
   const int64_t t = row / Hq;
   const int head = (int)(row - t * Hq);
   float M = -__builtin_inff(), sum = 0.f;
   floatx4 o = {0.f, 0.f, 0.f, 0.f};
-  const int g = tid / LPR, d0 = (tid % LPR) * 4;
+  const int g = lane / LPR, d0 = (lane % LPR) * 4;
+  Parts xs[2];
 #pragma unroll
   for (int which = 0; which < (TWO ? 2 : 1); ++which) {
     const Pass& p = which ? pb : pa;
-    Parts x;
-    x.i0 = x.i1 = 0;
-    if (p.plan) x = parts_of(p, t, head);
+    xs[which].i0 = xs[which].i1 = 0;
+    if (p.plan) xs[which] = parts_of(p, t, head);
+  }
+#pragma unroll
+  for (int which = 0; which < (TWO ? 2 : 1); ++which) {
+    const Pass& p = which ? pb : pa;
+    const Parts& x = xs[which];
     if (x.i0 == x.i1) {
       if (!TWO) return;
       const float l = p.whole_lse[row];
-      if (l == -__builtin_inff()) continue;
+      const floatx4 y = *reinterpret_cast<const floatx4*>(p.whole_out + row * D + d0);
+      if (l == -__builtin_inff() || part != 0) continue;
       const float m = l * attend::kLog2e;
       const float top = fmaxf(M, m);
       const float old = __builtin_amdgcn_exp2f(M - top), w = l == l ? __builtin_amdgcn_exp2f(m - top) : l;
       sum = sum * old + w;
-      const floatx4 y = *reinterpret_cast<const floatx4*>(p.whole_out + row * D + d0);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = o[j] * old + (g == 0 ? y[j] * w : 0.f);
       M = top;
       continue;
     }
     const int64_t G = p.G;
-    for (int base = x.i0; base <= x.i1; base += 256) {
-      // maxima and sums of up to 256 parts
-      const int i = base + tid;
+    // only the row's first part can be its workgroup's second (see Part::slot)
+    const int second = x.i0 * x.units / G <= x.u0 ? x.i0 : -1;
+    for (int base = x.i0 + part * CH; base <= x.i1; base += WPR * CH) {
+      floatx4 y[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int i = min(base + k * GR + g, x.i1);
+        y[k] = *reinterpret_cast<const floatx4*>(p.part_out + ((2 * (int64_t)i + (i == second ? 1 : 0)) * p.R + x.r) * D + d0);
+      }
+      // maxima and sums of the chunk's parts, one a lane
+      const int i = base + lane;
       float m = -__builtin_inff(), s = 0.f;
-      if (i <= x.i1) {
-        const int64_t b = i * x.units / G;
-        if (b != ((int64_t)i + 1) * x.units / G) {
-          const float* ml = p.part_ml + ((2 * (int64_t)i + (b > x.u0 ? 0 : 1)) * p.R + x.r) * 2;
-          m = ml[0];
-          s = ml[1];
+      if (lane < CH && i <= x.i1) {
+        const float* ml = p.part_ml + ((2 * (int64_t)i + (i == second ? 1 : 0)) * p.R + x.r) * 2;
+        const float m1 = ml[0], s1 = ml[1];
+        if (i * x.units / G != ((int64_t)i + 1) * x.units / G) {   // a workgroup with work
+          m = m1;
+          s = s1;
         }
       }
-      float wm = m;
+      float top = m;
 #pragma unroll
-      for (int off = 32; off > 0; off >>= 1) wm = fmaxf(wm, __shfl_xor(wm, off, 64));
-      if ((tid & 63) == 0) wmax[tid >> 6] = wm;
-      __syncthreads();
-      const float top = fmaxf(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), M);
+      for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+      top = fmaxf(top, M);
       const float ref = top == -__builtin_inff() ? 0.f : top;
-      const float w = __builtin_amdgcn_exp2f(m - ref);
-      weight[tid] = w;
-      s = wave_sum(s * w);
-      if ((tid & 63) == 0) wsum[tid >> 6] = s;
-      const float old = __builtin_amdgcn_exp2f(M - ref);
+      const float w = __builtin_amdgcn_exp2f(m - ref), old = __builtin_amdgcn_exp2f(M - ref);
       M = top;
-      __syncthreads();
-      sum = sum * old + wsum[0] + wsum[1] + wsum[2] + wsum[3];
+      sum = sum * old + wave_sum(s * w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] *= old;
-      const int n = min(256, x.i1 - base + 1);
-      // only the row's first part can be its workgroup's second (see Part::slot)
-      const int second = base == x.i0 && x.i0 * x.units / G <= x.u0 ? 0 : -1;
-#pragma unroll 4
-      for (int k = g; k < n; k += GR) {
-        const float wk = weight[k];
-        if (wk == 0.f) continue;   // no part, or one without a key
-        const int64_t slot = 2 * ((int64_t)base + k) + (k == second ? 1 : 0);
-        const floatx4 y = *reinterpret_cast<const floatx4*>(p.part_out + (slot * p.R + x.r) * D + d0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] += y[j] * wk;
+      for (int k = 0; k < PER; ++k) {
+        const float wk = __shfl(w, k * GR + g, 64);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] += wk == 0.f ? 0.f : y[k][j] * wk;   // no part: y is anything
       }
-      __syncthreads();
     }
   }
-  acc[tid] = o;
-  __syncthreads();
-  if (g > 0) return;
 #pragma unroll
-  for (int k = 1; k < GR; ++k) o += acc[k * LPR + tid];
+  for (int off = LPR; off < 64; off <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] += __shfl_xor(o[j], off, 64);
+  if constexpr (WPR > 1) {
+    if (g == 0) wave_o[wave][lane] = o;
+    if (lane == 0) {
+      wave_ml[wave][0] = M;
+      wave_ml[wave][1] = sum;
+    }
+    __syncthreads();
+    if (wave > 0 || g > 0) return;
+    float top = M;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) top = fmaxf(top, wave_ml[k][0]);
+    const float ref = top == -__builtin_inff() ? 0.f : top;
+    const float w0 = __builtin_amdgcn_exp2f(M - ref);
+    sum *= w0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] *= w0;
+#pragma unroll
+    for (int k = 1; k < WPR; ++k) {
+      const float w = __builtin_amdgcn_exp2f(wave_ml[k][0] - ref);
+      const floatx4 y = wave_o[k][lane];
+      sum += wave_ml[k][1] * w;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] += y[j] * w;
+    }
+    M = top;
+  }
+  if (g > 0) return;
   AttendArgs a{};
   a.out = out;
   a.lse = lse;
@@ -225,10 +255,11 @@ void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws) {
   // pages that hold whole groups of a wave's rows take the kernels that look a
   // page up once a group (a row cache is one page a sequence)
   const int wr = d == 64 ? shared_rows_of<64>(R) : d == 128 ? shared_rows_of<128>(R) : shared_rows_of<256>(R);
-  a.align = wr && !a.idx && (!a.kv.table || a.kv.page % wr == 0) ? wr : 1;
+  a.align = wr && !a.idx && a.kv.unit_shift == 0 && (!a.kv.table || a.kv.page % wr == 0) ? wr : 1;
   a.planned = attend_planned(a.T);
   a.G = a.planned ? attend_groups(d, R) : 0;
   a.odd = nullptr;
+  a.blocks = (uint32_t)blocks_of(a.T, a.Hkv, d, R, t);
   char* p = static_cast<char*>(ws);
   if (mixed) {
     a.odd = reinterpret_cast<int32_t*>(p);
@@ -262,16 +293,25 @@ hipError_t launch_attend_join(const AttendArgs& a, int Ra, const AttendArgs* b, 
                               bool half, hipStream_t st) {
   if (!b && !a.planned) return hipSuccess;
   const Pass pa = pass_of(a, Ra), pb = b ? pass_of(*b, Rb) : pa;
-  const dim3 grid((unsigned)(a.T * a.Hq));
-#define MISA_JOIN(HALF_, D_)                                                                                     \
-  do {                                                                                                           \
-    if (b) hipLaunchKernelGGL((attend_join_kernel<HALF_, D_, true>), grid, dim3(256), 0, st, pa, pb, a.Hq, out, lse);  \
-    else hipLaunchKernelGGL((attend_join_kernel<HALF_, D_, false>), grid, dim3(256), 0, st, pa, pb, a.Hq, out, lse);   \
+  const int64_t rows = a.T * a.Hq;
+  // few rows are spread over four waves each (256 rows of 32 parts: 8 us, 13 with a
+  // wave each); many fill the chip anyway (4096 rows of 24 parts: 12 us, 21 with four)
+  const bool few = rows <= 1024;
+  const dim3 grid((unsigned)(few ? rows : (rows + 3) / 4));
+#define MISA_JOIN_(HALF_, D_, TWO_, W_) \
+  hipLaunchKernelGGL((attend_join_kernel<HALF_, D_, TWO_, W_>), grid, dim3(256), 0, st, pa, pb, rows, a.Hq, out, lse)
+#define MISA_JOIN(HALF_, D_)                                                     \
+  do {                                                                           \
+    if (b && few) MISA_JOIN_(HALF_, D_, true, 4);                                \
+    else if (b) MISA_JOIN_(HALF_, D_, true, 1);                                  \
+    else if (few) MISA_JOIN_(HALF_, D_, false, 4);                               \
+    else MISA_JOIN_(HALF_, D_, false, 1);                                        \
   } while (0)
   if (a.d == 64) { if (half) MISA_JOIN(true, 64); else MISA_JOIN(false, 64); }
   if (a.d == 128) { if (half) MISA_JOIN(true, 128); else MISA_JOIN(false, 128); }
   if (a.d == 256) { if (half) MISA_JOIN(true, 256); else MISA_JOIN(false, 256); }
 #undef MISA_JOIN
+#undef MISA_JOIN_
   return hipGetLastError();
 }
 

@@ -78,6 +78,13 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+// What a kernel does to the scores besides the scale.
+enum Mode : int {
+  kPlain = 0,
+  kCap = 1,    // a cap up to kPlainCap
+  kBias = 2,   // anything
+};
+
 // Tile shapes. NK keys per group of waves and step; KT = KW * NK keys a step.
 // With RW = 1 a wave's keys are its own: one LDS buffer and no barrier in the
 // loop. Otherwise the RW waves of a group share them, in two buffers.
@@ -98,7 +105,7 @@ struct Shape {
   static constexpr int lds_bytes = buffers * stage_bytes > merge_bytes ? buffers * stage_bytes : merge_bytes;
   // workgroups that fit a CU (160 KiB of LDS, the plan's share included, and 512
   // registers a SIMD)
-  static constexpr int per_cu = D < 256 && (lds_bytes + kPlanMax * 20 + 64) * 2 <= 160 * 1024 ? 2 : 1;
+  static constexpr int per_cu = D < 256 && (lds_bytes + kPlanMax * 24 + 64) * 2 <= 160 * 1024 ? 2 : 1;
 };
 
 // 16-byte piece c of row r lies at piece c ^ swizzle(r) of its row in LDS. The
@@ -194,14 +201,20 @@ __device__ __forceinline__ int wave_max_of(int v) {
   return v;
 }
 
-// Sequence and interval of the queries of a planned batch, in LDS.
+// What a workgroup keeps of its queries (of the whole batch where it is planned)
+// in LDS: entry t - t0 for query t.
 struct Interval {
   int seq, lo, hi;
+  int pos;          // position relative to the row's token 0
 };
-__device__ __forceinline__ Interval interval_of(const AttendArgs& a, const Interval* known, int64_t t) {
-  if (known) return known[t];
+struct Known {
+  Interval* at;
+  int64_t t0;
+  __device__ __forceinline__ const Interval& operator[](int64_t t) const { return at[(int)(t - t0)]; }
+};
+__device__ __forceinline__ Interval interval_of(const AttendArgs& a, int64_t t) {
   const QueryInfo q = query_info(a, t);
-  return Interval{q.seq, q.lo, q.hi};
+  return Interval{q.seq, q.lo, q.hi, q.pos - q.kbase};
 }
 
 // Sequence and span of the visible keys of queries t0 .. t0 + nq - 1 (one sequence).
@@ -209,11 +222,11 @@ struct Span {
   int seq, lo, hi;   // keys that any of them sees lie in [lo, hi)
   int some;          // keys that all of them see
 };
-__device__ __forceinline__ Span span_of(const AttendArgs& a, const Interval* known, int64_t t0, int nq) {
+__device__ __forceinline__ Span span_of(const AttendArgs& a, const Known& known, int64_t t0, int nq) {
   const int lane = threadIdx.x & 63;
   Span s;
   if (nq == 1) {
-    const Interval r = interval_of(a, known, t0);
+    const Interval r = known[t0];
     s.seq = uniform(r.seq);
     s.lo = uniform(r.lo);
     s.hi = uniform(r.hi);
@@ -228,7 +241,7 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Interval* kno
   }
   int lo = 0x7fffffff, hi = 0, seq = -1, all_lo = 0, all_hi = 0x7fffffff;
   for (int i = lane; i < nq; i += 64) {
-    const Interval r = interval_of(a, known, t0 + i);
+    const Interval r = known[t0 + i];
     seq = max(seq, r.seq);
     if (r.hi > r.lo) {
       lo = min(lo, r.lo);
@@ -246,15 +259,49 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Interval* kno
   return s;
 }
 
-// tanh(y) for |y| <= 1/2 as y times a polynomial in y^2, fitted to 2.8e-8 of the
-// value; c4 .. c0 are its coefficients.
-constexpr float kTanh[5] = {1.f, -0.33333072066307f, 0.13324829936f, -0.05298925563693f, 0.017141323536634f};
+// tanh(y) for |y| <= kNear as y times a polynomial in y^2, fitted to 6e-8 of the
+// value (one half step of fp32).
+constexpr float kNear = 0.35f;
+constexpr float kTanh[4] = {0.9999999403953552f, -0.33332425355911255f, 0.13295884430408478f, -0.04896282404661179f};
 
-// Caps up to this one take 1 - 2 / (1 + e^2y) beyond |y| = 1/2 and, in a tile that
-// has such scores, for the others too: exp2, the sum and the reciprocal lose at
-// most 9 half steps of fp32 of one, times the cap (1.4e-4 of a score at the
-// limit, 3e-5 at 50). Larger caps choose for each score.
+// Caps up to this one take 1 - 2 / (1 + e^2y) beyond kNear and, in a tile that has
+// such scores, for the others too: exp2, the sum and the reciprocal lose at most
+// 9 half steps of fp32 of one, times the cap (1.4e-4 of a score at the limit,
+// 3e-5 at 50). Larger caps choose for each score.
 constexpr float kPlainCap = 256.f;
+
+// The cap in units of log2 for scores of |y| <= kNear: x P(x^2), y = c x.
+struct NearCap {
+  float k0, k1, k2, k3;
+  __device__ __forceinline__ float factor(float x) const {
+    const float z = x * x;
+    return k0 + z * (k1 + z * (k2 + z * k3));
+  }
+};
+__device__ __forceinline__ NearCap near_cap(float cap, float c) {
+  const float g = cap * kLog2e * c, c2 = c * c;
+  return NearCap{g * kTanh[0], g * kTanh[1] * c2, g * kTanh[2] * c2 * c2, g * kTanh[3] * c2 * c2 * c2};
+}
+// The cap in units of log2, less off, for any score.
+struct FarCap {
+  float cap2, e, c;
+  bool choose;        // a large cap: per score
+  __device__ __forceinline__ float plain(float x, float off) const {
+    return (cap2 - off) - 2.f * cap2 * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * e));
+  }
+  __device__ __forceinline__ float chosen(float x, float off) const {
+    const float y = x * c, z = y * y;
+    const float small = y * (kTanh[0] + z * (kTanh[1] + z * (kTanh[2] + z * kTanh[3])));
+    float big = plain(x, off);
+    asm("" : "+v"(big));   // both, then a select: a branch for each score costs more
+    return fabsf(y) < kNear ? cap2 * small - off : big;
+  }
+};
+__device__ __forceinline__ FarCap far_cap(float cap, float c) {
+  return FarCap{cap * kLog2e, c * (2.f * kLog2e), c, cap > kPlainCap};
+}
+// the coefficients stay normal numbers for c in this range
+__device__ __forceinline__ bool near_cap_holds(float c) { return c > 1e-4f && c < 1e4f; }
 
 // A finished row: sums relative to 2^m (m in units of log2) to the result and its log-sum.
 template <bool HALF, int D>
@@ -273,7 +320,7 @@ __device__ __forceinline__ void write_row(const AttendArgs& a, int64_t row, int 
   if (d0 == 0 && a.lse) a.lse[row] = sum == 0.f ? -__builtin_inff() : (m + __log2f(sum)) * kLn2;
 }
 
-template <bool HALF, int D, int R, bool EXTRA, bool ALIGNED, bool GUARD>
+template <bool HALF, int D, int R, int MODE, bool ALIGNED, bool GUARD>
 struct Kernel {
   using S = Shape<D, R>;
   static constexpr int MR = S::MR, RW = S::RW, KW = S::KW, NK = S::NK, KT = S::KT, WR = S::WR, TH = S::threads;
@@ -282,7 +329,9 @@ struct Kernel {
   static constexpr int NLD = NK / RW / RPI;        // load instructions per tensor, wave and step
   static constexpr int QF = D * MR / 512;          // query fragments: d / 16 or d / 32 products deep
   static constexpr int OT = D / MR;                // output tiles of MR dims
-  static constexpr int ST = NK / MR;               // score tiles of MR keys
+  static constexpr int KS = 32;                    // keys of a step that are taken at a time
+  static constexpr int NS = NK / KS;
+  static constexpr int ST = KS / MR;               // score tiles of MR keys
   static constexpr int AR = MR * MR / 64;          // accumulator registers of a tile: 16 or 4
   static_assert(NLD >= 1 && NK % MR == 0, "tile shape");
   using Acc = typename std::conditional<MR == 32, floatx16, floatx4>::type;
@@ -301,10 +350,15 @@ struct Kernel {
     int lo, hi;     // visible keys
     float slope;
     int pos;        // position - kbase
-    bool active;
-    int64_t t;
-    int head;
   };
+  // Query and head of row r of a part's tile; false: no such row.
+  __device__ static __forceinline__ bool row_of(const AttendArgs& a, const Part& p, int r, int64_t& t, int& head) {
+    const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
+    const int qi = (int)fast_quot(a.by_gw, (uint32_t)r);
+    head = kvh * a.group + hb * a.gw + (r - qi * a.gw);
+    t = p.t0 + qi;
+    return qi < p.nq && head < (kvh + 1) * a.group;
+  }
 
   // The keys of one step for one group of waves: lane l looks up key l, in three
   // steps of the loop: its token (the key's number, or a selected id), the table
@@ -393,8 +447,8 @@ struct Kernel {
     load_units(b, u, rw, kr, vr);
   }
 
-  // Aligned pages: a step's keys start at a multiple of WR, which divides the
-  // page, so that each wave's WR rows lie in one page. Lane j looks up the page of
+  // Aligned pages (of a cache that ends before 4 GiB): a step's keys start at a
+  // multiple of WR, which divides the page, so that each wave's WR rows lie in one page. Lane j looks up the page of
   // wave j's rows (every wave has to know which of them are keys); a wave's own
   // page is then a scalar, and its rows follow each other.
   __device__ static __forceinline__ int page_entry(const KvView& kv, const int32_t* table, int seq, int base, int end) {
@@ -402,8 +456,17 @@ struct Kernel {
     const int s = min(base + (lane & (RW - 1)) * WR, end - 1);
     return table ? table[fast_quot(kv.by_page, (uint32_t)s)] : seq;
   }
-  __device__ static __forceinline__ uint64_t load_aligned(const KvView& kv, const Bases& b, int entry, int base, int end, int rw,
-                                                          u32x4 (&kr)[NLD], u32x4 (&vr)[NLD]) {
+  // Where this lane's pieces lie behind the first of its wave's rows (byte offsets).
+  __device__ static __forceinline__ void piece_offsets(const KvView& kv, int rw, uint32_t (&piece)[NLD]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NLD; ++i) {
+      const int r = i * RPI + lane / LPR;
+      piece[i] = (uint32_t)r * kv.tok_units + 16 * ((lane % LPR) ^ swizzle<D>(rw * WR + r));
+    }
+  }
+  __device__ static __forceinline__ uint64_t load_aligned(const KvView& kv, const Bases& b, const uint32_t (&piece)[NLD], int entry,
+                                                          int base, int end, int rw, u32x4 (&kr)[NLD], u32x4 (&vr)[NLD]) {
     const int lane = threadIdx.x & 63;
     const bool ok = (uint32_t)entry < (uint32_t)kv.npages && base + (lane & (RW - 1)) * WR < end;
     const uint32_t bits = (uint32_t)__ballot(ok) & ((1u << RW) - 1);
@@ -412,13 +475,20 @@ struct Kernel {
     const uint32_t within = (uint32_t)s0 - fast_quot(kv.by_page, (uint32_t)s0) * (uint32_t)kv.page;
     const uint32_t first = page * kv.page_units + within * kv.tok_units;
     const int rows = (bits >> rw & 1) ? end - s0 : 0;
-    uint32_t u[NLD];
+    if (rows >= WR) {
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-      const int r = i * RPI + lane / LPR;
-      u[i] = r < rows ? first + (uint32_t)r * kv.tok_units : kNoRow;
+      for (int i = 0; i < NLD; ++i) {
+        kr[i] = buffer_row(b.kb, first + piece[i]);
+        vr[i] = buffer_row(b.vb, first + piece[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NLD; ++i) {
+        const uint32_t at = i * RPI + lane / LPR < rows ? first + piece[i] : kNoRow;
+        kr[i] = buffer_row(b.kb, at);
+        vr[i] = buffer_row(b.vb, at);
+      }
     }
-    load_units(b, u, rw, kr, vr);
     uint64_t valid = ~0ull;
     if (bits != (1u << RW) - 1) {
       valid = 0;
@@ -449,7 +519,7 @@ struct Kernel {
     }
   }
 
-  // scores of one step: S^T tiles of this wave's rows
+  // scores of KS keys: S^T tiles of this wave's rows
   __device__ static __forceinline__ void score(const uint16_t* ks, const u32x4 (&qf)[QF], Acc (&s)[ST]) {
     const int lane = threadIdx.x & 63;
     const int r = lane % MR, g = lane / MR;
@@ -503,9 +573,9 @@ struct Kernel {
     }
     return w;
   }
-  static constexpr int NP = MR == 32 ? NK / 16 : NK / 32;
+  static constexpr int NP = MR == 32 ? KS / 16 : KS / 32;
 
-  // O^T += V^T P^T over one step
+  // O^T += V^T P^T over KS keys
   __device__ static __forceinline__ void accumulate(const uint16_t* vs, const Acc (&s)[ST], Acc (&o)[OT]) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -519,8 +589,7 @@ struct Kernel {
   // are not all finite: the product would carry 0 * inf = NaN into rows that do
   // not see them. The finite values are multiplied as above; then, for +inf, -inf
   // and NaN in turn, a product of marks counts those that each row sees.
-  __device__ static __forceinline__ void accumulate_guarded(const uint16_t* vs, Acc (&s)[ST], Acc (&o)[OT], int base, int lo,
-                                                         int hi, uint64_t valid) {
+  __device__ static __forceinline__ void accumulate_guarded(const uint16_t* vs, Acc (&s)[ST], Acc (&o)[OT], uint32_t see) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -537,8 +606,7 @@ struct Kernel {
     for (int i = 0; i < ST; ++i)
 #pragma unroll
       for (int j = 0; j < AR; ++j) {
-        const int key = i * MR + acc_row(j, lane);
-        s[i][j] = base + key >= lo && base + key < hi && ((valid >> key) & 1) ? 1.f : 0.f;
+        s[i][j] = see >> (i * MR + acc_row(j, lane)) & 1 ? 1.f : 0.f;
       }
     constexpr uint32_t one = HALF ? 0x3c00u : 0x3f80u, inf = HALF ? 0x7c00u : 0x7f80u;
 #pragma unroll 1
@@ -571,48 +639,60 @@ struct Kernel {
     }
   }
 
-  // Cap and bias; the scores leave in units of log2.
-  __device__ static __forceinline__ void shape(const AttendArgs& a, Acc (&s)[ST], const Rows& row, const int32_t* ids, int base,
-                                               int token) {
-    const int lane = threadIdx.x & 63;
-    if (a.cap > 0.f) {
-      const float c = a.scale / a.cap, cap2 = a.cap * kLog2e;
-      float big = 0.f;
+  // the largest magnitude of this lane's scores
+  __device__ static __forceinline__ float largest(const Acc (&s)[ST]) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < ST; ++i)
+#pragma unroll
+      for (int j = 0; j < AR; ++j) big = fmaxf(big, fabsf(s[i][j]));
+    return big;
+  }
+  __device__ static __forceinline__ float highest(const Acc (&s)[ST]) {
+    float mx = s[0][0];
+#pragma unroll
+    for (int i = 0; i < ST; ++i)
+#pragma unroll
+      for (int j = 0; j < AR; ++j) mx = fmaxf(mx, s[i][j]);
+    return mx;
+  }
+
+  // Moves the reference m where a row's maximum mx (of this lane's row, over all of
+  // its keys of the step) passes it by more than slack.
+  __device__ static __forceinline__ void follow(float mx, float slack, float sc, float& m, float& sum, Acc (&o)[OT]) {
+    if (!__any(mx > m + slack)) return;
+    const float mn = fmaxf(m, mx);
+    const float alpha = __builtin_amdgcn_exp2f((m - (mn == -__builtin_inff() ? 0.f : mn)) * sc);
+    sum *= alpha;
+#pragma unroll
+    for (int i = 0; i < OT; ++i)
+#pragma unroll
+      for (int j = 0; j < AR; ++j) o[i][j] *= alpha;
+    m = mn;
+  }
+
+  __device__ static __forceinline__ void cap_far(const FarCap& g, float off, Acc (&s)[ST]) {
+    if (g.choose) {
 #pragma unroll
       for (int i = 0; i < ST; ++i)
 #pragma unroll
-        for (int j = 0; j < AR; ++j) big = fmaxf(big, fabsf(s[i][j]));
-      const float g = cap2 * c, c2 = c * c;
-      const float k0 = g * kTanh[0], k1 = g * kTanh[1] * c2, k2 = g * kTanh[2] * c2 * c2, k3 = g * kTanh[3] * c2 * c2 * c2,
-                  k4 = g * kTanh[4] * c2 * c2 * c2 * c2;
-      // coefficients of powers of the raw score stay normal numbers for |c| in this range
-      const bool mild = c > 1e-4f && c < 1e4f;
-      if (mild && !__any(!(big * c <= 0.5f))) {
+        for (int j = 0; j < AR; ++j) s[i][j] = g.chosen(s[i][j], off);
+    } else {
 #pragma unroll
-        for (int i = 0; i < ST; ++i)
+      for (int i = 0; i < ST; ++i)
 #pragma unroll
-          for (int j = 0; j < AR; ++j) {
-            const float x = s[i][j], z = x * x;
-            s[i][j] = x * (k0 + z * (k1 + z * (k2 + z * (k3 + z * k4))));
-          }
-      } else if (a.cap <= kPlainCap) {
-        const float e = c * (2.f * kLog2e);
-#pragma unroll
-        for (int i = 0; i < ST; ++i)
-#pragma unroll
-          for (int j = 0; j < AR; ++j)
-            s[i][j] = cap2 - 2.f * cap2 * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s[i][j] * e));
-      } else {
-#pragma unroll
-        for (int i = 0; i < ST; ++i)
-#pragma unroll
-          for (int j = 0; j < AR; ++j) {
-            const float y = s[i][j] * c, z = y * y;
-            const float far = 1.f - 2.f * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(y * (2.f * kLog2e)));
-            const float near = y * (kTanh[0] + z * (kTanh[1] + z * (kTanh[2] + z * (kTanh[3] + z * kTanh[4]))));
-            s[i][j] = cap2 * (fabsf(y) < 0.5f ? near : far);
-          }
-      }
+        for (int j = 0; j < AR; ++j) s[i][j] = g.plain(s[i][j], off);
+    }
+  }
+
+  // Cap and bias; the scores leave in units of log2.
+  __device__ static __forceinline__ void shape(const AttendArgs& a, Acc (&s)[ST], const Rows& row, const int32_t* ids, int base,
+                                               int token, int sub) {
+    const int lane = threadIdx.x & 63;
+    if (a.cap > 0.f) {
+      const float c = a.scale / a.cap;
+      const FarCap g = far_cap(a.cap, c);
+      cap_far(g, 0.f, s);
     } else {
       const float c = a.scale * kLog2e;
 #pragma unroll
@@ -627,7 +707,7 @@ struct Kernel {
       for (int i = 0; i < ST; ++i)
 #pragma unroll
         for (int j = 0; j < AR; ++j)
-          s[i][j] -= slope * fabsf((float)(row.pos - __shfl(token, i * MR + acc_row(j, lane), 64)));
+          s[i][j] -= slope * fabsf((float)(row.pos - __shfl(token, sub * KS + i * MR + acc_row(j, lane), 64)));
     } else {
       const int first = row.pos - base - acc_row(0, lane);
       if (__any(first > (1 << 23) || first < -(1 << 23))) {
@@ -645,14 +725,14 @@ struct Kernel {
     }
   }
 
-  // Bits from b on of 64.
-  __device__ static __forceinline__ uint64_t bits_from(int b) { return b >= 64 ? 0 : ~0ull << (b > 0 ? b : 0); }
+  // Bits from b on of 32.
+  __device__ static __forceinline__ uint32_t bits_from(int b) { return b >= 32 ? 0u : ~0u << (b > 0 ? b : 0); }
   // -inf for the scores of keys whose bit in `see` is not set.
-  __device__ static __forceinline__ void hide(uint64_t see, Acc (&s)[ST]) {
+  __device__ static __forceinline__ void hide(uint32_t see, Acc (&s)[ST]) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < ST; ++i) {
-      const uint32_t w = (uint32_t)(see >> (i * MR)) >> acc_row(0, lane);
+      const uint32_t w = see >> (i * MR) >> acc_row(0, lane);
 #pragma unroll
       for (int j = 0; j < AR; ++j)
         s[i][j] = w >> acc_row(j, 0) & 1 ? s[i][j] : -__builtin_inff();
@@ -688,13 +768,13 @@ struct Kernel {
   // that do not see it (0 * inf). Where the queries of a part do not see the same
   // keys (odd is not null) and anything comes out infinite or NaN, *odd is set
   // and the guarded form computes the workgroup's parts again.
-  __device__ static __forceinline__ void run_part(ArgPtr ap, const Part& p, unsigned char* lds, const Interval* known,
+  __device__ static __forceinline__ void run_part(ArgPtr ap, const Part& p, unsigned char* lds, const Known& known,
                                                   int* odd) {
     const AttendArgs& a = fresh(ap);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int rw = wave % RW, kw = wave / RW;
-    const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
+    const int kvh = p.hh / a.head_tiles;
     const Span sp = span_of(a, known, p.t0, p.nq);
     // p.tile1 * KT may pass the last key (and 2^31): 64 bits
     const int begin = sp.lo + p.tile0 * KT;
@@ -703,46 +783,42 @@ struct Kernel {
 
     // this lane's row
     const int r = rw * MR + lane % MR;
-    const int qi = (int)fast_quot(a.by_gw, (uint32_t)r);
+    int64_t row_t;
+    int row_head;
+    const bool active = row_of(a, p, r, row_t, row_head);
     Rows row;
-    row.head = kvh * a.group + hb * a.gw + (r - qi * a.gw);
-    row.active = qi < p.nq && row.head < (kvh + 1) * a.group;
-    row.t = p.t0 + qi;
     row.lo = row.hi = 0;
     row.slope = 0.f;
     row.pos = 0;
-    if (row.active) {
-      const Interval q = interval_of(a, known, row.t);
+    if (active) {
+      const Interval q = known[row_t];
       row.lo = a.idx ? 0 : q.lo;
       row.hi = a.idx ? a.topk : q.hi;
-      if (EXTRA && a.slopes) {
-        const QueryInfo z = query_info(a, row.t);
-        row.slope = a.slopes[row.head];
-        row.pos = z.pos - z.kbase;
-      }
+      row.pos = q.pos;
+      if (MODE == kBias && a.slopes) row.slope = a.slopes[row_head];
     }
     // visible token ids of selected tokens (one query a segment; also for waves
     // without a row, which load for the others)
     const int32_t* ids = nullptr;
     int id_lo = 0, id_hi = 0x7fffffff;
     if (a.idx) {
-      const Interval q = interval_of(a, known, p.t0);
+      const Interval q = known[p.t0];
       ids = a.idx + p.t0 * a.topk;
       id_lo = uniform(q.lo);
       id_hi = uniform(q.hi);
     }
     // keys that every row of this wave sees, and keys that any of them sees
-    const int all_lo = uniform(wave_max_of(row.active ? row.lo : 0));
-    const int all_hi = uniform(wave_min_of(row.active ? row.hi : 0x7fffffff));
-    const int any_lo = uniform(wave_min_of(row.active ? row.lo : 0x7fffffff));
-    const int any_hi = uniform(wave_max_of(row.active ? row.hi : 0));
+    const int all_lo = uniform(wave_max_of(active ? row.lo : 0));
+    const int all_hi = uniform(wave_min_of(active ? row.hi : 0x7fffffff));
+    const int any_lo = uniform(wave_min_of(active ? row.lo : 0x7fffffff));
+    const int any_hi = uniform(wave_max_of(active ? row.hi : 0));
 
     u32x4 qf[QF];
     {
-      const uint16_t* src = a.q + row.t * a.q_ts + row.head * a.q_hs + 8 * (lane / MR);
+      const uint16_t* src = a.q + row_t * a.q_ts + row_head * a.q_hs + 8 * (lane / MR);
 #pragma unroll
       for (int f = 0; f < QF; ++f) {
-        if (row.active) qf[f] = *reinterpret_cast<const u32x4*>(src + f * (512 / MR));
+        if (active) qf[f] = *reinterpret_cast<const u32x4*>(src + f * (512 / MR));
         else qf[f] = u32x4{0u, 0u, 0u, 0u};
       }
     }
@@ -753,7 +829,7 @@ struct Kernel {
     for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int j = 0; j < AR; ++j) o[i][j] = 0.f;
-    const float sc = EXTRA ? 1.f : a.scale * kLog2e;
+    const float sc = MODE == kPlain ? a.scale * kLog2e : 1.f;
 
     uint16_t* buf = reinterpret_cast<uint16_t*>(lds);
     constexpr int GB = NK * D;             // elements of one tensor of one group's step
@@ -770,9 +846,11 @@ struct Kernel {
     int far = -1, cur_token = -1;
     uint64_t valid = 0;
     int entry = 0;
-    if (ALIGNED) {
+    uint32_t piece[NLD];
+    if constexpr (ALIGNED) {
+      piece_offsets(a.kv, rw, piece);
       if (mine > 0) {
-        valid = load_aligned(a.kv, bases, page_entry(a.kv, table, sp.seq, k0, end), k0, end, rw, kr, vr);
+        valid = load_aligned(a.kv, bases, piece, page_entry(a.kv, table, sp.seq, k0, end), k0, end, rw, kr, vr);
         entry = page_entry(a.kv, table, sp.seq, k0 + KT, end);
         store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
       }
@@ -792,16 +870,18 @@ struct Kernel {
     // the maximum is followed lazily: the reference m moves when a row's maximum
     // passes it by more than 2^8, so that rescaling is rare after the first step
     const float slack = 8.f / sc;
+    const float cap_c = MODE == kCap ? a.scale / a.cap : 0.f;
+    const bool near_holds = near_cap_holds(cap_c);
     sync_rows();
     for (int it = 0; it < mine; ++it) {
       const bool more = it + 1 < mine;
       uint64_t next_valid = 0;
       int next_token = -1;
-      if (ALIGNED) {
+      if constexpr (ALIGNED) {
         if (more) {
           const int now = entry;
           entry = page_entry(a.kv, table, sp.seq, k0 + (it + 2) * KT, end);
-          next_valid = load_aligned(a.kv, bases, now, k0 + (it + 1) * KT, end, rw, kr, vr);
+          next_valid = load_aligned(a.kv, bases, piece, now, k0 + (it + 1) * KT, end, rw, kr, vr);
         }
       } else if (more) {
         const uint32_t unit = row_unit(a.kv, nxt);
@@ -812,42 +892,60 @@ struct Kernel {
         load_rows(bases, unit, rw, kr, vr);
       }
       const uint16_t* ks = buf + (S::buffers > 1 ? (it & 1) * SB : 0) + kw * 2 * GB;
-      const int base = k0 + it * KT;
-      if (base < any_hi && base + NK > any_lo && valid != 0) {
+#pragma unroll
+      for (int sub = 0; sub < NS; ++sub) {
+        // one run of KS keys after the other: their registers are the same
+        if (sub > 0) __builtin_amdgcn_sched_barrier(0);
+        const int base = k0 + it * KT + sub * KS;
+        const uint32_t have = (uint32_t)(valid >> (sub * KS));
+        if (base >= any_hi || base + KS <= any_lo || have == 0) continue;
         Acc s[ST];
-        score(ks, qf, s);
-        if constexpr (EXTRA) shape(a, s, row, ids, base, cur_token);
-        constexpr uint64_t kAll = NK == 64 ? ~0ull : (1ull << (NK & 63)) - 1;
-        if (!(valid == kAll && base >= all_lo && base + NK <= all_hi))
-          hide(valid & bits_from(row.lo - base) & ~bits_from(row.hi - base), s);
-        float mx = s[0][0];
+        score(ks + sub * KS * D, qf, s);
+        const bool full = have == ~0u && base >= all_lo && base + KS <= all_hi;
+        const uint32_t see = have & bits_from(row.lo - base) & ~bits_from(row.hi - base);
+        if constexpr (MODE == kBias) shape(a, s, row, ids, base, cur_token, sub);
+        if (!full) hide(see, s);
+        float mx = over_rows_max(highest(s));
+        if constexpr (MODE == kCap) {
+          // the cap grows with the score, so the maximum is taken before it and the
+          // reference is subtracted in its last step
+          const bool near = near_holds && full && !__any(!(largest(s) * cap_c <= kNear));
+          const NearCap f = near_cap(a.cap, cap_c);
+          const FarCap g = far_cap(a.cap, cap_c);
+          follow(near ? mx * f.factor(mx) : g.plain(mx, 0.f), slack, sc, m, sum, o);
+          const float off = m == -__builtin_inff() ? 0.f : m;
+          if (near) {
 #pragma unroll
-        for (int i = 0; i < ST; ++i)
+            for (int i = 0; i < ST; ++i)
 #pragma unroll
-          for (int j = 0; j < AR; ++j) mx = fmaxf(mx, s[i][j]);
-        mx = over_rows_max(mx);
-        if (__any(mx > m + slack)) {
-          const float mn = fmaxf(m, mx);
-          const float alpha = __builtin_amdgcn_exp2f((m - (mn == -__builtin_inff() ? 0.f : mn)) * sc);
-          sum *= alpha;
+              for (int j = 0; j < AR; ++j) s[i][j] = __builtin_fmaf(s[i][j], f.factor(s[i][j]), -off);
+          } else {
 #pragma unroll
-          for (int i = 0; i < OT; ++i)
+            for (int i = 0; i < ST; ++i)
 #pragma unroll
-            for (int j = 0; j < AR; ++j) o[i][j] *= alpha;
-          m = mn;
+              for (int j = 0; j < AR; ++j) s[i][j] = g.plain(s[i][j], off);
+            if (!full) hide(see, s);   // tanh(-inf) is finite
+          }
+        } else {
+          follow(mx, slack, sc, m, sum, o);
+          const float off = (m == -__builtin_inff() ? 0.f : m) * sc;
+#pragma unroll
+          for (int i = 0; i < ST; ++i)
+#pragma unroll
+            for (int j = 0; j < AR; ++j) s[i][j] = s[i][j] * sc - off;
         }
-        const float off = (m == -__builtin_inff() ? 0.f : m) * sc;
         float add[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < ST; ++i)
 #pragma unroll
           for (int j = 0; j < AR; ++j) {
-            s[i][j] = __builtin_amdgcn_exp2f(s[i][j] * sc - off);
+            s[i][j] = __builtin_amdgcn_exp2f(s[i][j]);
             add[j & 1] += s[i][j];
           }
         sum += add[0] + add[1];
-        if constexpr (GUARD) accumulate_guarded(ks + GB, s, o, base, row.lo, row.hi, valid);
-        else accumulate(ks + GB, s, o);
+        const uint16_t* vs = ks + GB + sub * KS * D;
+        if constexpr (GUARD) accumulate_guarded(vs, s, o, see);
+        else accumulate(vs, s, o);
       }
       valid = next_valid;
       cur_token = next_token;
@@ -858,15 +956,14 @@ struct Kernel {
       }
       sync_rows();
     }
-    finish(fresh(ap), p, sp, lds, odd, row, r, kw, rw, m * sc, sum, o);
+    finish(fresh(ap), p, sp, lds, odd, r, kw, m * sc, sum, o);
   }
 
   // The end of a part: joins the groups of waves and writes the rows.
   __device__ static __forceinline__ void finish(const AttendArgs& a, const Part& p, const Span& sp, unsigned char* lds,
-                                                int* odd, const Rows& row, int r, int kw, int rw, float m, float sum,
+                                                int* odd, int r, int kw, float m, float sum,
                                                 Acc (&o)[OT]) {
     const int lane = threadIdx.x & 63;
-    const int kvh = p.hh / a.head_tiles, hb = p.hh % a.head_tiles;
     if constexpr (!GUARD) {
       if (odd && sp.some < sp.hi - sp.lo) {
         float z = 0.f;
@@ -879,12 +976,14 @@ struct Kernel {
     }
     sum = over_rows_sum(sum);
     if constexpr (KW == 1) {
-      if (row.active) {
+      int64_t t;
+      int head;
+      if (row_of(a, p, r, t, head)) {
 #pragma unroll
         for (int i = 0; i < OT; ++i)
 #pragma unroll
           for (int j = 0; j < AR; j += 4)
-            emit(a, p, row.t, row.head, r, i * MR + acc_row(j, lane), m, sum,
+            emit(a, p, t, head, r, i * MR + acc_row(j, lane), m, sum,
                  floatx4{o[i][j], o[i][j + 1], o[i][j + 2], o[i][j + 3]});
       }
     } else {
@@ -919,28 +1018,28 @@ struct Kernel {
       __syncthreads();
       for (int e = threadIdx.x; e < R * (D / 4); e += TH) {
         const int rr = e / (D / 4), d0 = (e % (D / 4)) * 4;
-        const int q = (int)fast_quot(a.by_gw, (uint32_t)rr);
-        const int head = kvh * a.group + hb * a.gw + (rr - q * a.gw);
-        if (q >= p.nq || head >= (kvh + 1) * a.group) continue;
+        int64_t t;
+        int head;
+        if (!row_of(a, p, rr, t, head)) continue;
         floatx4 x = *reinterpret_cast<const floatx4*>(ob + rr * (D + 4) + d0);
 #pragma unroll
         for (int i = 1; i < KW; ++i) x += *reinterpret_cast<const floatx4*>(ob + (i * R + rr) * (D + 4) + d0);
-        emit(a, p, p.t0 + q, head, rr, d0, fin[rr * 2], fin[rr * 2 + 1], x);
+        emit(a, p, t, head, rr, d0, fin[rr * 2], fin[rr * 2 + 1], x);
       }
       __syncthreads();   // the next part's first rows go to the same memory
     }
   }
 
   // Queries from t0 on that belong to t0's sequence and row tile.
-  __device__ static __forceinline__ int run_length(const AttendArgs& a, const Interval* known, int64_t t0) {
+  __device__ static __forceinline__ int run_length(const AttendArgs& a, const Known& known, int64_t t0) {
     const int lane = threadIdx.x & 63;
     int64_t end = (t0 / a.qt + 1) * a.qt;
     if (end > a.T) end = a.T;
     const int n = (int)(end - t0);
     if (n <= 1) return n;
-    const int seq = interval_of(a, known, t0).seq;
+    const int seq = known[t0].seq;
     for (int i = 0; i < n; i += 64) {
-      const bool other = i + lane < n && interval_of(a, known, t0 + i + lane).seq != seq;
+      const bool other = i + lane < n && known[t0 + i + lane].seq != seq;
       const uint64_t b = __ballot(other);
       if (b) return __builtin_amdgcn_readfirstlane(i + (int)__builtin_ctzll(b));
     }
@@ -949,9 +1048,9 @@ struct Kernel {
 
   // Key tiles before each query's segment: cum[t] for t < T, and their sum; the
   // queries' intervals.
-  __device__ static __forceinline__ int64_t make_plan(const AttendArgs& a, int64_t* cum, Interval* known) {
+  __device__ static __forceinline__ int64_t make_plan(const AttendArgs& a, int64_t* cum, const Known& known) {
     const int T = (int)a.T, tid = threadIdx.x;
-    for (int t = tid; t < T; t += TH) known[t] = interval_of(a, nullptr, t);
+    for (int t = tid; t < T; t += TH) known.at[t] = interval_of(a, t);
     __syncthreads();
     constexpr int PER = kPlanMax / TH;       // queries a thread sums
     int64_t w[PER];
@@ -1008,12 +1107,10 @@ struct Kernel {
     return total;
   }
 
-  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int64_t* cum, Interval* intervals, int* odd) {
+  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int64_t* cum, Interval* intervals, int* odd, unsigned block) {
     const AttendArgs& a = fresh(ap);
     const bool mixed = a.odd != nullptr;
-    if (GUARD) {
-      if (!a.odd[blockIdx.x]) return;
-    } else if (mixed) {
+    if (!GUARD && mixed) {
       if (threadIdx.x == 0) *odd = 0;
       __syncthreads();
     }
@@ -1022,19 +1119,23 @@ struct Kernel {
     const bool planned = a.planned;
     int64_t total = 0, u, u1;
     int hh = 0;
+    Known known{intervals, 0};
     if (planned) {
-      total = uniform(make_plan(a, cum, intervals));
+      total = uniform(make_plan(a, cum, known));
       const int64_t units = total * NH;
-      u = blockIdx.x * units / a.G;
-      u1 = ((int64_t)blockIdx.x + 1) * units / a.G;
-      if (blockIdx.x == 0 && !GUARD) publish_plan(a, cum, intervals, total);
+      u = block * units / a.G;
+      u1 = ((int64_t)block + 1) * units / a.G;
+      if (block == 0 && !GUARD) publish_plan(a, cum, known, total);
     } else {
       // one workgroup per row tile, the last queries (the longest of a causal prompt) first
       const unsigned ntiles = (unsigned)((T + a.qt - 1) / a.qt);
-      const unsigned tile = ntiles - 1 - blockIdx.x / (unsigned)NH;
-      hh = blockIdx.x % (unsigned)NH;
+      const unsigned tile = ntiles - 1 - block / (unsigned)NH;
+      hh = block % (unsigned)NH;
       u = (int64_t)tile * a.qt;
       u1 = min((int64_t)T, u + a.qt);
+      known.t0 = u;
+      for (int i = threadIdx.x; i < (int)(u1 - u); i += TH) intervals[i] = interval_of(a, u + i);
+      __syncthreads();
     }
     while (u < u1) {
       Part p;
@@ -1049,7 +1150,7 @@ struct Kernel {
         lo = uniform(lo);
         const int64_t first = uniform(cum[lo]);
         p.t0 = lo;
-        p.nq = run_length(a, intervals, lo);
+        p.nq = run_length(a, known, lo);
         const int next = lo + p.nq;
         const int tiles = (int)((next < T ? uniform(cum[next]) : total) - first);
         const int64_t in = u - first * NH;
@@ -1058,11 +1159,11 @@ struct Kernel {
         const int64_t left = u1 - u;
         p.tile1 = left < tiles - p.tile0 ? p.tile0 + (int)left : tiles;
         p.whole = p.tile0 == 0 && p.tile1 == tiles;
-        p.slot = (int)(2 * blockIdx.x + (p.tile0 > 0 ? 0 : 1));
+        p.slot = (int)(2 * block + (p.tile0 > 0 ? 0 : 1));
         u += p.tile1 - p.tile0;
       } else {
         p.t0 = u;
-        p.nq = run_length(a, nullptr, u);
+        p.nq = run_length(a, known, u);
         p.hh = hh;
         p.tile0 = 0;
         p.tile1 = 0x7fffffff;
@@ -1070,16 +1171,16 @@ struct Kernel {
         p.slot = 0;
         u += p.nq;
       }
-      run_part(ap, p, lds, planned ? intervals : nullptr, mixed ? odd : nullptr);
+      run_part(ap, p, lds, known, mixed ? odd : nullptr);
     }
     if (!GUARD && mixed) {
       __syncthreads();
-      if (threadIdx.x == 0) fresh(ap).odd[blockIdx.x] = *odd;
+      if (threadIdx.x == 0) fresh(ap).odd[block] = *odd;
     }
   }
 
   // What the join needs: every query takes the entry of its segment.
-  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int64_t* cum, const Interval* known,
+  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int64_t* cum, const Known& known,
                                                      int64_t total) {
     for (int t = threadIdx.x; t < (int)a.T; t += TH) {
       int t0 = t, next = t + 1;
@@ -1096,7 +1197,7 @@ struct Kernel {
   }
 };
 
-template <bool HALF, int D, int R, bool EXTRA, bool ALIGNED, bool GUARD>
+template <bool HALF, int D, int R, int MODE, bool ALIGNED, bool GUARD>
 __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shape<D, R>::threads / 256 > 0
                                                           ? Shape<D, R>::per_cu * Shape<D, R>::threads / 256
                                                           : 1)) void attend_kernel(AttendArgs) {
@@ -1105,29 +1206,45 @@ __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shap
   __shared__ Interval intervals[kPlanMax];
   __shared__ int odd;
   // the arguments are read where they lie (see fresh)
-  Kernel<HALF, D, R, EXTRA, ALIGNED, GUARD>::body((ArgPtr)__builtin_amdgcn_kernarg_segment_ptr(), lds, cum, intervals, &odd);
+  const ArgPtr args = (ArgPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  if constexpr (GUARD) {
+    // each workgroup looks over the words of a run of them at once
+    const unsigned blocks = args->blocks, per = (blocks + gridDim.x - 1) / gridDim.x;
+    for (unsigned b0 = blockIdx.x * per; b0 < blocks && b0 < (blockIdx.x + 1) * per; b0 += blockDim.x) {
+      const unsigned n = min(min(blocks, (blockIdx.x + 1) * per) - b0, blockDim.x);
+      if (!__syncthreads_or(threadIdx.x < n && args->odd[b0 + threadIdx.x])) continue;
+      for (unsigned b = b0; b < b0 + n; ++b) {
+        if (!args->odd[b]) continue;
+        __syncthreads();
+        Kernel<HALF, D, R, MODE, ALIGNED, GUARD>::body(args, lds, cum, intervals, &odd, b);
+      }
+    }
+  } else {
+    Kernel<HALF, D, R, MODE, ALIGNED, GUARD>::body(args, lds, cum, intervals, &odd, blockIdx.x);
+  }
 }
 
 template <bool HALF, int D, int R>
 hipError_t launch_shape(const AttendArgs& a, unsigned blocks, hipStream_t st) {
   const dim3 grid(blocks), block(Shape<D, R>::threads);
-  const bool extra = a.cap > 0.f || a.slopes;
-  if constexpr (Shape<D, R>::RW > 1) {
-    if (a.align > 1) {
-      if (extra)
-        hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, true, false>), grid, block, 0, st, a);
-      else
-        hipLaunchKernelGGL((attend_kernel<HALF, D, R, false, true, false>), grid, block, 0, st, a);
+  const int mode = a.slopes || a.cap > kPlainCap ? kBias : a.cap > 0.f ? kCap : kPlain;
+#define MISA_ATTEND(MODE_, ALIGNED_) \
+  hipLaunchKernelGGL((attend_kernel<HALF, D, R, MODE_, ALIGNED_, false>), grid, block, 0, st, a)
+  if (a.align > 1) {
+    if constexpr (Shape<D, R>::RW > 1) {
+      if (mode == kPlain) MISA_ATTEND(kPlain, true);
+      if (mode == kCap) MISA_ATTEND(kCap, true);
+      if (mode == kBias) MISA_ATTEND(kBias, true);
     }
+  } else {
+    if (mode == kPlain) MISA_ATTEND(kPlain, false);
+    if (mode == kCap) MISA_ATTEND(kCap, false);
+    if (mode == kBias) MISA_ATTEND(kBias, false);
   }
-  if (a.align == 1) {
-    if (extra)
-      hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, false, false>), grid, block, 0, st, a);
-    else
-      hipLaunchKernelGGL((attend_kernel<HALF, D, R, false, false, false>), grid, block, 0, st, a);
-  }
+#undef MISA_ATTEND
   // workgroups that met values that are not finite where not all rows see them
-  if (a.odd) hipLaunchKernelGGL((attend_kernel<HALF, D, R, true, false, true>), grid, block, 0, st, a);
+  if (a.odd)
+    hipLaunchKernelGGL((attend_kernel<HALF, D, R, kBias, false, true>), dim3(blocks < 256 ? blocks : 256), block, 0, st, a);
   return hipGetLastError();
 }
 

@@ -57,6 +57,7 @@ struct AttendArgs {
   // one word a workgroup, set if its parts have to be computed again by the
   // guarded form; null where all rows of a part see the same keys
   int32_t* odd;
+  uint32_t blocks;          // workgroups of the launch
   // planned batches
   int32_t planned;
   int32_t G;                // workgroups

@@ -52,9 +52,9 @@ def one_query(q, k, v, scale, cap, slopes, dist, dtype):
         x = cap * torch.tanh(x / cap)
         # tanh = 1 - 2 / (1 + t), t = exp2(..): the exponent's rounding moves it by at most |y| (1 - tanh^2) e < 0.45 e,
         # exp2 (2 e) by 2 t / (1 + t)^2 2 e <= e, the sum (e) and the reciprocal (2 e) by 2 / (1 + t) 3 e <= 6 e, the
-        # last difference by e: under 9 e of one, times the cap. Caps above 256 take y P(y^2) up to |y| = 1/2, fitted to
+        # last difference by e: under 9 e of one, times the cap. Caps above 256 take y P(y^2) up to |y| = 0.35, fitted to
         # e and rounded in each of its steps: under 9 e of the value.
-        dx = dx + 9 * E * torch.where((x.abs() > 0.4 * cap) | (cap <= 256), torch.full_like(x, float(cap)), x.abs())
+        dx = dx + 9 * E * torch.where((x.abs() > 0.3 * cap) | (cap <= 256), torch.full_like(x, float(cap)), x.abs())
     if slopes is not None:
         b = slopes.double()[:, None] * dist[None, :]
         x = x - b
