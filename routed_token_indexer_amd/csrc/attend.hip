@@ -12,7 +12,7 @@ constexpr int kCUs = 256;
 // What the join reads of a pass.
 struct Pass {
   const PlanEntry* plan;    // null: every row is whole
-  const int64_t* plan_total;
+  const int32_t* plan_total;
   const float* part_out;
   const float* part_ml;
   const float* whole_out;   // [T][Hq][D] and [T][Hq], for rows that are whole
@@ -47,8 +47,8 @@ __device__ __forceinline__ Parts parts_of(const Pass& p, int64_t t, int head) {
   const PlanEntry e = p.plan[t];
   const int in = head % p.group;
   const int hh = head / p.group * p.head_tiles + in / p.gw;
-  x.units = *p.plan_total * p.NH;
-  x.u0 = e.first * p.NH + (int64_t)hh * e.tiles;
+  x.units = (int64_t)*p.plan_total * p.NH;
+  x.u0 = (int64_t)e.first * p.NH + (int64_t)hh * e.tiles;
   x.r = (int)(t - e.t0) * p.gw + in % p.gw;
   x.i0 = (int)(((x.u0 + 1) * p.G - 1) / x.units);
   x.i1 = (int)(((x.u0 + e.tiles) * p.G - 1) / x.units);
@@ -214,7 +214,10 @@ int attend_rows(int64_t T, int64_t nseq, int group, int d, bool single) {
   return rows <= 16 && d < 256 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
 }
 
-bool attend_planned(int64_t T) { return T <= kPlanMax; }
+// (32 keys a tile is the least of all shapes: the tiles of all segments fit 31 bits)
+bool attend_planned(int64_t T, int64_t most_keys) {
+  return T <= kPlanMax && T * (most_keys / 32 + 2) < (int64_t(1) << 31);
+}
 
 int attend_groups(int d, int R) { return kCUs * (d == 64 ? per_cu<64>(R) : d == 128 ? per_cu<128>(R) : per_cu<256>(R)); }
 
@@ -230,15 +233,17 @@ static Tile tile_of(int group, int R, bool single) {
   return t;
 }
 
-static int64_t blocks_of(int64_t T, int heads, int d, int R, const Tile& t) {
-  return attend_planned(T) ? attend_groups(d, R) : (T + t.qt - 1) / t.qt * heads * t.head_tiles;
+static int64_t blocks_of(int64_t T, int heads, int d, int R, const Tile& t, bool planned) {
+  return planned ? attend_groups(d, R) : (T + t.qt - 1) / t.qt * heads * t.head_tiles;
 }
 
 size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, bool mixed) {
   const Tile t = tile_of(Hq / heads, R, single);
   size_t b = 0;
-  if (mixed) b += up((size_t)blocks_of(T, heads, d, R, t) * 4);
-  if (!attend_planned(T)) return b;
+  const int64_t direct = blocks_of(T, heads, d, R, t, false);
+  if (T > kPlanMax) return mixed ? up((size_t)direct * 4) : 0;
+  const int64_t most = direct > attend_groups(d, R) ? direct : attend_groups(d, R);
+  if (mixed) b += up((size_t)most * 4);
   const size_t slots = 2 * (size_t)attend_groups(d, R);
   return b + up(slots * R * d * 4) + up(slots * R * 8) + up((size_t)T * sizeof(PlanEntry)) + 256;
 }
@@ -256,14 +261,14 @@ void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws) {
   // page up once a group (a row cache is one page a sequence)
   const int wr = d == 64 ? shared_rows_of<64>(R) : d == 128 ? shared_rows_of<128>(R) : shared_rows_of<256>(R);
   a.align = wr && !a.idx && a.kv.unit_shift == 0 && (!a.kv.table || a.kv.page % wr == 0) ? wr : 1;
-  a.planned = attend_planned(a.T);
+  a.planned = attend_planned(a.T, a.idx ? a.topk : a.kv.Lmax);
   a.G = a.planned ? attend_groups(d, R) : 0;
   a.odd = nullptr;
-  a.blocks = (uint32_t)blocks_of(a.T, a.Hkv, d, R, t);
+  a.blocks = (uint32_t)blocks_of(a.T, a.Hkv, d, R, t, a.planned);
   char* p = static_cast<char*>(ws);
   if (mixed) {
     a.odd = reinterpret_cast<int32_t*>(p);
-    p += up((size_t)blocks_of(a.T, a.Hkv, d, R, t) * 4);
+    p += up((size_t)a.blocks * 4);
   }
   if (!a.planned) return;
   const size_t slots = 2 * (size_t)a.G;
@@ -273,11 +278,11 @@ void attend_setup(AttendArgs& a, int R, bool single, bool mixed, void* ws) {
   p += up(slots * R * 8);
   a.plan = reinterpret_cast<PlanEntry*>(p);
   p += up((size_t)a.T * sizeof(PlanEntry));
-  a.plan_total = reinterpret_cast<int64_t*>(p);
+  a.plan_total = reinterpret_cast<int32_t*>(p);
 }
 
 int64_t attend_blocks(const AttendArgs& a) {
-  return a.planned ? a.G : (a.T + a.qt - 1) / a.qt * a.NH;
+  return a.planned ? a.G : (a.T + a.qt - 1) / a.qt * (int64_t)a.NH;
 }
 
 hipError_t launch_attend(const AttendArgs& a, int R, bool half, hipStream_t st) {

@@ -95,6 +95,7 @@ struct Shape {
   static constexpr int RW = R / MR;
   static constexpr int KW = RW >= 4 ? 1 : 4 / RW;
   static constexpr int NK = D == 256 ? 32 : (D == 128 ? (R == 128 ? 64 : 32) : 64);
+  static constexpr int waves = D == 256 ? 1 : 2;   // a SIMD, by their registers
   static constexpr int KT = KW * NK;
   static constexpr int WR = NK / RW;     // rows of a step that each wave loads
   static constexpr int threads = 64 * RW * KW;
@@ -103,9 +104,10 @@ struct Shape {
   // the keys' waves join their sums through LDS: rows of D + 4 floats
   static constexpr int merge_bytes = KW > 1 ? KW * R * (D + 4) * 4 + KW * R * 8 + R * 8 : 0;
   static constexpr int lds_bytes = buffers * stage_bytes > merge_bytes ? buffers * stage_bytes : merge_bytes;
-  // workgroups that fit a CU (160 KiB of LDS, the plan's share included, and 512
-  // registers a SIMD)
-  static constexpr int per_cu = D < 256 && (lds_bytes + kPlanMax * 24 + 64) * 2 <= 160 * 1024 ? 2 : 1;
+  // workgroups that fit a CU: 160 KiB of LDS (the plan's share included), and the
+  // waves that their registers allow
+  static constexpr int by_lds = 160 * 1024 / (lds_bytes + kPlanMax * 20 + 64), by_waves = waves * 256 / threads;
+  static constexpr int per_cu = by_lds < 1 ? 1 : (by_lds < by_waves ? by_lds : by_waves);
 };
 
 // 16-byte piece c of row r lies at piece c ^ swizzle(r) of its row in LDS. The
@@ -133,32 +135,31 @@ struct QueryInfo {
 __device__ __forceinline__ int clamp_len(int64_t v, int64_t most) { return (int)(v < 0 ? 0 : (v > most ? most : v)); }
 
 __device__ __forceinline__ QueryInfo query_info(const AttendArgs& a, int64_t t) {
+  // all loads first: they wait for nothing but t
+  const bool prefix = a.mode == kAttendPrefix;
+  const int own = (prefix ? a.own_seq : a.q_seq)[t];
+  const int len = a.q_len[t];
+  int start = 0, pos = 0, pre = -1;
+  if (a.q_start) start = a.q_start[t];
+  if (a.q_pos) pos = a.q_pos[t];
+  if (a.mode != kAttendPlain) pre = a.pre[t];
+  const bool ok = own >= 0 && own < (prefix ? a.own_nseq : a.kv.nseq);
+  int plen = 0;
+  if (pre >= 0 && pre < a.npre) plen = clamp_len(a.pre_len[pre], a.pre_max);
+  else pre = -1;
   QueryInfo r;
   r.lo = 0;
-  r.kbase = 0;
-  const int own = a.mode == kAttendPrefix ? a.own_seq[t] : a.q_seq[t];
-  const int64_t nown = a.mode == kAttendPrefix ? a.own_nseq : a.kv.nseq;
-  const bool ok = own >= 0 && own < nown;
-  int plen = 0, pre = -1;
-  if (a.mode != kAttendPlain) {
-    pre = a.pre[t];
-    if (pre >= 0 && pre < a.npre) plen = clamp_len(a.pre_len[pre], a.pre_max);
-    else pre = -1;
-  }
-  const int len = a.q_len[t];
-  if (a.mode == kAttendPrefix) {
+  if (prefix) {
     r.seq = ok ? pre : -1;
     r.hi = r.seq >= 0 ? plen : 0;
+    r.kbase = 0;
   } else {
     r.seq = ok ? own : -1;
     r.hi = ok ? clamp_len(len, a.kv.Lmax) : 0;
-    if (a.q_start) {
-      const int s = a.q_start[t];
-      r.lo = s < 0 ? 0 : (s > r.hi ? r.hi : s);
-    }
+    r.lo = start < 0 ? 0 : (start > r.hi ? r.hi : start);
     r.kbase = plen;
   }
-  r.pos = a.q_pos ? a.q_pos[t] : plen + len - 1;
+  r.pos = a.q_pos ? pos : plen + len - 1;
   return r;
 }
 
@@ -190,16 +191,23 @@ struct Part {
   int slot;        // unfinished parts: where they are kept
 };
 
-__device__ __forceinline__ int wave_min_of(int v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = min(v, __shfl_xor(v, off, 64));
-  return v;
+// Reductions over a wave by data-parallel moves (rows of 16 lanes, then from row
+// to row); the result, of lane 63, as a scalar. A shuffle through LDS costs some
+// 130 cycles a step, and a part begins with eight of these.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_max(int v) {
+  return max(v, __builtin_amdgcn_update_dpp((int)0x80000000, v, CTRL, ROWS, 0xf, false));
 }
 __device__ __forceinline__ int wave_max_of(int v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v = max(v, __shfl_xor(v, off, 64));
-  return v;
+  v = dpp_max<0x111, 0xf>(v);   // from 1, 2, 4, 8 lanes below in the row
+  v = dpp_max<0x112, 0xf>(v);
+  v = dpp_max<0x114, 0xf>(v);
+  v = dpp_max<0x118, 0xf>(v);
+  v = dpp_max<0x142, 0xa>(v);   // lane 15 of a row to the next row
+  v = dpp_max<0x143, 0xc>(v);   // lane 31 to the upper half
+  return __builtin_amdgcn_readlane(v, 63);
 }
+__device__ __forceinline__ int wave_min_of(int v) { return ~wave_max_of(~v); }
 
 // What a workgroup keeps of its queries (of the whole batch where it is planned)
 // in LDS: entry t - t0 for query t.
@@ -250,11 +258,11 @@ __device__ __forceinline__ Span span_of(const AttendArgs& a, const Known& known,
     all_lo = max(all_lo, r.lo);
     all_hi = min(all_hi, r.hi);
   }
-  s.seq = uniform(wave_max_of(seq));
-  s.lo = uniform(wave_min_of(lo));
-  s.hi = uniform(wave_max_of(hi));
+  s.seq = wave_max_of(seq);
+  s.lo = wave_min_of(lo);
+  s.hi = wave_max_of(hi);
   if (s.hi <= s.lo) s.lo = s.hi = 0;
-  s.some = uniform(wave_min_of(all_hi) - wave_max_of(all_lo));
+  s.some = wave_min_of(all_hi) - wave_max_of(all_lo);
   s.lo &= -a.align;
   return s;
 }
@@ -359,6 +367,12 @@ struct Kernel {
     t = p.t0 + qi;
     return qi < p.nq && head < (kvh + 1) * a.group;
   }
+
+  struct Stage {        // a step's rows on their way to LDS
+    u32x4 k[NLD], v[NLD];
+    uint64_t valid;     // keys that there are
+    int token;          // this lane's key
+  };
 
   // The keys of one step for one group of waves: lane l looks up key l, in three
   // steps of the loop: its token (the key's number, or a selected id), the table
@@ -519,10 +533,38 @@ struct Kernel {
     }
   }
 
-  // scores of KS keys: S^T tiles of this wave's rows
-  __device__ static __forceinline__ void score(const uint16_t* ks, const u32x4 (&qf)[QF], Acc (&s)[ST]) {
+  // LDS addresses. A piece's place is its row's start with the piece number XORed
+  // by the row's swizzle, so the places of one row differ from a base by an XOR
+  // with a constant. The bases are made anew for each run of keys (opaque to the
+  // compiler): kept in the loop, the 16 to 24 places of a lane would take as many
+  // registers as its output tile.
+  typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+  typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
+  __device__ static __forceinline__ uint32_t lds_address(const uint16_t* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint16_t*)p;
+  }
+  __device__ static __forceinline__ u32x4 read_lds(uint32_t at) {
+    const u32x4 v = *(lds_u32x4*)(uintptr_t)at;
+    return v;
+  }
+  __device__ static __forceinline__ uint32_t key_base(const uint16_t* ks) {
     const int lane = threadIdx.x & 63;
-    const int r = lane % MR, g = lane / MR;
+    const int r = lane % MR;
+    uint32_t b = lds_address(ks) + r * (2 * D) + 16 * ((lane / MR) ^ swizzle<D>(r));
+    asm volatile("" : "+v"(b));
+    return b;
+  }
+  // the operand K of KS keys
+  __device__ static __forceinline__ void key_frags(const uint16_t* ks, u32x4 (&kf)[QF][ST]) {
+    const uint32_t b = key_base(ks);
+#pragma unroll
+    for (int f = 0; f < QF; ++f)
+#pragma unroll
+      for (int i = 0; i < ST; ++i)   // 16 rows further on the swizzle is the same
+        kf[f][i] = read_lds((b ^ (f * (64 / MR) * 16)) + i * MR * 2 * D);
+  }
+  // scores of KS keys: S^T tiles of this wave's rows
+  __device__ static __forceinline__ void score(const u32x4 (&kf)[QF][ST], const u32x4 (&qf)[QF], Acc (&s)[ST]) {
 #pragma unroll
     for (int i = 0; i < ST; ++i)
 #pragma unroll
@@ -530,22 +572,21 @@ struct Kernel {
 #pragma unroll
     for (int f = 0; f < QF; ++f)
 #pragma unroll
-      for (int i = 0; i < ST; ++i) {
-        const int row = i * MR + r;
-        const int c = (f * (64 / MR) + g) ^ swizzle<D>(row);
-        s[i] = mma(*reinterpret_cast<const u32x4*>(ks + row * D + 8 * c), qf[f], s[i]);
-      }
+      for (int i = 0; i < ST; ++i) s[i] = mma(kf[f][i], qf[f], s[i]);
   }
 
-  // 4 values V[key0 + 0..3][dim] of this lane's output dim: 16 lanes read 4 rows of 16 dims
-  __device__ static __forceinline__ u32x2 read_tr(const uint16_t* vs, int key0, int dim0) {
+  // Base of the transposing reads: 16 lanes read 4 rows (keys) of 16 dims, 4 values
+  // each, and get one dim of the 4 keys.
+  __device__ static __forceinline__ uint32_t value_base(const uint16_t* vs) {
     const int lane = threadIdx.x & 63;
-    const int row = key0 + ((lane & 15) >> 2);
-    const int piece = (dim0 >> 3) + ((lane & 3) >> 1);
-    const uint16_t* p = vs + row * D + 8 * (piece ^ swizzle<D>(row)) + 4 * (lane & 1);
-    typedef __attribute__((address_space(3))) shortx4 lds_shortx4;
-    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(uintptr_t)(
-                                         __attribute__((address_space(3))) const uint16_t*)p));
+    const int r = (MR == 32 ? 4 * (lane >> 5) : 4 * (lane >> 4)) + ((lane & 15) >> 2);
+    const int piece = (MR == 32 ? (lane & 16) >> 3 : 0) + ((lane & 3) >> 1);
+    uint32_t b = lds_address(vs) + r * (2 * D) + 16 * (piece ^ swizzle<D>(r)) + 8 * (lane & 1);
+    asm volatile("" : "+v"(b));
+    return b;
+  }
+  __device__ static __forceinline__ u32x2 read_tr(uint32_t at) {
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_shortx4*)(uintptr_t)at));
   }
 
   // The halves of x without infinities and NaNs.
@@ -554,12 +595,13 @@ struct Kernel {
     return x & (((x & e) == e ? 0u : 0xffffu) | ((x & (e << 16)) == (e << 16) ? 0u : 0xffff0000u));
   }
 
-  // The operand V^T of product p, output tile i.
-  __device__ static __forceinline__ u32x4 value_frag(const uint16_t* vs, int p, int i) {
-    const int lane = threadIdx.x & 63;
-    const int k0 = MR == 32 ? p * 16 + 4 * (lane >> 5) : p * 32 + 4 * (lane >> 4);
-    const int dim0 = i * MR + (MR == 32 ? (lane & 16) : 0);
-    const u32x2 x = read_tr(vs, k0, dim0), y = read_tr(vs, k0 + (MR == 32 ? 8 : 16), dim0);
+  // The operand V^T of product p, output tile i: MR == 32: keys 16 p + 4 (lane / 32)
+  // + 0..3 and 8 further (another swizzle); MR == 16: 32 p + 4 (lane / 16) + 0..3 and
+  // 16 further (the same one).
+  __device__ static __forceinline__ u32x4 value_frag(uint32_t base, int p, int i) {
+    const uint32_t a = base ^ (i * (MR / 8) * 16);
+    const u32x2 x = read_tr(a + p * (MR == 32 ? 16 : 32) * 2 * D);
+    const u32x2 y = read_tr(MR == 32 ? (a ^ 32) + (16 * p + 8) * 2 * D : a + (32 * p + 16) * 2 * D);
     return u32x4{x[0], x[1], y[0], y[1]};
   }
   // The operand P^T of product p from this lane's score registers: MR == 32: 16
@@ -576,12 +618,12 @@ struct Kernel {
   static constexpr int NP = MR == 32 ? KS / 16 : KS / 32;
 
   // O^T += V^T P^T over KS keys
-  __device__ static __forceinline__ void accumulate(const uint16_t* vs, const Acc (&s)[ST], Acc (&o)[OT]) {
+  __device__ static __forceinline__ void accumulate(const u32x4 (&vf)[NP][OT], const Acc (&s)[ST], Acc (&o)[OT]) {
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const u32x4 w = weight_frag(s, p);
 #pragma unroll
-      for (int i = 0; i < OT; ++i) o[i] = mma(value_frag(vs, p, i), w, o[i]);
+      for (int i = 0; i < OT; ++i) o[i] = mma(vf[p][i], w, o[i]);
     }
   }
 
@@ -591,12 +633,13 @@ struct Kernel {
   // and NaN in turn, a product of marks counts those that each row sees.
   __device__ static __forceinline__ void accumulate_guarded(const uint16_t* vs, Acc (&s)[ST], Acc (&o)[OT], uint32_t see) {
     const int lane = threadIdx.x & 63;
+    const uint32_t base = value_base(vs);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const u32x4 w = weight_frag(s, p);
 #pragma unroll
       for (int i = 0; i < OT; ++i) {
-        u32x4 v = value_frag(vs, p, i);
+        u32x4 v = value_frag(base, p, i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = finite_only(v[e]);
         o[i] = mma(v, w, o[i]);
@@ -619,7 +662,7 @@ struct Kernel {
         for (int j = 0; j < AR; ++j) n[j] = 0.f;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          u32x4 v = value_frag(vs, p, i);
+          u32x4 v = value_frag(base, p, i);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             uint32_t mark = 0;
@@ -739,13 +782,31 @@ struct Kernel {
     }
   }
 
+  // Over the lanes that hold a row (MR apart): the permutations swap rows of 16 or
+  // 32 lanes between their two operands, so both halves come out for every lane.
+  __device__ static __forceinline__ void halves(float v, bool by16, float& x, float& y) {
+    const auto r = by16 ? __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false)
+                        : __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    x = __uint_as_float(r[0]);
+    y = __uint_as_float(r[1]);
+  }
   __device__ static __forceinline__ float over_rows_max(float v) {
-    if constexpr (MR == 16) v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+    float x, y;
+    if constexpr (MR == 16) {
+      halves(v, true, x, y);
+      v = fmaxf(x, y);
+    }
+    halves(v, false, x, y);
+    return fmaxf(x, y);
   }
   __device__ static __forceinline__ float over_rows_sum(float v) {
-    if constexpr (MR == 16) v += __shfl_xor(v, 16, 64);
-    return v + __shfl_xor(v, 32, 64);
+    float x, y;
+    if constexpr (MR == 16) {
+      halves(v, true, x, y);
+      v = x + y;
+    }
+    halves(v, false, x, y);
+    return x + y;
   }
 
   // Result or unfinished sums of row r (of the tile), dims d0 .. d0 + 3.
@@ -808,10 +869,10 @@ struct Kernel {
       id_hi = uniform(q.hi);
     }
     // keys that every row of this wave sees, and keys that any of them sees
-    const int all_lo = uniform(wave_max_of(active ? row.lo : 0));
-    const int all_hi = uniform(wave_min_of(active ? row.hi : 0x7fffffff));
-    const int any_lo = uniform(wave_min_of(active ? row.lo : 0x7fffffff));
-    const int any_hi = uniform(wave_max_of(active ? row.hi : 0));
+    const int all_lo = wave_max_of(active ? row.lo : 0);
+    const int all_hi = wave_min_of(active ? row.hi : 0x7fffffff);
+    const int any_lo = wave_min_of(active ? row.lo : 0x7fffffff);
+    const int any_hi = wave_max_of(active ? row.hi : 0);
 
     u32x4 qf[QF];
     {
@@ -839,30 +900,48 @@ struct Kernel {
     const int k0 = begin + kw * NK;
     // steps of this wave: its own where no other shares its keys
     const int mine = RW > 1 ? steps : (end > k0 ? (end - k0 + KT - 1) / KT : 0);
-    u32x4 kr[NLD], vr[NLD];
+    // rows on their way to LDS; what is looked up for them (tokens, pages) runs one
+    // and two steps further ahead
+    Stage stage;
     Keys nxt;
     nxt.token = -1;
     nxt.within = nxt.page = 0;
-    int far = -1, cur_token = -1;
-    uint64_t valid = 0;
-    int entry = 0;
+    int far = -1, entry = 0;
     uint32_t piece[NLD];
-    if constexpr (ALIGNED) {
-      piece_offsets(a.kv, rw, piece);
-      if (mine > 0) {
-        valid = load_aligned(a.kv, bases, piece, page_entry(a.kv, table, sp.seq, k0, end), k0, end, rw, kr, vr);
-        entry = page_entry(a.kv, table, sp.seq, k0 + KT, end);
-        store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
+    auto fetch = [&](int it) __attribute__((always_inline)) {
+      if constexpr (ALIGNED) {
+        const int now = entry;
+        entry = page_entry(a.kv, table, sp.seq, k0 + (it + 1) * KT, end);
+        stage.valid = load_aligned(a.kv, bases, piece, now, k0 + it * KT, end, rw, stage.k, stage.v);
+        stage.token = -1;
+      } else {
+        const uint32_t unit = row_unit(a.kv, nxt);
+        stage.valid = __ballot(unit != kNoRow);
+        stage.token = nxt.token;
+        nxt = page_of(a.kv, table, sp.seq, far, id_lo, id_hi);
+        far = token_of(ids, k0 + (it + 2) * KT, end);
+        load_rows(bases, unit, rw, stage.k, stage.v);
       }
-    } else if (mine > 0) {
-      const Keys cur = page_of(a.kv, table, sp.seq, token_of(ids, k0, end), id_lo, id_hi);
-      nxt = page_of(a.kv, table, sp.seq, token_of(ids, k0 + KT, end), id_lo, id_hi);
-      far = token_of(ids, k0 + 2 * KT, end);
-      const uint32_t unit = row_unit(a.kv, cur);
-      load_rows(bases, unit, rw, kr, vr);
-      valid = __ballot(unit != kNoRow);
-      cur_token = cur.token;
-      store_rows(buf + kw * 2 * GB, buf + kw * 2 * GB + GB, rw, kr, vr);
+    };
+    uint64_t valid = 0;
+    int cur_token = -1;
+    auto land = [&](int it) __attribute__((always_inline)) {
+      uint16_t* to = buf + (S::buffers > 1 ? (it & 1) * SB : 0) + kw * 2 * GB;
+      store_rows(to, to + GB, rw, stage.k, stage.v);
+      valid = stage.valid;
+      cur_token = stage.token;
+    };
+    if (mine > 0) {
+      if constexpr (ALIGNED) {
+        piece_offsets(a.kv, rw, piece);
+        entry = page_entry(a.kv, table, sp.seq, k0, end);
+      } else {
+        const int first = token_of(ids, k0, end);
+        far = token_of(ids, k0 + KT, end);
+        nxt = page_of(a.kv, table, sp.seq, first, id_lo, id_hi);
+      }
+      fetch(0);
+      land(0);
     }
     // the loop's first products wait for these loads here, not for its own
 #pragma unroll
@@ -874,23 +953,7 @@ struct Kernel {
     const bool near_holds = near_cap_holds(cap_c);
     sync_rows();
     for (int it = 0; it < mine; ++it) {
-      const bool more = it + 1 < mine;
-      uint64_t next_valid = 0;
-      int next_token = -1;
-      if constexpr (ALIGNED) {
-        if (more) {
-          const int now = entry;
-          entry = page_entry(a.kv, table, sp.seq, k0 + (it + 2) * KT, end);
-          next_valid = load_aligned(a.kv, bases, piece, now, k0 + (it + 1) * KT, end, rw, kr, vr);
-        }
-      } else if (more) {
-        const uint32_t unit = row_unit(a.kv, nxt);
-        next_valid = __ballot(unit != kNoRow);
-        next_token = nxt.token;
-        nxt = page_of(a.kv, table, sp.seq, far, id_lo, id_hi);
-        far = token_of(ids, k0 + (it + 3) * KT, end);
-        load_rows(bases, unit, rw, kr, vr);
-      }
+      if (it + 1 < mine) fetch(it + 1);
       const uint16_t* ks = buf + (S::buffers > 1 ? (it & 1) * SB : 0) + kw * 2 * GB;
 #pragma unroll
       for (int sub = 0; sub < NS; ++sub) {
@@ -900,7 +963,21 @@ struct Kernel {
         const uint32_t have = (uint32_t)(valid >> (sub * KS));
         if (base >= any_hi || base + KS <= any_lo || have == 0) continue;
         Acc s[ST];
-        score(ks + sub * KS * D, qf, s);
+        u32x4 kf[QF][ST];
+        key_frags(ks + sub * KS * D, kf);
+        __builtin_amdgcn_sched_barrier(0);
+        score(kf, qf, s);
+        const uint16_t* vs = ks + GB + sub * KS * D;
+        u32x4 vf[NP][OT];
+        if constexpr (!GUARD) {
+          // asked for before the weights are worked out
+          const uint32_t vb = value_base(vs);
+#pragma unroll
+          for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int i = 0; i < OT; ++i) vf[n][i] = value_frag(vb, n, i);
+        }
+        __builtin_amdgcn_sched_barrier(0);
         const bool full = have == ~0u && base >= all_lo && base + KS <= all_hi;
         const uint32_t see = have & bits_from(row.lo - base) & ~bits_from(row.hi - base);
         if constexpr (MODE == kBias) shape(a, s, row, ids, base, cur_token, sub);
@@ -943,17 +1020,11 @@ struct Kernel {
             add[j & 1] += s[i][j];
           }
         sum += add[0] + add[1];
-        const uint16_t* vs = ks + GB + sub * KS * D;
         if constexpr (GUARD) accumulate_guarded(vs, s, o, see);
-        else accumulate(vs, s, o);
+        else accumulate(vf, s, o);
       }
-      valid = next_valid;
-      cur_token = next_token;
       if (S::buffers == 1) sync_rows();   // this wave has read what it now overwrites
-      if (more) {
-        uint16_t* to = buf + (S::buffers > 1 ? ((it + 1) & 1) * SB : 0) + kw * 2 * GB;
-        store_rows(to, to + GB, rw, kr, vr);
-      }
+      if (it + 1 < mine) land(it + 1);
       sync_rows();
     }
     finish(fresh(ap), p, sp, lds, odd, r, kw, m * sc, sum, o);
@@ -1048,13 +1119,13 @@ struct Kernel {
 
   // Key tiles before each query's segment: cum[t] for t < T, and their sum; the
   // queries' intervals.
-  __device__ static __forceinline__ int64_t make_plan(const AttendArgs& a, int64_t* cum, const Known& known) {
+  __device__ static __forceinline__ int make_plan(const AttendArgs& a, int* cum, const Known& known) {
     const int T = (int)a.T, tid = threadIdx.x;
     for (int t = tid; t < T; t += TH) known.at[t] = interval_of(a, t);
     __syncthreads();
     constexpr int PER = kPlanMax / TH;       // queries a thread sums
-    int64_t w[PER];
-    int64_t mine = 0;
+    int w[PER];
+    int mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int t = tid * PER + i;
@@ -1081,17 +1152,18 @@ struct Kernel {
       mine += w[i];
     }
     // prefix sum over the threads
-    __shared__ int64_t wsum[TH / 64];
+    __shared__ int wsum[TH / 64];
     const int lane = tid & 63;
-    int64_t inc = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int64_t v = __shfl_up(inc, off, 64);
-      if (lane >= off) inc += v;
-    }
+    int inc = mine;
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x111, 0xf, 0xf, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x112, 0xf, 0xf, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x114, 0xf, 0xf, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x118, 0xf, 0xf, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x142, 0xa, 0xf, false);
+    inc += __builtin_amdgcn_update_dpp(0, inc, 0x143, 0xc, 0xf, false);
     if (lane == 63) wsum[tid >> 6] = inc;
     __syncthreads();
-    int64_t before = inc - mine, total = 0;
+    int before = inc - mine, total = 0;
 #pragma unroll
     for (int i = 0; i < TH / 64; ++i) {
       if (i < (tid >> 6)) before += wsum[i];
@@ -1107,7 +1179,7 @@ struct Kernel {
     return total;
   }
 
-  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int64_t* cum, Interval* intervals, int* odd, unsigned block) {
+  __device__ static __forceinline__ void body(ArgPtr ap, unsigned char* lds, int* cum, Interval* intervals, int* odd, unsigned block) {
     const AttendArgs& a = fresh(ap);
     const bool mixed = a.odd != nullptr;
     if (!GUARD && mixed) {
@@ -1117,12 +1189,13 @@ struct Kernel {
     // units of work [u, u1): queries of this workgroup's row tile, or key tiles of the plan
     const int NH = a.NH, T = (int)a.T;
     const bool planned = a.planned;
-    int64_t total = 0, u, u1;
+    int total = 0;
+    int64_t u, u1;
     int hh = 0;
     Known known{intervals, 0};
     if (planned) {
       total = uniform(make_plan(a, cum, known));
-      const int64_t units = total * NH;
+      const int64_t units = (int64_t)total * NH;
       u = block * units / a.G;
       u1 = ((int64_t)block + 1) * units / a.G;
       if (block == 0 && !GUARD) publish_plan(a, cum, known, total);
@@ -1144,16 +1217,16 @@ struct Kernel {
         int lo = 0, hi = T - 1;
         while (lo < hi) {
           const int mid = (lo + hi + 1) >> 1;
-          if (cum[mid] * NH <= u) lo = mid;
+          if ((int64_t)cum[mid] * NH <= u) lo = mid;
           else hi = mid - 1;
         }
         lo = uniform(lo);
-        const int64_t first = uniform(cum[lo]);
+        const int first = uniform(cum[lo]);
         p.t0 = lo;
         p.nq = run_length(a, known, lo);
         const int next = lo + p.nq;
-        const int tiles = (int)((next < T ? uniform(cum[next]) : total) - first);
-        const int64_t in = u - first * NH;
+        const int tiles = (next < T ? uniform(cum[next]) : total) - first;
+        const int64_t in = u - (int64_t)first * NH;
         p.hh = (int)(in / tiles);
         p.tile0 = (int)(in - (int64_t)p.hh * tiles);
         const int64_t left = u1 - u;
@@ -1180,8 +1253,8 @@ struct Kernel {
   }
 
   // What the join needs: every query takes the entry of its segment.
-  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int64_t* cum, const Known& known,
-                                                     int64_t total) {
+  __device__ static __forceinline__ void publish_plan(const AttendArgs& a, const int* cum, const Known& known,
+                                                     int total) {
     for (int t = threadIdx.x; t < (int)a.T; t += TH) {
       int t0 = t, next = t + 1;
       const int seq = known[t].seq;
@@ -1189,7 +1262,7 @@ struct Kernel {
       while (next < (int)a.T && next % a.qt != 0 && known[next].seq == seq) ++next;
       PlanEntry e;
       e.first = cum[t0];
-      e.tiles = (int32_t)((next < (int)a.T ? cum[next] : total) - cum[t0]);
+      e.tiles = (next < (int)a.T ? cum[next] : total) - cum[t0];
       e.t0 = t0;
       a.plan[t] = e;
     }
@@ -1201,8 +1274,8 @@ template <bool HALF, int D, int R, int MODE, bool ALIGNED, bool GUARD>
 __global__ __launch_bounds__((Shape<D, R>::threads), (Shape<D, R>::per_cu * Shape<D, R>::threads / 256 > 0
                                                           ? Shape<D, R>::per_cu * Shape<D, R>::threads / 256
                                                           : 1)) void attend_kernel(AttendArgs) {
-  __shared__ __align__(16) unsigned char lds[Shape<D, R>::lds_bytes];
-  __shared__ int64_t cum[kPlanMax];
+  __shared__ __align__(1024) unsigned char lds[Shape<D, R>::lds_bytes];
+  __shared__ int cum[kPlanMax];
   __shared__ Interval intervals[kPlanMax];
   __shared__ int odd;
   // the arguments are read where they lie (see fresh)

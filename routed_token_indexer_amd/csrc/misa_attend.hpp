@@ -13,11 +13,11 @@ enum AttendMode : int {
 };
 
 // Batches of at most this many queries are planned (see attend_kernel.hpp).
-constexpr int kPlanMax = 512;
+constexpr int kPlanMax = 256;
 
 // What the join needs to know of a query's part of the plan.
 struct PlanEntry {
-  int64_t first;   // key tiles of the segments before its own (per head tile)
+  int32_t first;   // key tiles of the segments before its own (per head tile)
   int32_t tiles;   // key tiles of its segment
   int32_t t0;      // first query of its segment
 };
@@ -64,16 +64,17 @@ struct AttendArgs {
   float* part_out;          // [2 G][R][d]
   float* part_ml;           // [2 G][R][2]
   PlanEntry* plan;          // [T]
-  int64_t* plan_total;      // [1] key tiles of all segments
+  int32_t* plan_total;      // [1] key tiles of all segments
 };
 
 // Rows (query, head) of a workgroup's tile for a batch: 16, 32, 64 or 128.
 // single: a row tile takes one query (selected tokens are each query's own; in a
 // decode step no two queries share a sequence).
 int attend_rows(int64_t T, int64_t nseq, int group, int d, bool single);
-bool attend_planned(int64_t T);
+bool attend_planned(int64_t T, int64_t most_keys);
 // Workgroups of a planned launch, and its workspace.
 int attend_groups(int d, int R);
+// (which is the same for a planned batch and one that has too many key tiles for it).
 size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, bool mixed);
 // Fills the fields that depend on the tile and carves the workspace.
 // mixed: rows of one part may see different keys, or not all keys of its steps
