@@ -528,11 +528,19 @@ def _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale, slope
     return c, dev, q_ts, q_hs, T, Hq, float(scale), out, lse, ptrs
 
 
-def _attend_ws(ws, op, T, Hq, c, dev, npre=0):
+def _attend_ws(ws, op, T, Hq, c, dev, stream, npre=0):
     need = attend_workspace_bytes(op, T, Hq, c.heads, c.d, c.nseq, npre)
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"ws: on {ws.device}, the cache on {dev}")
-    return _workspace(ws, need, dev)
+    if ws is not None:
+        if ws.device != dev:
+            raise ValueError(f"ws: on {ws.device}, the cache on {dev}")
+        if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+            raise TypeError("ws: expected a contiguous torch.uint8 tensor")
+        if ws.numel() >= need:
+            return ws
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    if stream is not None:
+        ws.record_stream(stream)   # dropped on return: its memory waits for that stream
+    return ws
 
 
 def attend(q, k_cache, v_cache, q_seq, q_len, table=None, q_start=None, q_pos=None, scale=None, cap=0.0, slopes=None,
@@ -544,7 +552,7 @@ def attend(q, k_cache, v_cache, q_seq, q_len, table=None, q_start=None, q_pos=No
     slope * |q_pos - s| (q_pos default: q_len - 1)."""
     c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
                                                                    slopes, out, lse, want_lse)
-    ws = _attend_ws(ws, OP_ATTEND, T, Hq, c, dev)
+    ws = _attend_ws(ws, OP_ATTEND, T, Hq, c, dev, stream)
     _call(dev, "misa_attend", ctypes.byref(c), q.data_ptr(), q_ts, q_hs, p[0],
           _vec(q_start, "q_start", torch.int32, (T,), dev), p[1], p[2], T, Hq, scale, cap, p[3], p[4], p[5],
           ws.data_ptr(), ws.numel(), _on(dev, stream))
@@ -560,7 +568,7 @@ def attend_selected(q, k_cache, v_cache, idx, q_seq, q_len, table=None, q_pos=No
     if idx.dim() != 2:
         raise ValueError(f"idx: expected 2 dims, got shape {tuple(idx.shape)}")
     topk = idx.shape[1]
-    ws = _attend_ws(ws, OP_ATTEND_SELECTED, T, Hq, c, dev)
+    ws = _attend_ws(ws, OP_ATTEND_SELECTED, T, Hq, c, dev, stream)
     _call(dev, "misa_attend_selected", ctypes.byref(c), q.data_ptr(), q_ts, q_hs,
           _vec(idx, "idx", torch.int32, (T, topk), dev), topk, p[0], p[1], p[2], T, Hq, scale, cap, p[3], p[4], p[5],
           ws.data_ptr(), ws.numel(), _on(dev, stream))
@@ -580,7 +588,7 @@ def attend_shared(q, k_cache, v_cache, q_seq, q_len, pre, pre_len, table=None, p
         if pre_table.dim() != 2:
             raise ValueError(f"pre_table: expected 2 dims, got shape {tuple(pre_table.shape)}")
         cols = pre_table.shape[1]
-    ws = _attend_ws(ws, OP_ATTEND_SHARED, T, Hq, c, dev, npre)
+    ws = _attend_ws(ws, OP_ATTEND_SHARED, T, Hq, c, dev, stream, npre)
     _call(dev, "misa_attend_shared", ctypes.byref(c), q.data_ptr(), q_ts, q_hs, p[0], p[1], p[2],
           _vec(pre, "pre", torch.int32, (T,), dev), _vec(pre_len, "pre_len", torch.int32, (npre,), dev),
           None if pre_table is None else _vec(pre_table, "pre_table", torch.int32, (npre, cols), dev), cols, npre, T, Hq,

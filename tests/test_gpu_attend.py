@@ -159,30 +159,126 @@ def test_queries_in_any_order():
     A.check(got, A.attend(q, kc, vc, seq, length, table=table), "any order")
 
 
-@pytest.mark.parametrize("nq", [1, 60])
-def test_large_scores_and_nan_of_visible_values(nq):
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 5, 12, 25, 60, 300])
+def test_large_scores_and_nan_of_visible_values(nq, d):
     """Scores of +-hundreds (weights that vanish) stay finite; a NaN value reaches
     exactly the queries that see it, an infinite one gives an infinity."""
     g = torch.Generator().manual_seed(4)
-    kc, vc, table = cache(g, 1, 8, 32, 1, 64, BF)
-    q = (torch.randn(nq, 2, 64, generator=g) * 30).to(BF).cuda()
-    length = ints([200 - nq + i + 1 for i in range(nq)])
+    L = 200 + nq
+    kc, vc, table = cache(g, 1, -(-L // 32), 32, 1, d, BF)
+    q = (torch.randn(nq, 2, d, generator=g) * 30).to(BF).cuda()
+    length = ints([L - nq + i + 1 for i in range(nq)])
     seq = ints([0] * nq)
     got = M.attend(q, kc, vc, seq, length, table=table, want_lse=True)
     torch.cuda.synchronize()
     A.check(got, A.attend(q, kc, vc, seq, length, table=table), "large scores")
-    bad = 200 - nq // 2 - 1                                       # the first half does not see it
+    bad = L - nq // 2 - 1                                         # the first half does not see it
     q2 = (q.float() / 30).to(BF)
+    want = A.attend(q2, kc, vc, seq, length, table=table)
     vc[int(table[0, bad // 32]), bad % 32, 0, 5] = math.nan
     vc[int(table[0, bad // 32]), bad % 32, 0, 9] = math.inf
-    out, _ = M.attend(q2, kc, vc, seq, length, table=table)
+    vc[int(table[0, bad // 32]), bad % 32, 0, 11] = -math.inf
+    out, lse = M.attend(q2, kc, vc, seq, length, table=table, want_lse=True)
     torch.cuda.synchronize()
     sees = (length > bad).cpu()
-    out = out.cpu().float()
-    assert bool(torch.isnan(out[sees][..., 5]).all()) and bool((out[sees][..., 9] == math.inf).all())
-    assert bool(torch.isfinite(out[~sees]).all())
-    rest = [i for i in range(64) if i not in (5, 9)]
-    assert bool(torch.isfinite(out[..., rest]).all())
+    o = out.cpu().float()
+    assert bool(torch.isnan(o[sees][..., 5]).all())
+    assert bool((o[sees][..., 9] == math.inf).all()) and bool((o[sees][..., 11] == -math.inf).all())
+    for i in (5, 9, 11):                # everything else as without them
+        out[sees.cuda(), :, i] = want[0][sees][..., i].to(BF).cuda()
+    A.check((out, lse), want, "around a NaN")
+
+
+@pytest.mark.parametrize("name", ["prompt_docs", "prompt_window_group3", "prompt_prefix_256", "direct_256"])
+def test_values_outside_the_interval_may_be_anything(name):
+    """NaN and infinities in the values of tokens that some queries of a row tile
+    see and others do not (other documents, tokens behind the window)."""
+    q, kc, vc, seq, length, kw = build(CASES[name])
+    start = kw["q_start"] if kw["q_start"] is not None else torch.zeros_like(length)
+    clean = A.attend(q, kc, vc, seq, length, **kw)
+    page, table = kc.shape[1], kw["table"]
+    bad = [100, 117, 121] if name == "prompt_prefix_256" else [3, 57, 120]   # behind the prefix that all see
+    for n in range(min(3, table.shape[0])):
+        for s in bad:
+            if s // page < table.shape[1]:
+                vc[int(table[n, s // page]), s % page] = math.nan if s % 2 else math.inf
+    out, lse = M.attend(q, kc, vc, seq, length, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    sees = torch.zeros(len(length), dtype=torch.bool)
+    for s in bad:
+        sees |= ((start <= s) & (s < length) & (seq < 3)).cpu()
+    assert bool((~sees).any())
+    A.check((out[~sees.cuda()], lse[~sees.cuda()]), tuple(x[~sees] for x in clean), name)
+    assert not bool(torch.isfinite(out[sees.cuda()].float()).all()) or not bool(sees.any())
+
+
+@pytest.mark.parametrize("Hq,d", [(8, 128), (64, 128), (64, 64), (40, 256), (100, 128)])
+def test_windows_of_single_queries(Hq, d):
+    """A decode step with sliding windows: what lies before a window may hold anything."""
+    g = torch.Generator().manual_seed(31)
+    kc, vc, table = cache(g, 4, 10, 32, 1, d, BF)
+    q = torch.randn(4, Hq, d, generator=g).to(BF).cuda()
+    seq, length, start = ints([0, 1, 2, 3]), ints([300, 77, 130, 320]), ints([171, 76, 100, 319])
+    want = A.attend(q, kc, vc, seq, length, table=table, q_start=start)
+    for n in range(4):
+        for s in range(max(0, int(start[n]) - 40), int(start[n])):
+            kc[int(table[n, s // 32]), s % 32] = math.nan
+            vc[int(table[n, s // 32]), s % 32] = math.nan if s % 2 else -math.inf
+    got = M.attend(q, kc, vc, seq, length, table=table, q_start=start, want_lse=True)
+    torch.cuda.synchronize()
+    A.check(got, want, "windows")
+
+
+@pytest.mark.parametrize("cap", [0.5, 3.0, 40.0, 300.0, 20000.0])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("nq", [1, 40])
+def test_caps(cap, bias, nq):
+    """Caps that most scores pass, caps that none comes near, and large ones."""
+    g = torch.Generator().manual_seed(41)
+    kc, vc, table = cache(g, 2, 20, 16, 2, 128, FP)
+    q = (torch.randn(2 * nq, 8, 128, generator=g) * 4).to(FP).cuda()
+    q[0] *= 0.01                                            # scores near zero
+    seq = ints([0] * nq + [1] * nq)
+    length = ints([320 - nq + i + 1 for i in range(nq)] * 2)
+    kw = dict(table=table, cap=cap, slopes=torch.linspace(0.0, 0.3, 8).cuda() if bias else None)
+    got = M.attend(q, kc, vc, seq, length, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    A.check(got, A.attend(q, kc, vc, seq, length, **kw), f"cap {cap}")
+
+
+def test_infinite_scores_of_visible_keys():
+    """Keys that overflow to infinity: NaN as in the formula without a cap, the cap
+    itself with one; rows of other heads and queries stay."""
+    g = torch.Generator().manual_seed(42)
+    kc, vc, table = cache(g, 1, 4, 16, 2, 64, BF)
+    q = torch.randn(3, 4, 64, generator=g).to(BF).cuda()
+    seq, length = ints([0, 0, 0]), ints([20, 30, 40])
+    clean = A.attend(q, kc, vc, seq, length, table=table)
+    kc[int(table[0, 1]), 9, 0] = math.inf                   # token 25 of the first kv head
+    q[:, :2] = q[:, :2].abs() + 0.1
+    want = A.attend(q[:, 2:], kc[:, :, 1:], vc[:, :, 1:], seq, length, table=table)
+    out, lse = M.attend(q, kc, vc, seq, length, table=table, want_lse=True)
+    capped, _ = M.attend(q, kc, vc, seq, length, table=table, cap=10.0)
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(out[1:, :2]).all()) and bool(torch.isfinite(out[0]).all())
+    A.check((out[:, 2:], lse[:, 2:]), want, "other heads")
+    assert bool(torch.isfinite(capped).all())
+
+
+def test_stream_argument():
+    """A call on a stream of the caller's, its workspace made by the call, while the
+    current stream goes on allocating."""
+    q, kc, vc, seq, length, kw = build(CASES["decode_gqa8"])
+    want = M.attend(q, kc, vc, seq, length, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        got = M.attend(q, kc, vc, seq, length, want_lse=True, stream=side, **kw)
+        junk = [torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        side.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        del junk
 
 
 def test_same_call_twice_and_dirty_workspace():
