@@ -728,7 +728,8 @@ struct Kernel {
     }
   }
 
-  // Cap and bias; the scores leave in units of log2.
+  // Cap and bias. Capped scores leave in units of log2, others still without the
+  // scale (the bias divided by it).
   __device__ static __forceinline__ void shape(const AttendArgs& a, Acc (&s)[ST], const Rows& row, const int32_t* ids, int base,
                                                int token, int sub) {
     const int lane = threadIdx.x & 63;
@@ -736,15 +737,9 @@ struct Kernel {
       const float c = a.scale / a.cap;
       const FarCap g = far_cap(a.cap, c);
       cap_far(g, 0.f, s);
-    } else {
-      const float c = a.scale * kLog2e;
-#pragma unroll
-      for (int i = 0; i < ST; ++i)
-#pragma unroll
-        for (int j = 0; j < AR; ++j) s[i][j] *= c;
     }
     if (!a.slopes) return;
-    const float slope = row.slope * kLog2e;
+    const float slope = a.cap > 0.f ? row.slope * kLog2e : row.slope / a.scale;
     if (ids) {
 #pragma unroll
       for (int i = 0; i < ST; ++i)
@@ -777,8 +772,11 @@ struct Kernel {
     for (int i = 0; i < ST; ++i) {
       const uint32_t w = see >> (i * MR) >> acc_row(0, lane);
 #pragma unroll
-      for (int j = 0; j < AR; ++j)
-        s[i][j] = w >> acc_row(j, 0) & 1 ? s[i][j] : -__builtin_inff();
+      for (int j = 0; j < AR; ++j) {
+        // the bit as a mask of all bits: the score or the bits of -inf
+        const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)w, acc_row(j, 0), 1);
+        s[i][j] = __uint_as_float((__float_as_uint(s[i][j]) & keep) | (0xff800000u & ~keep));
+      }
     }
   }
 
@@ -890,7 +888,7 @@ struct Kernel {
     for (int i = 0; i < OT; ++i)
 #pragma unroll
       for (int j = 0; j < AR; ++j) o[i][j] = 0.f;
-    const float sc = MODE == kPlain ? a.scale * kLog2e : 1.f;
+    const float sc = MODE == kPlain || (MODE == kBias && a.cap == 0.f) ? a.scale * kLog2e : 1.f;
 
     uint16_t* buf = reinterpret_cast<uint16_t*>(lds);
     constexpr int GB = NK * D;             // elements of one tensor of one group's step
