@@ -24,9 +24,9 @@
 //
 // Keys and values go through LDS: while one tile is used, the next one's rows
 // are on their way into registers and the page ids of the tile after it are
-// looked up. The 16-byte pieces of a row are permuted by the row's
-// low bits (swizzle) so that neither the row-wise nor the transposing reads
-// meet in a bank.
+// looked up. The 16-byte pieces of a row are permuted by the row's low bits
+// (swizzle) so that neither the row-wise nor the transposing reads meet in a bank
+// (counted: none at 8192 tokens).
 //
 // Batches of up to kPlanMax queries are planned: every workgroup sums the key
 // tiles of all segments (runs of queries of one sequence that share a row
@@ -34,6 +34,16 @@
 // equal runs, so that a ragged batch loads all CUs evenly. A segment that a cut
 // divides leaves unfinished parts, at most two a workgroup, which a second
 // launch joins in a fixed order. Larger batches take one workgroup per row tile.
+//
+// What bounds it (MI355X; a large copy moves 5.07 TB/s, a large bf16 product runs at
+// 1.29 PFLOP/s). Decode: memory; 8 sequences of up to 32768 tokens, 64 / 8 heads of
+// 128, read at 5.1 TB/s (145 us). Prompts: vector instructions; 8192 causal tokens
+// with capped scores take 1.4 ms, 0.78 PFLOP/s. A tile of 32 rows x 64 keys costs a
+// wave 1024 cycles of MFMA and some 1900 of vector issue (polynomial cap, exp2, sums,
+// rounding), and the two waves of a SIMD overlap little: 60% and 33% of the cycles.
+// Three waves a SIMD (spills at 168 registers), halves of the keys a step, the score
+// product split over two accumulators, and wave priorities around the products were
+// each measured slower or the same.
 #pragma once
 
 #include <type_traits>
@@ -87,7 +97,13 @@ enum Mode : int {
 
 // Tile shapes. NK keys per group of waves and step; KT = KW * NK keys a step.
 // With RW = 1 a wave's keys are its own: one LDS buffer and no barrier in the
-// loop. Otherwise the RW waves of a group share them, in two buffers.
+// loop (8 x 32768 tokens of decode: 148 us, 175 with barriers and one workgroup a
+// CU). Otherwise the RW waves of a group share them, in two buffers. Tiles of 64
+// rows split the keys over two groups of waves: one group of four waves of 16 rows
+// took 264 us for the selected prompt (2048 queries x 2048 tokens, 64 heads), one of
+// two waves 301, two of two 238. At d = 256 tiles of 32 rows take two waves of 16:
+// a wave of 32 rows holds 128 output registers and spills (139 -> 78 us for 4 x 4
+// queries of 16384 tokens).
 template <int D, int R>
 struct Shape {
   static_assert(D < 256 || R > 16, "head dimension 256 takes tiles of 32 rows and more");
@@ -342,6 +358,11 @@ struct Kernel {
   static constexpr int ST = KS / MR;               // score tiles of MR keys
   static constexpr int AR = MR * MR / 64;          // accumulator registers of a tile: 16 or 4
   static_assert(NLD >= 1 && NK % MR == 0, "tile shape");
+  // The values of a run of keys are read from LDS before its weights are worked out
+  // (selected prompt 237 -> 224 us) where the registers hold them: the other shapes
+  // and forms would spill.
+  static constexpr bool AHEAD = !GUARD && (D == 64 || (D == 256 ? R == 32 : R == 16 || (R == 64 && MODE == kPlain) ||
+                                                                               (R == 128 && (ALIGNED || MODE == kPlain))));
   using Acc = typename std::conditional<MR == 32, floatx16, floatx4>::type;
 
   __device__ static __forceinline__ Acc mma(const u32x4& x, const u32x4& y, const Acc& c) {
@@ -462,9 +483,11 @@ struct Kernel {
   }
 
   // Aligned pages (of a cache that ends before 4 GiB): a step's keys start at a
-  // multiple of WR, which divides the page, so that each wave's WR rows lie in one page. Lane j looks up the page of
-  // wave j's rows (every wave has to know which of them are keys); a wave's own
-  // page is then a scalar, and its rows follow each other.
+  // multiple of WR, which divides the page, so that each wave's WR rows lie in one
+  // page. Lane j looks up the page of wave j's rows (every wave has to know which of
+  // them are keys); a wave's own page is then a scalar, and its rows follow each
+  // other. It spares the shuffles and most of the arithmetic of the general look-up
+  // (8192-token capped prompt 1.65 -> 1.53 ms).
   __device__ static __forceinline__ int page_entry(const KvView& kv, const int32_t* table, int seq, int base, int end) {
     const int lane = threadIdx.x & 63;
     const int s = min(base + (lane & (RW - 1)) * WR, end - 1);
@@ -624,6 +647,16 @@ struct Kernel {
       const u32x4 w = weight_frag(s, p);
 #pragma unroll
       for (int i = 0; i < OT; ++i) o[i] = mma(vf[p][i], w, o[i]);
+    }
+  }
+
+  __device__ static __forceinline__ void accumulate_now(const uint16_t* vs, const Acc (&s)[ST], Acc (&o)[OT]) {
+    const uint32_t base = value_base(vs);
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const u32x4 w = weight_frag(s, p);
+#pragma unroll
+      for (int i = 0; i < OT; ++i) o[i] = mma(value_frag(base, p, i), w, o[i]);
     }
   }
 
@@ -963,19 +996,18 @@ struct Kernel {
         Acc s[ST];
         u32x4 kf[QF][ST];
         key_frags(ks + sub * KS * D, kf);
-        __builtin_amdgcn_sched_barrier(0);
+        if (AHEAD) __builtin_amdgcn_sched_barrier(0);   // all reads first
         score(kf, qf, s);
         const uint16_t* vs = ks + GB + sub * KS * D;
         u32x4 vf[NP][OT];
-        if constexpr (!GUARD) {
-          // asked for before the weights are worked out
+        if constexpr (AHEAD) {
           const uint32_t vb = value_base(vs);
 #pragma unroll
           for (int n = 0; n < NP; ++n)
 #pragma unroll
             for (int i = 0; i < OT; ++i) vf[n][i] = value_frag(vb, n, i);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        if (AHEAD) __builtin_amdgcn_sched_barrier(0);
         const bool full = have == ~0u && base >= all_lo && base + KS <= all_hi;
         const uint32_t see = have & bits_from(row.lo - base) & ~bits_from(row.hi - base);
         if constexpr (MODE == kBias) shape(a, s, row, ids, base, cur_token, sub);
@@ -1019,7 +1051,8 @@ struct Kernel {
           }
         sum += add[0] + add[1];
         if constexpr (GUARD) accumulate_guarded(vs, s, o, see);
-        else accumulate(vf, s, o);
+        else if constexpr (AHEAD) accumulate(vf, s, o);
+        else accumulate_now(vs, s, o);
       }
       if (S::buffers == 1) sync_rows();   // this wave has read what it now overwrites
       if (it + 1 < mine) land(it + 1);

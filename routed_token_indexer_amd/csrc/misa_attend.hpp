@@ -72,9 +72,9 @@ struct AttendArgs {
 // decode step no two queries share a sequence).
 int attend_rows(int64_t T, int64_t nseq, int group, int d, bool single);
 bool attend_planned(int64_t T, int64_t most_keys);
-// Workgroups of a planned launch, and its workspace.
+// Workgroups of a planned launch, and the workspace of a pass (the same whether a
+// batch of at most kPlanMax queries is planned or has too many key tiles for it).
 int attend_groups(int d, int R);
-// (which is the same for a planned batch and one that has too many key tiles for it).
 size_t attend_ws_bytes(int64_t T, int Hq, int heads, int d, int R, bool single, bool mixed);
 // Fills the fields that depend on the tile and carves the workspace.
 // mixed: rows of one part may see different keys, or not all keys of its steps

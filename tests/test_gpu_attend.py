@@ -333,8 +333,9 @@ def test_graph_replays_and_streams():
         A.check((out, lse), A.attend(q, kc, vc, seq, length, **kw), f"replay {i}")
 
 
-def test_rows_behind_32_bits():
-    """Keys and values beyond 2^32 elements of their caches."""
+@pytest.mark.parametrize("nq", [1, 40])
+def test_rows_behind_32_bits(nq):
+    """Keys and values beyond 2^32 elements of their caches, for small and large row tiles."""
     npages = 66000
     g = torch.Generator().manual_seed(9)
     kc = torch.empty(npages, 64, 8, 128, dtype=BF, device="cuda")
@@ -343,14 +344,12 @@ def test_rows_behind_32_bits():
     used = torch.tensor([npages - 1, 0, 32768, npages - 2])
     for x in (kc, vc):
         x[used.cuda()] = torch.randn(4, 64, 8, 128, generator=g).to(BF).cuda()
-    q = torch.randn(1, 16, 128, generator=g).to(BF).cuda()
+    q = torch.randn(nq, 64, 128, generator=g).to(BF).cuda()
     small = ints([[0, 1, 2, 3]])
-    got = M.attend(q, kc, vc, ints([0]), ints([250]), table=used[None].to(torch.int32).cuda(), want_lse=True)
-    want = M.attend(q, kc[used.cuda()].contiguous(), vc[used.cuda()].contiguous(), ints([0]), ints([250]), table=small,
-                    want_lse=True)
+    args = ints([0] * nq), ints([250 - nq + i + 1 for i in range(nq)])
+    got = M.attend(q, kc, vc, *args, table=used[None].to(torch.int32).cuda(), want_lse=True)
     torch.cuda.synchronize()
-    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-    A.check(got, A.attend(q, kc[used.cuda()], vc[used.cuda()], ints([0]), ints([250]), table=small), "behind 32 bits")
+    A.check(got, A.attend(q, kc[used.cuda()], vc[used.cuda()], *args, table=small), "behind 32 bits")
 
 
 # ---------------------------------------------------------------- selected tokens
