@@ -425,7 +425,7 @@ MISA_API int32_t misa_cache_append(const misa_kv_cache* cache, const void* k, in
  *   q_seq, q_len  int32 [T];  q_start  int32 [T] or NULL (0)
  *   q_pos    int32 [T] or NULL (q_len - 1), not negative; read with slopes only
  *   scale    in [1e-30, 1e30];  cap  0 (none) or in [1e-6, 1e30];  slopes  fp32 [Hq] or NULL
- *   out      [T][Hq][d] of the cache's type;  lse  fp32 [T][Hq] or NULL
+ *   out      [T][Hq][d] of the cache's type, apart from q;  lse  fp32 [T][Hq] or NULL
  * A query that sees nothing (empty interval, sequence out of range) gets zeros
  * and lse = -inf. q_len is clamped to what a sequence can address, q_start to
  * [0, q_len]. What a query does not see may hold anything, NaN included; a NaN

@@ -348,10 +348,14 @@ int32_t check_attend(const char* fn, const misa_kv_cache* c, const void* q, int6
   return MISA_OK;
 }
 
-int32_t check_attend_grid(const char* fn, const misa::AttendArgs& a) {
+// The last check of a call. A launch holds fewer than 2^32 threads, 256 a workgroup;
+// the join takes 4 rows a workgroup. out is written while other workgroups (and the
+// guarded second launch) still read q.
+int32_t check_attend_grid(const char* fn, const misa::AttendArgs& a, const void* out, bool joined) {
   const int64_t rows = a.T * (int64_t)a.Hq;
-  if (misa::attend_blocks(a) >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31))
+  if (misa::attend_blocks(a) >= (int64_t(1) << 24) || rows >= (int64_t(1) << (joined ? 26 : 31)))
     return fail(MISA_ERR_ARG, "%s: grid too large", fn);
+  if (out == a.q) return fail(MISA_ERR_ARG, "%s: out must not be q", fn);
   return MISA_OK;
 }
 
@@ -1103,7 +1107,7 @@ int32_t misa_attend(const misa_kv_cache* cache, const void* q, int64_t q_ts, int
   const bool single = T <= a.kv.nseq;
   const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, single);
   misa::attend_setup(a, R, single, !single || q_start, ws);
-  if ((rc = check_attend_grid(fn, a))) return rc;
+  if ((rc = check_attend_grid(fn, a, out, a.planned))) return rc;
   return run_attend(fn, a, R, cache->dtype == MISA_FP16, (hipStream_t)stream);
 }
 
@@ -1126,7 +1130,7 @@ int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q, int64_t 
   a.mode = misa::kAttendPlain;
   const int R = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, true);
   misa::attend_setup(a, R, true, false, ws);
-  if ((rc = check_attend_grid(fn, a))) return rc;
+  if ((rc = check_attend_grid(fn, a, out, a.planned))) return rc;
   return run_attend(fn, a, R, cache->dtype == MISA_FP16, (hipStream_t)stream);
 }
 
@@ -1188,7 +1192,7 @@ int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_
   const bool single = T <= a.kv.nseq;
   const int Ra = rows_of(T, a.kv.nseq, Hq, a.Hkv, a.d, single);
   misa::attend_setup(a, Ra, single, !single, p);
-  if ((rc = check_attend_grid(fn, a)) || (rc = check_attend_grid(fn, b))) return rc;
+  if ((rc = check_attend_grid(fn, a, out, true)) || (rc = check_attend_grid(fn, b, out, true))) return rc;
   const bool half = cache->dtype == MISA_FP16;
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = misa::launch_attend(b, Rb, half, st);

@@ -128,6 +128,17 @@ def test_attention_sizes(B, call):
     assert call(B, cache(B), T=0, q=None, seq=None, len=None, out=None, ws=None, ws_bytes=0) == 0
 
 
+@pytest.mark.parametrize("call", [attend, selected, shared])
+def test_grids_and_aliases(B, call):
+    """Launches of 2^32 threads or more, and outputs over the queries, are refused as a whole."""
+    assert call(B, cache(B), out=2 * FAKE, T=(1 << 31) - 1, Hq=8, ws_bytes=1 << 60) == -1 and "grid" in err(B)
+    # one query a workgroup, two kv heads: 2^24 workgroups
+    assert selected(B, cache(B), out=2 * FAKE, T=1 << 23) == -1 and "grid" in err(B)
+    # four rows a workgroup of the join
+    assert shared(B, cache(B), out=2 * FAKE, T=1 << 23, Hq=8, ws_bytes=1 << 60) == -1 and "grid" in err(B)
+    assert call(B, cache(B)) == -1 and "must not be q" in err(B)
+
+
 def test_own_arguments(B):
     assert attend(B, cache(B), start=FAKE + 2) == -2
     assert selected(B, cache(B), topk=0) == -1
