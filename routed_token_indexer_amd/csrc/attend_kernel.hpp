@@ -38,9 +38,9 @@
 // What bounds it (MI355X; a large copy moves 5.07 TB/s, a large bf16 product runs at
 // 1.29 PFLOP/s). Decode: memory; 8 sequences of up to 32768 tokens, 64 / 8 heads of
 // 128, read at 5.1 TB/s (145 us). Prompts: vector instructions; 8192 causal tokens
-// with capped scores take 1.4 ms, 0.78 PFLOP/s. A tile of 32 rows x 64 keys costs a
-// wave 1024 cycles of MFMA and some 1900 of vector issue (polynomial cap, exp2, sums,
-// rounding), and the two waves of a SIMD overlap little: 60% and 33% of the cycles.
+// with capped scores take 1.42 ms, 0.77 PFLOP/s. A tile of 32 rows x 64 keys costs a
+// wave 1024 cycles of MFMA and some 1600 of vector issue (polynomial cap, exp2, sums,
+// rounding), and the two waves of a SIMD overlap little: 35% and 52% of the cycles.
 // Three waves a SIMD (spills at 168 registers), halves of the keys a step, the score
 // product split over two accumulators, and wave priorities around the products were
 // each measured slower or the same.
