@@ -247,6 +247,27 @@ def test_caps(cap, bias, nq):
     A.check(got, A.attend(q, kc, vc, seq, length, **kw), f"cap {cap}")
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [20, 64])
+@pytest.mark.parametrize("nq", [3, 320])
+def test_caps_by_size_of_the_scores(nq, page, d):
+    """Row tiles of small, middling and large scores against one cap: up to 0.18, up to
+    0.35 and beyond of it, which take different forms; pages that hold whole groups of
+    rows and others."""
+    g = torch.Generator().manual_seed(43)
+    kc, vc, table = cache(g, 1, (400 + page - 1) // page, page, 2, d, BF)
+    q = torch.randn(nq, 16, d, generator=g)
+    sizes = [0.05, 1.0, 1.8, 8.0]
+    for i in range(nq):
+        q[i] *= sizes[i * 4 // nq]
+    q = q.to(BF).cuda()
+    seq, length = ints([0] * nq), ints([400 - nq + i + 1 for i in range(nq)])
+    kw = dict(table=table, cap=24.0)
+    got = M.attend(q, kc, vc, seq, length, want_lse=True, **kw)
+    torch.cuda.synchronize()
+    A.check(got, A.attend(q, kc, vc, seq, length, **kw), f"d {d} page {page}")
+
+
 def test_infinite_scores_of_visible_keys():
     """Keys that overflow to infinity: NaN as in the formula without a cap, the cap
     itself with one; rows of other heads and queries stay."""
