@@ -292,10 +292,10 @@ constexpr float kTanh[4] = {0.9999999403953552f, -0.33332425355911255f, 0.132958
 constexpr float kNearest = 0.18f;
 constexpr float kTanh2[3] = {0.9999999403953552f, -0.3333021402359009f, 0.13075149059295654f};
 
-// Caps up to this one take 1 - 2 / (1 + e^2y) beyond kNear and, in a tile that has
-// such scores, for the others too: exp2, the sum and the reciprocal lose at most
+// Caps up to this one take 1 - 2 / (1 + e^2y) beyond kNear and, in a tile that every
+// row sees whole and that has such scores, for the others too: exp2, the sum and the reciprocal lose at most
 // 9 half steps of fp32 of one, times the cap (1.4e-4 of a score at the limit,
-// 3e-5 at 50). Larger caps choose for each score.
+// 3e-5 at 50). Larger caps, and tiles that are seen in part, choose for each score.
 constexpr float kPlainCap = 256.f;
 
 // The cap in units of log2 for scores of |y| <= kNear: x P(x^2), y = c x.
@@ -1058,12 +1058,21 @@ struct Kernel {
             for (int i = 0; i < ST; ++i)
 #pragma unroll
               for (int j = 0; j < AR; ++j) s[i][j] = __builtin_fmaf(s[i][j], f.factor(s[i][j]), -off);
-          } else {
+          } else if (full) {
 #pragma unroll
             for (int i = 0; i < ST; ++i)
 #pragma unroll
               for (int j = 0; j < AR; ++j) s[i][j] = g.plain(s[i][j], off);
-            if (!full) hide(see, s);   // tanh(-inf) is finite
+          } else {
+            // the ends of intervals, which may be all that a row sees: chosen per score
+#pragma unroll
+            for (int i = 0; i < ST; ++i)
+#pragma unroll
+              for (int j = 0; j < AR; ++j) {
+                s[i][j] = g.chosen(s[i][j], off);
+                if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few scores' terms at a time
+              }
+            hide(see, s);   // tanh(-inf) is finite
           }
         } else {
           follow(mx, slack, sc, m, sum, o);
