@@ -38,7 +38,7 @@
 // What bounds it (MI355X; a large copy moves 5.07 TB/s, a large bf16 product runs at
 // 1.29 PFLOP/s). Decode: memory; 8 sequences of up to 32768 tokens, 64 / 8 heads of
 // 128, read at 5.1 TB/s (145 us). Prompts: vector instructions; 8192 causal tokens
-// with capped scores take 1.42 ms, 0.77 PFLOP/s. A tile of 32 rows x 64 keys costs a
+// with capped scores take 1.41 ms, 0.78 PFLOP/s. A tile of 32 rows x 64 keys costs a
 // wave 1024 cycles of MFMA and some 1600 of vector issue (polynomial cap, exp2, sums,
 // rounding), and the two waves of a SIMD overlap little: 35% and 52% of the cycles.
 // Three waves a SIMD (spills at 168 registers), halves of the keys a step, the score
@@ -293,9 +293,10 @@ constexpr float kNearest = 0.18f;
 constexpr float kTanh2[3] = {0.9999999403953552f, -0.3333021402359009f, 0.13075149059295654f};
 
 // Caps up to this one take 1 - 2 / (1 + e^2y) beyond kNear and, in a tile that every
-// row sees whole and that has such scores, for the others too: exp2, the sum and the reciprocal lose at most
-// 9 half steps of fp32 of one, times the cap (1.4e-4 of a score at the limit,
-// 3e-5 at 50). Larger caps, and tiles that are seen in part, choose for each score.
+// row sees whole and that has such scores, for the others too: exp2, the sum and the
+// reciprocal lose at most 9 half steps of fp32 of one, times the cap (1.4e-4 of a
+// score at the limit, 3e-5 at 50). Larger caps, and tiles that are seen in part,
+// choose for each score.
 constexpr float kPlainCap = 256.f;
 
 // The cap in units of log2 for scores of |y| <= kNear: x P(x^2), y = c x.
