@@ -463,6 +463,19 @@ def _call(device, name: str, *args):
         _check(name, rc)
 
 
+def _empty(shape, dtype, device, stream, returned: bool = True):
+    """An output or workspace that a call makes itself, from the memory of the stream that it launches on: a block
+    that the allocator hands out again then has no user left but earlier work of that stream. What is returned is read
+    on the current stream, so its release waits for that one as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        x = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        x.record_stream(torch.cuda.current_stream(device))
+    return x
+
+
 def attend_workspace_bytes(op: int, T: int, Hq: int, heads: int, d: int, nseq: int, npre: int = 0) -> int:
     return int(lib().misa_attend_workspace_bytes(op, T, Hq, heads, d, nseq, npre))
 
@@ -491,7 +504,7 @@ def cache_append(k, v, k_cache, v_cache, q_seq, q_tok, table=None, q=None, q_out
         q_ts, q_hs = _rows(q, "q", k_cache, N)
         Hq = q.shape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = _empty(q.shape, q.dtype, dev, stream)
         o_ts, o_hs = _rows(q_out, "q_out", k_cache, N, Hq)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -509,7 +522,7 @@ def cache_append(k, v, k_cache, v_cache, q_seq, q_tok, table=None, q=None, q_out
     return q_out
 
 
-def _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale, slopes, out, lse, want_lse):
+def _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale, slopes, out, lse, want_lse, stream):
     if v_cache is None:
         raise ValueError("v_cache: attention needs values")
     c = _kv_cache(k_cache, v_cache, table)
@@ -519,9 +532,9 @@ def _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale, slope
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        out = _empty((T, Hq, d), q.dtype, dev, stream)
     if lse is None and want_lse:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((T, Hq), torch.float32, dev, stream)
     ptrs = (_vec(q_seq, "q_seq", torch.int32, (T,), dev), _vec(q_len, "q_len", torch.int32, (T,), dev),
             _vec(q_pos, "q_pos", torch.int32, (T,), dev), _vec(slopes, "slopes", torch.float32, (Hq,), dev),
             _vec(out, "out", k_cache.dtype, (T, Hq, d), dev), _vec(lse, "lse", torch.float32, (T, Hq), dev))
@@ -537,10 +550,7 @@ def _attend_ws(ws, op, T, Hq, c, dev, stream, npre=0):
             raise TypeError("ws: expected a contiguous torch.uint8 tensor")
         if ws.numel() >= need:
             return ws
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-    if stream is not None:
-        ws.record_stream(stream)   # dropped on return: its memory waits for that stream
-    return ws
+    return _empty(max(need, 256), torch.uint8, dev, stream, returned=False)
 
 
 def attend(q, k_cache, v_cache, q_seq, q_len, table=None, q_start=None, q_pos=None, scale=None, cap=0.0, slopes=None,
@@ -551,7 +561,7 @@ def attend(q, k_cache, v_cache, q_seq, q_len, table=None, q_start=None, q_pos=No
     > 0 caps the scores by cap * tanh(x / cap); ``slopes`` [Hq] subtracts
     slope * |q_pos - s| (q_pos default: q_len - 1)."""
     c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
-                                                                   slopes, out, lse, want_lse)
+                                                                   slopes, out, lse, want_lse, stream)
     ws = _attend_ws(ws, OP_ATTEND, T, Hq, c, dev, stream)
     _call(dev, "misa_attend", ctypes.byref(c), q.data_ptr(), q_ts, q_hs, p[0],
           _vec(q_start, "q_start", torch.int32, (T,), dev), p[1], p[2], T, Hq, scale, cap, p[3], p[4], p[5],
@@ -564,7 +574,7 @@ def attend_selected(q, k_cache, v_cache, idx, q_seq, q_len, table=None, q_pos=No
     """As ``attend``, over the tokens idx [T, topk] that an indexer selected
     (entries outside [0, q_len) are skipped)."""
     c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
-                                                                   slopes, out, lse, want_lse)
+                                                                   slopes, out, lse, want_lse, stream)
     if idx.dim() != 2:
         raise ValueError(f"idx: expected 2 dims, got shape {tuple(idx.shape)}")
     topk = idx.shape[1]
@@ -581,7 +591,7 @@ def attend_shared(q, k_cache, v_cache, q_seq, q_len, pre, pre_len, table=None, p
     pre_len[pre[t]] tokens of prefix pre[t] (pages pre_table [npre, cols]; without
     a table prefix i is page i), then the q_len[t] tokens of its own sequence."""
     c, dev, q_ts, q_hs, T, Hq, scale, out, lse, p = _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale,
-                                                                   slopes, out, lse, want_lse)
+                                                                   slopes, out, lse, want_lse, stream)
     npre = pre_len.shape[0]
     cols = 0
     if pre_table is not None:
