@@ -147,14 +147,28 @@ def _req(x: torch.Tensor, dtype, name: str, ndim: int):
         raise ValueError(f"{name}: must be contiguous")
 
 
+def _empty(shape, dtype, device, stream, returned: bool = True, zeros: bool = False):
+    """An output or workspace that a call makes itself, from the memory of the stream that it launches on: a block
+    that the allocator hands out again then has no user left but earlier work of that stream. What is returned is read
+    on the current stream, so its release waits for that one as well."""
+    make = torch.zeros if zeros else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        x = make(shape, dtype=dtype, device=device)
+    if returned:
+        x.record_stream(torch.cuda.current_stream(device))
+    return x
+
+
 def workspace_bytes(op: int, T: int, H: int, Lmax: int, B: int = 0, topk: int = 0, kc: int = 0) -> int:
     return int(lib().misa_workspace_bytes(op, T, H, Lmax, B, topk, kc))
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+def _workspace(ws: Optional[torch.Tensor], need: int, device, stream) -> torch.Tensor:
     if ws is not None and ws.numel() >= need:
         return ws
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return _empty(max(need, 256), torch.uint8, device, stream, returned=False)
 
 
 def pool_keys(k: torch.Tensor, B: int, kbar: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -162,7 +176,7 @@ def pool_keys(k: torch.Tensor, B: int, kbar: Optional[torch.Tensor] = None, stre
     _req(k, torch.bfloat16, "k", 3)
     nseq, L, d = k.shape
     if kbar is None:
-        kbar = torch.empty((nseq, L // B, d), dtype=torch.float32, device=k.device)
+        kbar = _empty((nseq, L // B, d), torch.float32, k.device, stream)
     _check("misa_pool_keys", lib().misa_pool_keys(_ptr(k), nseq, L, d, B, _ptr(kbar), _stream(stream)))
     return kbar
 
@@ -184,19 +198,19 @@ def route(q, w, k, kbar, q_seq, q_len, B: int, h: int, heads=None, router_key=No
     T, H, d = q.shape
     nseq, L, _ = k.shape
     if heads is None:
-        heads = torch.empty((T, h), dtype=torch.int32, device=q.device)
-    ws = _workspace(ws, workspace_bytes(OP_ROUTE, T, H, L, B), q.device)
+        heads = _empty((T, h), torch.int32, q.device, stream)
+    ws = _workspace(ws, workspace_bytes(OP_ROUTE, T, H, L, B), q.device, stream)
     _check("misa_route", lib().misa_route(_ptr(q), _ptr(w), _ptr(k), _ptr(kbar), _ptr(q_seq), _ptr(q_len), T, H, d,
                                           nseq, L, B, h, _ptr(heads), _ptr(router_key), _ptr(ws), ws.numel(),
                                           _stream(stream)))
     return heads
 
 
-def _outs(T, topk, device, idx, score, want_score):
+def _outs(T, topk, device, idx, score, want_score, stream):
     if idx is None:
-        idx = torch.empty((T, topk), dtype=torch.int32, device=device)
+        idx = _empty((T, topk), torch.int32, device, stream)
     if score is None and want_score:
-        score = torch.empty((T, topk), dtype=torch.float32, device=device)
+        score = _empty((T, topk), torch.float32, device, stream)
     return idx, score
 
 
@@ -207,8 +221,8 @@ def score_topk(q, w, k, heads, q_seq, q_len, topk: int, idx=None, score=None, wa
     _req(heads, torch.int32, "heads", 2)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_SCORE_TOPK, T, H, L, 0, topk), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_SCORE_TOPK, T, H, L, 0, topk), q.device, stream)
     _check("misa_score_topk", lib().misa_score_topk(_ptr(q), _ptr(w), _ptr(k), _ptr(heads), heads.shape[1],
                                                     _ptr(q_seq), _ptr(q_len), T, H, d, nseq, L, topk, _ptr(idx),
                                                     _ptr(score), _ptr(ws), ws.numel(), _stream(stream)))
@@ -223,8 +237,8 @@ def hier_rerank(q, w, k, cand, q_seq, q_len, topk: int, idx=None, score=None, wa
     T, H, d = q.shape
     nseq, L, _ = k.shape
     kc = cand.shape[1]
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_HIER_RERANK, T, H, L, 0, topk, kc), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_HIER_RERANK, T, H, L, 0, topk, kc), q.device, stream)
     _check("misa_hier_rerank", lib().misa_hier_rerank(_ptr(q), _ptr(w), _ptr(k), _ptr(cand), kc, _ptr(q_seq),
                                                       _ptr(q_len), T, H, d, nseq, L, topk, _ptr(idx), _ptr(score),
                                                       _ptr(ws), ws.numel(), _stream(stream)))
@@ -237,8 +251,8 @@ def dsa_index_dense(q, w, k, q_seq, q_len, topk: int, idx=None, score=None, want
     _req(q, torch.bfloat16, "q", 3)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_DSA_DENSE, T, H, L, 0, topk), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_DSA_DENSE, T, H, L, 0, topk), q.device, stream)
     _check("dsa_index_dense", lib().dsa_index_dense(_ptr(q), _ptr(w), _ptr(k), _ptr(q_seq), _ptr(q_len), T, H, d,
                                                     nseq, L, topk, _ptr(idx), _ptr(score), _ptr(ws), ws.numel(),
                                                     _stream(stream)))
@@ -251,8 +265,8 @@ def indexer(q, w, k, kbar, q_seq, q_len, B: int, h: int, topk: int, heads=None, 
     _req(q, torch.bfloat16, "q", 3)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_INDEXER, T, H, L, B, topk), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_INDEXER, T, H, L, B, topk), q.device, stream)
     _check("misa_indexer", lib().misa_indexer(_ptr(q), _ptr(w), _ptr(k), _ptr(kbar), _ptr(q_seq), _ptr(q_len), T, H,
                                               d, nseq, L, B, h, topk, _ptr(heads), _ptr(idx), _ptr(score), _ptr(ws),
                                               ws.numel(), _stream(stream)))
@@ -265,8 +279,8 @@ def hier_indexer(q, w, k, kbar, q_seq, q_len, B: int, h: int, kc: int, topk: int
     _req(q, torch.bfloat16, "q", 3)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_HIER_INDEXER, T, H, L, B, topk, kc), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_HIER_INDEXER, T, H, L, B, topk, kc), q.device, stream)
     _check("misa_hier_indexer", lib().misa_hier_indexer(_ptr(q), _ptr(w), _ptr(k), _ptr(kbar), _ptr(q_seq),
                                                         _ptr(q_len), T, H, d, nseq, L, B, h, kc, topk, _ptr(heads),
                                                         _ptr(cand), _ptr(idx), _ptr(score), _ptr(ws), ws.numel(),
@@ -285,10 +299,10 @@ def block_filter(q, w, kbar, heads, q_seq, q_len, Lmax: int, B: int, m: int, blo
     T, H, d = q.shape
     nseq = kbar.shape[0]
     if blocks is None:
-        blocks = torch.empty((T, m), dtype=torch.int32, device=q.device)
+        blocks = _empty((T, m), torch.int32, q.device, stream)
     if cand is None and want_cand:
-        cand = torch.empty((T, (m + 1) * B), dtype=torch.int32, device=q.device)
-    ws = _workspace(ws, workspace_bytes(OP_BLOCK_FILTER, T, H, Lmax, B, 0, m), q.device)
+        cand = _empty((T, (m + 1) * B), torch.int32, q.device, stream)
+    ws = _workspace(ws, workspace_bytes(OP_BLOCK_FILTER, T, H, Lmax, B, 0, m), q.device, stream)
     _check("misa_block_filter", lib().misa_block_filter(_ptr(q), _ptr(w), _ptr(kbar), _ptr(heads), heads.shape[1],
                                                         _ptr(q_seq), _ptr(q_len), T, H, d, nseq, Lmax, B, m,
                                                         _ptr(blocks), _ptr(cand), _ptr(ws), ws.numel(),
@@ -302,8 +316,8 @@ def block_indexer(q, w, k, kbar, q_seq, q_len, B: int, h: int, m: int, topk: int
     _req(q, torch.bfloat16, "q", 3)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_BLOCK_INDEXER, T, H, L, B, topk, m), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_BLOCK_INDEXER, T, H, L, B, topk, m), q.device, stream)
     _check("misa_block_indexer", lib().misa_block_indexer(_ptr(q), _ptr(w), _ptr(k), _ptr(kbar), _ptr(q_seq),
                                                           _ptr(q_len), T, H, d, nseq, L, B, h, m, topk, _ptr(heads),
                                                           _ptr(blocks), _ptr(idx), _ptr(score), _ptr(ws), ws.numel(),
@@ -318,8 +332,8 @@ def pivot_indexer(q, w, k, q_seq, q_len, G: int, kc: int, topk: int, cand=None, 
     _req(q, torch.bfloat16, "q", 3)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
-    ws = _workspace(ws, workspace_bytes(OP_PIVOT_INDEXER, T, H, L, G, topk, kc), q.device)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
+    ws = _workspace(ws, workspace_bytes(OP_PIVOT_INDEXER, T, H, L, G, topk, kc), q.device, stream)
     _check("misa_pivot_indexer", lib().misa_pivot_indexer(_ptr(q), _ptr(w), _ptr(k), _ptr(q_seq), _ptr(q_len), T, H,
                                                           d, nseq, L, G, kc, topk, _ptr(cand), _ptr(idx), _ptr(score),
                                                           _ptr(ws), ws.numel(), _stream(stream)))
@@ -332,7 +346,7 @@ def debug_scores(q, w, k, heads, q_seq, q_len, out=None, stream=None):
     T, H, d = q.shape
     nseq, L, _ = k.shape
     if out is None:
-        out = torch.zeros((T, L), dtype=torch.float32, device=q.device)
+        out = _empty((T, L), torch.float32, q.device, stream, zeros=True)
     h = H if heads is None else heads.shape[1]
     _check("misa_debug_scores", lib().misa_debug_scores(_ptr(q), _ptr(w), _ptr(k), _ptr(heads), h, _ptr(q_seq),
                                                         _ptr(q_len), T, H, d, nseq, L, _ptr(out), _stream(stream)))
@@ -346,7 +360,7 @@ def hier_indexer_noalloc(q, w, k, kbar, q_seq, q_len, B: int, h: int, kc: int, t
     _req(q, torch.bfloat16, "q", 3)
     T, H, d = q.shape
     nseq, L, _ = k.shape
-    idx, score = _outs(T, topk, q.device, idx, score, want_score)
+    idx, score = _outs(T, topk, q.device, idx, score, want_score, stream)
     _check("misa_hier_indexer_noalloc",
            lib().misa_hier_indexer_noalloc(_ptr(q), _ptr(w), _ptr(k), _ptr(kbar), _ptr(q_seq), _ptr(q_len), T, H, d,
                                            nseq, L, B, h, kc, topk, _ptr(heads), _ptr(cand), _ptr(idx), _ptr(score),
@@ -461,19 +475,6 @@ def _call(device, name: str, *args):
             rc = fn(*args)
     if rc != MISA_OK:
         _check(name, rc)
-
-
-def _empty(shape, dtype, device, stream, returned: bool = True):
-    """An output or workspace that a call makes itself, from the memory of the stream that it launches on: a block
-    that the allocator hands out again then has no user left but earlier work of that stream. What is returned is read
-    on the current stream, so its release waits for that one as well."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        x = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        x.record_stream(torch.cuda.current_stream(device))
-    return x
 
 
 def attend_workspace_bytes(op: int, T: int, Hq: int, heads: int, d: int, nseq: int, npre: int = 0) -> int:

@@ -87,3 +87,25 @@ def test_results_dropped_while_they_are_read(big):
     torch.cuda.synchronize()
     assert torch.equal(copy, want)
     del other
+
+
+def test_an_indexer_on_a_stream_of_its_own(big):
+    g = torch.Generator().manual_seed(8)
+    q, k = torch.randn(4, 8, 128, generator=g).to(BF).cuda(), torch.randn(2, 512, 128, generator=g).to(BF).cuda()
+    w = torch.rand(4, 8, generator=g).cuda()
+    seq = torch.tensor([0, 0, 1, 1], dtype=torch.int32, device="cuda")
+    length = torch.tensor([511, 512, 300, 301], dtype=torch.int32, device="cuda")
+    kbar = M.pool_keys(k, 32)
+    want = M.indexer(q, w, k, kbar, seq, length, 32, 4, 64)
+    rows = M.debug_scores(q, w, k, None, seq, length)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    queue_work(*big)
+    junk = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for n in (1 << 9, 1 << 10, 1 << 13, 1 << 16, 1 << 21, 1 << 25)
+            for _ in range(2)]
+    del junk
+    got = M.indexer(q, w, k, kbar, seq, length, 32, 4, 64, stream=side) + (
+        M.debug_scores(q, w, k, None, seq, length, stream=side), M.pool_keys(k, 32, stream=side))
+    assert all(home(x) == side.cuda_stream for x in got)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, (*want, rows, kbar)))

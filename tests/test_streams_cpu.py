@@ -88,3 +88,30 @@ def test_cache_and_attention(made, name):
     else:
         r = M.attend_shared(q, kc, kc, i, i, i, i, want_lse=True, stream=side)
     check(made, r)
+
+
+INDEXERS = {
+    "pool_keys": lambda x, s: M.pool_keys(x["k"], 8, stream=s),
+    "route": lambda x, s: M.route(x["q"], x["w"], x["k"], x["kbar"], x["i"], x["i"], 8, 2, stream=s),
+    "score_topk": lambda x, s: M.score_topk(x["q"], x["w"], x["k"], x["heads"], x["i"], x["i"], 4, stream=s),
+    "hier_rerank": lambda x, s: M.hier_rerank(x["q"], x["w"], x["k"], x["heads"], x["i"], x["i"], 2, stream=s),
+    "dsa_index_dense": lambda x, s: M.dsa_index_dense(x["q"], x["w"], x["k"], x["i"], x["i"], 4, stream=s),
+    "indexer": lambda x, s: M.indexer(x["q"], x["w"], x["k"], x["kbar"], x["i"], x["i"], 8, 2, 4, stream=s),
+    "hier_indexer": lambda x, s: M.hier_indexer(x["q"], x["w"], x["k"], x["kbar"], x["i"], x["i"], 8, 2, 8, 4, stream=s),
+    "hier_indexer_noalloc": lambda x, s: M.hier_indexer_noalloc(x["q"], x["w"], x["k"], x["kbar"], x["i"], x["i"], 8, 2, 8,
+                                                               4, stream=s),
+    "block_filter": lambda x, s: M.block_filter(x["q"], x["w"], x["kbar"], x["heads"], x["i"], x["i"], 32, 8, 2, stream=s),
+    "block_indexer": lambda x, s: M.block_indexer(x["q"], x["w"], x["k"], x["kbar"], x["i"], x["i"], 8, 2, 2, 4, stream=s),
+    "pivot_indexer": lambda x, s: M.pivot_indexer(x["q"], x["w"], x["k"], x["i"], x["i"], 2, 8, 4, stream=s),
+    "debug_scores": lambda x, s: M.debug_scores(x["q"], x["w"], x["k"], None, x["i"], x["i"], stream=s),
+}
+
+
+@pytest.mark.parametrize("name", list(INDEXERS))
+def test_indexers(made, name):
+    bf, i32 = torch.bfloat16, torch.int32
+    x = dict(q=torch.randn(2, 4, 128).to(bf), w=torch.randn(2, 4), k=torch.randn(2, 32, 128).to(bf),
+             kbar=torch.randn(2, 4, 128), heads=torch.zeros(2, 2, dtype=i32), i=torch.zeros(2, dtype=i32))
+    x = {n: dev(t) for n, t in x.items()}
+    made[0].clear()
+    check(made, INDEXERS[name](x, Stream("side")))
