@@ -116,12 +116,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Pass pa, Pass pb, int6
       // maxima and sums of the chunk's parts, one a lane
       const int i = base + lane;
       float m = -__builtin_inff(), s = 0.f;
+      bool part_here = false;
       if (lane < CH && i <= x.i1) {
         const float* ml = p.part_ml + ((2 * (int64_t)i + (i == second ? 1 : 0)) * p.R + x.r) * 2;
         const float m1 = ml[0], s1 = ml[1];
         if (i * x.units / G != ((int64_t)i + 1) * x.units / G) {   // a workgroup with work
           m = m1;
           s = s1;
+          part_here = true;
         }
       }
       float top = m;
@@ -134,11 +136,14 @@ __global__ __launch_bounds__(256) void attend_join_kernel(Pass pa, Pass pb, int6
       sum = sum * old + wave_sum(s * w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] *= old;
+      // Where there is no part y is anything and is left out (-1); a part whose weight
+      // vanishes is not: a NaN or an infinity among its values reaches the row.
+      const float mark = part_here ? w : -1.f;
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const float wk = __shfl(w, k * GR + g, 64);
+        const float wk = __shfl(mark, k * GR + g, 64);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] += wk == 0.f ? 0.f : y[k][j] * wk;   // no part: y is anything
+        for (int j = 0; j < 4; ++j) o[j] += wk == -1.f ? 0.f : y[k][j] * wk;
       }
     }
   }
