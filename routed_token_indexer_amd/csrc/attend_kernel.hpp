@@ -749,6 +749,21 @@ struct Kernel {
     return mx;
   }
 
+  // The exponent (of 2) that a row's weights and sums are relative to: its reference m
+  // or, for weights in fp16, kLift below it. Those weights are then normal numbers down
+  // to 2^-21 of the row's largest and zero below 2^-32 of it, not 2^-14 and 2^-25:
+  // thousands of keys that small, beside one whose value is near zero, make the
+  // result. The largest stays below 2^15: `follow` lets it pass 2^m by 2^8, and the
+  // rounding up by 2^-22 covers those of the products that it is compared by.
+  static constexpr float kLift = HALF ? 7.f : 0.f;
+  __device__ static __forceinline__ float reference(float m, float sc) {
+    const float r = m * sc;
+    return HALF && m != -__builtin_inff() ? __builtin_fmaf(fabsf(r), 0x1p-22f, r) - kLift : r;
+  }
+  __device__ static __forceinline__ float finite_reference(float m, float sc) {
+    return m == -__builtin_inff() ? 0.f : reference(m, sc);
+  }
+
   // Moves the reference m where a row's maximum mx (of this lane's row, over all of
   // its keys of the step) passes it by more than slack.
   __device__ static __forceinline__ void follow(float mx, float slack, float sc, float& m, float& sum, Acc (&o)[OT]) {
@@ -1047,7 +1062,7 @@ struct Kernel {
           const NearCap f = near_cap(a.cap, cap_c);
           const FarCap g = far_cap(a.cap, cap_c);
           follow(near ? mx * f.factor(mx) : g.plain(mx, 0.f), slack, sc, m, sum, o);
-          const float off = m == -__builtin_inff() ? 0.f : m;
+          const float off = finite_reference(m, sc);
           if (nearest) {
             const NearestCap f2 = nearest_cap(a.cap, cap_c);
 #pragma unroll
@@ -1077,7 +1092,7 @@ struct Kernel {
           }
         } else {
           follow(mx, slack, sc, m, sum, o);
-          const float off = (m == -__builtin_inff() ? 0.f : m) * sc;
+          const float off = finite_reference(m, sc);
 #pragma unroll
           for (int i = 0; i < ST; ++i)
 #pragma unroll
@@ -1100,7 +1115,7 @@ struct Kernel {
       if (it + 1 < mine) land(it + 1);
       sync_rows();
     }
-    finish(fresh(ap), p, sp, lds, odd, r, kw, m * sc, sum, o);
+    finish(fresh(ap), p, sp, lds, odd, r, kw, reference(m, sc), sum, o);
   }
 
   // The end of a part: joins the groups of waves and writes the rows.
