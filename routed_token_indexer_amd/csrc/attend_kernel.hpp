@@ -292,11 +292,13 @@ constexpr float kTanh[4] = {0.9999999403953552f, -0.33332425355911255f, 0.132958
 constexpr float kNearest = 0.18f;
 constexpr float kTanh2[3] = {0.9999999403953552f, -0.3333021402359009f, 0.13075149059295654f};
 
-// Caps up to this one take 1 - 2 / (1 + e^2y) beyond kNear and, in a tile that every
-// row sees whole and that has such scores, for the others too: exp2, the sum and the
-// reciprocal lose at most 9 half steps of fp32 of one, times the cap (1.4e-4 of a
-// score at the limit, 3e-5 at 50). Larger caps, and tiles that are seen in part,
-// choose for each score.
+// Caps up to this one take 1 - 2 / (1 + e^2y) for all scores of a run of keys that
+// every row sees whole, where one of them is beyond kNear or the cap goes with a
+// distance bias: exp2, the sum and the reciprocal lose at most 9 half steps of fp32
+// of one, times the cap (1.4e-4 of a score at the limit, 3e-5 at 50), for rows that
+// see these 32 keys at least. Larger caps, runs that are seen in part and the
+// guarded form choose for each score. Choosing everywhere: an 8192-token prompt with
+// scores up to the cap 1525 -> 1846 us.
 constexpr float kPlainCap = 256.f;
 
 // The cap in units of log2 for scores of |y| <= kNear: x P(x^2), y = c x.
@@ -778,8 +780,8 @@ struct Kernel {
     m = mn;
   }
 
-  __device__ static __forceinline__ void cap_far(const FarCap& g, float off, Acc (&s)[ST]) {
-    if (g.choose) {
+  __device__ static __forceinline__ void cap_far(const FarCap& g, bool choose, float off, Acc (&s)[ST]) {
+    if (GUARD || choose) {
 #pragma unroll
       for (int i = 0; i < ST; ++i)
 #pragma unroll
@@ -795,12 +797,12 @@ struct Kernel {
   // Cap and bias. Capped scores leave in units of log2, others still without the
   // scale (the bias divided by it).
   __device__ static __forceinline__ void shape(const AttendArgs& a, Acc (&s)[ST], const Rows& row, const int32_t* ids, int base,
-                                               int token, int sub) {
+                                               int token, int sub, bool full) {
     const int lane = threadIdx.x & 63;
     if (a.cap > 0.f) {
       const float c = a.scale / a.cap;
       const FarCap g = far_cap(a.cap, c);
-      cap_far(g, 0.f, s);
+      cap_far(g, g.choose || !full, 0.f, s);
     }
     if (!a.slopes) return;
     const float slope = a.cap > 0.f ? row.slope * kLog2e : row.slope / a.scale;
@@ -1044,15 +1046,31 @@ struct Kernel {
         // (8192-token prompt 1458 -> 1428 us; selected tokens, whose pages are not
         // aligned, 226 -> 229, so theirs are always)
         uint32_t see = ALIGNED ? 0u : have & bits_from(row.lo - base) & ~bits_from(row.hi - base);
-        if constexpr (MODE == kBias) shape(a, s, row, ids, base, cur_token, sub);
+        if constexpr (MODE == kBias) shape(a, s, row, ids, base, cur_token, sub, full);
         if (!full) {
           if (ALIGNED) see = have & bits_from(row.lo - base) & ~bits_from(row.hi - base);
+          if constexpr (MODE == kCap) {
+            // The ends of intervals, which may be all that a row sees: chosen per score,
+            // before the maximum. The form's terms are made here: kept in the loop they
+            // take its registers (d = 128, 32 rows a tile: 91 spilled, 10 like this; 4 x 4
+            // queries of 16384 tokens 72 -> 57 us).
+            float cap = a.cap, c = cap_c;
+            asm volatile("" : "+s"(cap), "+v"(c));
+            const FarCap g = far_cap(cap, c);
+#pragma unroll
+            for (int i = 0; i < ST; ++i)
+#pragma unroll
+              for (int j = 0; j < AR; ++j) {
+                s[i][j] = g.chosen(s[i][j], 0.f);
+                if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few scores' terms at a time
+              }
+          }
           hide(see, s);
         }
         float mx = over_rows_max(highest(s));
         if constexpr (MODE == kCap) {
-          // the cap grows with the score, so the maximum is taken before it and the
-          // reference is subtracted in its last step
+          // the cap grows with the score, so where all keys are seen the maximum is
+          // taken before it and the reference is subtracted in its last step
           bool near = near_holds && full, nearest = false;
           if (near) {
             const float big = largest(s) * cap_c;
@@ -1061,7 +1079,7 @@ struct Kernel {
           }
           const NearCap f = near_cap(a.cap, cap_c);
           const FarCap g = far_cap(a.cap, cap_c);
-          follow(near ? mx * f.factor(mx) : g.plain(mx, 0.f), slack, sc, m, sum, o);
+          follow(!full ? mx : near ? mx * f.factor(mx) : g.plain(mx, 0.f), slack, sc, m, sum, o);
           const float off = finite_reference(m, sc);
           if (nearest) {
             const NearestCap f2 = nearest_cap(a.cap, cap_c);
@@ -1080,15 +1098,10 @@ struct Kernel {
 #pragma unroll
               for (int j = 0; j < AR; ++j) s[i][j] = g.plain(s[i][j], off);
           } else {
-            // the ends of intervals, which may be all that a row sees: chosen per score
 #pragma unroll
             for (int i = 0; i < ST; ++i)
 #pragma unroll
-              for (int j = 0; j < AR; ++j) {
-                s[i][j] = g.chosen(s[i][j], off);
-                if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // few scores' terms at a time
-              }
-            hide(see, s);   // tanh(-inf) is finite
+              for (int j = 0; j < AR; ++j) s[i][j] -= off;
           }
         } else {
           follow(mx, slack, sc, m, sum, o);
