@@ -398,7 +398,8 @@ typedef struct misa_kv_cache {
  * tokens of a call may have the same (sequence, index) or share a page's row
  * (the row would hold parts of both). Rows of other tokens keep their values.
  * The pooled keys of an indexer cache follow with misa_pool_update.
- * Errors: MISA_ERR_ARG (sizes, null pointers), MISA_ERR_ALIGN.
+ * Errors: MISA_ERR_ARG (sizes, null pointers; 2^24 workgroups and more, which no
+ * N below 2^24 needs), MISA_ERR_ALIGN.
  */
 MISA_API int32_t misa_cache_append(const misa_kv_cache* cache, const void* k, int64_t k_ts, int64_t k_hs, const void* v,
                                    int64_t v_ts, int64_t v_hs, const void* q, int64_t q_ts, int64_t q_hs, void* q_out,

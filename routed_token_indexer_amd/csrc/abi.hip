@@ -1087,6 +1087,8 @@ int32_t misa_cache_append(const misa_kv_cache* cache, const void* k, int64_t k_t
   a.rot = rot;
   a.interleaved = interleaved != 0;
   a.half = cache->dtype == MISA_FP16;
+  // a launch holds fewer than 2^32 threads
+  if (misa::append_blocks(a) >= (int64_t(1) << 24)) return fail(MISA_ERR_ARG, "%s: N = %lld: grid too large", fn, (long long)N);
   return hip_status(misa::launch_append(a, (hipStream_t)stream), fn);
 }
 

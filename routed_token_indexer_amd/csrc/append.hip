@@ -126,13 +126,25 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int unit
 
 }  // namespace
 
-hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
-  const int units = a.d / 16;
+// Threads of a workgroup: `units` pieces times `lanes` heads times tokens.
+static void split_of(const AppendArgs& a, int& units, int& lanes, int& per_block) {
+  units = a.d / 16;
   const int heads = a.Hq + a.Hkv + (a.v ? a.Hkv : 0);
-  int lanes = 1;
+  lanes = 1;
   while (2 * lanes * units <= kThreads && lanes < heads) lanes *= 2;
-  const int per_block = kThreads / (units * lanes);
-  const dim3 grid((unsigned)((a.N + per_block - 1) / per_block));
+  per_block = kThreads / (units * lanes);
+}
+
+int64_t append_blocks(const AppendArgs& a) {
+  int units, lanes, per_block;
+  split_of(a, units, lanes, per_block);
+  return (a.N + per_block - 1) / per_block;
+}
+
+hipError_t launch_append(const AppendArgs& a, hipStream_t st) {
+  int units, lanes, per_block;
+  split_of(a, units, lanes, per_block);
+  const dim3 grid((unsigned)append_blocks(a));
 #define MISA_APPEND(HALF_, INTER_) \
   hipLaunchKernelGGL((append_kernel<HALF_, INTER_>), grid, dim3(kThreads), 0, st, a, units, lanes, per_block)
   if (a.half) {

@@ -72,6 +72,7 @@ struct AppendArgs {
   bool interleaved;
   bool half;                // fp16 (else bf16)
 };
+int64_t append_blocks(const AppendArgs& a);   // workgroups (of 256 threads) of its launch
 hipError_t launch_append(const AppendArgs& a, hipStream_t st);
 
 }  // namespace misa
