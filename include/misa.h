@@ -425,8 +425,10 @@ MISA_API int32_t misa_cache_append(const misa_kv_cache* cache, const void* k, in
  *            (multiples of 8); Hq a multiple of the cache's heads
  *   q_seq, q_len  int32 [T];  q_start  int32 [T] or NULL (0)
  *   q_pos    int32 [T] or NULL (q_len - 1), not negative; read with slopes only
- *   scale    in [1e-30, 1e30];  cap  0 (none) or in [1e-6, 1e30];  slopes  fp32 [Hq] or NULL
+ *   scale    in [1e-30, 1e4];  cap  0 (none) or in [1e-6, 1e30];  slopes  fp32 [Hq] or NULL
  *   out      [T][Hq][d] of the cache's type, apart from q;  lse  fp32 [T][Hq] or NULL
+ * Scores are fp32: the largest x_s of a row is taken to be at most 5e7 in size
+ * (where neighbouring values are 4 apart); beyond that its weights may overflow.
  * A query that sees nothing (empty interval, sequence out of range) gets zeros
  * and lse = -inf. q_len is clamped to what a sequence can address, q_start to
  * [0, q_len]. What a query does not see may hold anything, NaN included; a NaN

@@ -322,7 +322,7 @@ int32_t check_attend(const char* fn, const misa_kv_cache* c, const void* q, int6
   if (!c->v) return fail(MISA_ERR_ARG, "%s: null value cache", fn);
   if (T < 0 || T >= (int64_t(1) << 31)) return fail(MISA_ERR_ARG, "%s: T = %lld out of range", fn, (long long)T);
   if (Hq < 1 || Hq % c->heads || Hq > 65536) return fail(MISA_ERR_ARG, "%s: Hq = %d not a multiple of heads = %d", fn, Hq, c->heads);
-  if (!(scale >= 1e-30f) || scale > 1e30f) return fail(MISA_ERR_ARG, "%s: scale = %g not in [1e-30, 1e30]", fn, scale);
+  if (!(scale >= 1e-30f) || scale > 1e4f) return fail(MISA_ERR_ARG, "%s: scale = %g not in [1e-30, 1e4]", fn, scale);
   if (!(cap == 0.f || (cap >= 1e-6f && cap <= 1e30f)))
     return fail(MISA_ERR_ARG, "%s: cap = %g neither 0 nor in [1e-6, 1e30]", fn, cap);
   if (T > 0 && (!q || !q_seq || !q_len || !out)) return fail(MISA_ERR_ARG, "%s: null pointer", fn);

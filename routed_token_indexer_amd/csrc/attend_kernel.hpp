@@ -756,11 +756,14 @@ struct Kernel {
   // to 2^-21 of the row's largest and zero below 2^-32 of it, not 2^-14 and 2^-25:
   // thousands of keys that small, beside one whose value is near zero, make the
   // result. The largest stays below 2^15: `follow` lets it pass 2^m by 2^8, and the
-  // rounding up by 2^-22 covers those of the products that it is compared by.
+  // reference is rounded up by at least what m sc lost to rounding, which would
+  // otherwise be a factor of all the row's weights (2^4 at the largest documented
+  // scores, exponents of 2^26; rounded up it takes at most 2^12 from them there). The
+  // range of bf16 holds that factor.
   static constexpr float kLift = HALF ? 7.f : 0.f;
   __device__ static __forceinline__ float reference(float m, float sc) {
     const float r = m * sc;
-    return HALF && m != -__builtin_inff() ? __builtin_fmaf(fabsf(r), 0x1p-22f, r) - kLift : r;
+    return HALF && m != -__builtin_inff() ? __builtin_fmaf(fabsf(r), 0x1p-23f, r) - kLift : r;
   }
   __device__ static __forceinline__ float finite_reference(float m, float sc) {
     return m == -__builtin_inff() ? 0.f : reference(m, sc);
@@ -769,7 +772,7 @@ struct Kernel {
   // Moves the reference m where a row's maximum mx (of this lane's row, over all of
   // its keys of the step) passes it by more than slack.
   __device__ static __forceinline__ void follow(float mx, float slack, float sc, float& m, float& sum, Acc (&o)[OT]) {
-    if (!__any(mx > m + slack)) return;
+    if (!__any(mx - m > slack)) return;   // exact, however large they are
     const float mn = fmaxf(m, mx);
     const float alpha = __builtin_amdgcn_exp2f((m - (mn == -__builtin_inff() ? 0.f : mn)) * sc);
     sum *= alpha;
