@@ -358,6 +358,10 @@ MISA_API int32_t misa_pivot_indexer(const void* q, const float* w, const void* k
  *    less than 2^31 - 65536.
  *  - A table entry outside [0, npages) is no page: nothing is written there, and
  *    its tokens are not visible.
+ *  - The table's rows follow each other (table_cols entries each).
+ *  - Keys, and values, reach over less than 4 GiB, or over at most 2^32 - 2^16 times
+ *    the largest power of two that divides page_stride and token_stride (2^35
+ *    elements for odd multiples of 8, 2^39 for multiples of 128).
  */
 #define MISA_BF16 1
 #define MISA_FP16 2
@@ -466,7 +470,7 @@ MISA_API int32_t misa_attend_selected(const misa_kv_cache* cache, const void* q,
  *   pre_len    int32 [npre]
  *   pre_table  int32 [npre][pre_cols] pages of the prefixes in the same cache, or
  *              NULL: prefix i is page i
- *   q_pos      int32 [T] or NULL (pre_len + q_len - 1); read with slopes only
+ *   q_pos      int32 [T] or NULL (pre_len + q_len - 1, below 2^31); read with slopes only
  *   the rest as misa_attend (q_seq, q_len: the own part)
  *   ws: misa_attend_workspace_bytes(MISA_OP_ATTEND_SHARED, T, Hq, heads, d, nseq, npre)
  */
