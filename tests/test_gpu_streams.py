@@ -109,3 +109,25 @@ def test_an_indexer_on_a_stream_of_its_own(big):
     assert all(home(x) == side.cuda_stream for x in got)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, (*want, rows, kbar)))
+
+
+@pytest.mark.parametrize("name", ["append", "attend", "selected", "shared"])
+def test_captured_on_a_stream_of_its_own(name, big):
+    """A call given the capturing stream makes its outputs and workspace in the graph's memory: replays with work
+    between them repeat the eager result."""
+    f = attention(name)
+    want = f()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = f(stream=side)
+    for _ in range(4):
+        for x in got:
+            x.fill_(7)
+        junk = torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda")
+        graph.replay()
+        torch.mm(*big, out=big[1])
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        del junk
