@@ -22,6 +22,10 @@
  *   7. attention over the selected tokens                      (misa_attend_selected)
  *   8. attention over the whole cache, also behind a prefix
  *      that the batch shares             (misa_attend, misa_attend_shared)
+ *   9. how much weight attention gave each cached token        (misa_attend_mass)
+ *  10. eviction: the tokens of most weight become the first
+ *      rows of the cache              (misa_cache_evict, misa_cache_move)
+ *  11. the next tokens from a step's logits                    (misa_sample)
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -489,6 +493,119 @@ MISA_API int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, i
 /* Workspace bytes of one attention call (0: none needed, or sizes out of range). */
 MISA_API size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, int32_t heads, int32_t d, int64_t nseq,
                                             int64_t npre);
+
+/*
+ * Accumulated attention weight, the measure that misa_cache_evict keeps tokens by:
+ * how much weight the T queries of an attention call gave each cached token. With
+ * x_s as in misa_attend (same scale, cap, slopes and intervals) and lse the log-sums
+ * that the attention call returned,
+ *     out[n][g][s] = in[n][g][s] + sum over the queries t of sequence n that see s, and
+ *                    the heads j of kv head g, of  exp(x_s - lse[t][j])
+ * for every token s that a sequence can address (L = table_cols * page, or page without
+ * a table). Keys are read once, values not at all (cache->v may be NULL).
+ *   lse     fp32 [T][Hq]; a row of -inf (a query that sees nothing) gives nothing
+ *   lists   cache->heads: a sum per kv head; 1: one sum over all heads
+ *   in      fp32 [nseq][lists][L] or NULL (zeros);  out  the same shape, every element
+ *           written; may be in itself
+ * The queries of a call may stand in any order; those of a sequence next to each other
+ * are fastest. The last queries of a prompt, all of them, or a decode step's make such a
+ * sum alike. It is the same from run to run: nothing depends on the order of workgroups.
+ * What a query does not see may hold anything; tokens without a page get nothing.
+ *   ws: misa_cache_workspace_bytes(MISA_OP_ATTEND_MASS, cache, T, Hq, lists, 0)
+ * Errors: as misa_attend (d in {64, 128, 256}); MISA_ERR_ARG for lists neither 1 nor
+ * cache->heads, T * Hq / heads of 2^31 and more, or nseq * heads * L too large for one launch.
+ */
+MISA_API int32_t misa_attend_mass(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs,
+                                  const float* lse, const int32_t* q_seq, const int32_t* q_start,
+                                  const int32_t* q_len, const int32_t* q_pos, int64_t T, int32_t Hq, float scale,
+                                  float cap, const float* slopes, int32_t lists, const float* in, float* out, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * Evicts tokens from the cache, in place. Of each sequence's lens[n] tokens at most
+ * `budget` stay and become its first rows. The rank of a token:
+ *   1. protected ones: pos < sinks, or among the `recent` latest positions
+ *      (pos > newest - recent, newest the largest position of the list);
+ *   2. then by mass, larger first (NaN above all numbers, -0 equal to 0);
+ *   3. ties to the lower row.
+ * With lists = cache->heads each kv head keeps its own tokens, with lists = 1 all heads
+ * the same. new_len = min(lens, budget). A kept row below new_len stays where it is; the
+ * rows of dropped tokens below new_len take, both in ascending order, the kept rows from
+ * behind. So the kept rows are in no order of position afterwards (attention over
+ * [0, new_len) needs none; `pos` says which is which), few rows move, and no row that is
+ * read is written. Rows from new_len on keep their contents in the cache.
+ *   mass     fp32 [nseq][lists][L]; L = table_cols * page, or page without a table
+ *   pos      int32 [nseq][lists][L] positions, or NULL: a row's number is its position
+ *   lens     int32 [nseq], clamped to [0, L]
+ *   mass_out, pos_out  the same shapes, or NULL; may be mass and pos themselves. Rows
+ *            follow their tokens; behind new_len: 0 and -1.
+ *   src      int32 [nseq][lists][budget] out: the row that each of the first rows came
+ *            from, -1 from new_len on
+ *   new_len  int32 [nseq] out
+ * No two rows that a sequence addresses below lens[n] may be one place of memory, and no
+ * two sequences may share such rows (a prefix they share is to be kept apart, as
+ * misa_attend_shared does). A row whose page, or whose source's page, does not exist is
+ * not moved. d: any multiple of 8 up to 1024; cache->v may be NULL.
+ *   ws: misa_cache_workspace_bytes(MISA_OP_CACHE_EVICT, cache, 0, 0, lists, budget)
+ * Errors: MISA_ERR_ARG (budget < 1, sinks or recent negative or together more than
+ * budget, lists neither 1 nor cache->heads, sizes), MISA_ERR_ALIGN, MISA_ERR_WORKSPACE.
+ */
+MISA_API int32_t misa_cache_evict(const misa_kv_cache* cache, const float* mass, const int32_t* pos,
+                                  const int32_t* lens, int32_t lists, int64_t budget, int64_t sinks, int64_t recent,
+                                  float* mass_out, int32_t* pos_out, int32_t* src, int32_t* new_len, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/*
+ * The same moves in another cache of the same sequences (the indexer's keys, another
+ * layer's cache): row i of a list takes row src[n][list][i], for i < n_src. Entries
+ * outside [0, L), and those equal to i, move nothing; rows without a page neither. A row
+ * that is a source must not be moved onto by the same call (src of misa_cache_evict never
+ * does that). Pooled keys of an indexer cache whose rows moved are to be pooled again.
+ *   src  int32 [nseq][lists][n_src];  lists  1 (all heads) or cache->heads
+ * Errors: MISA_ERR_ARG, MISA_ERR_ALIGN.
+ */
+MISA_API int32_t misa_cache_move(const misa_kv_cache* cache, const int32_t* src, int32_t lists, int64_t n_src,
+                                 void* stream);
+
+/* op codes of misa_cache_workspace_bytes */
+#define MISA_OP_ATTEND_MASS 13
+#define MISA_OP_CACHE_EVICT 14
+
+/* Workspace bytes of one call (0: none needed, or sizes out of range); the cache's pointers are not used. */
+MISA_API size_t misa_cache_workspace_bytes(int32_t op, const misa_kv_cache* cache, int64_t T, int32_t Hq,
+                                           int32_t lists, int64_t budget);
+
+/* ------------------------------------------------------------------------
+ * The next token of each of T rows of logits, from given random numbers.
+ * With temperature t > 0, w_i = exp((l_i - max l) / t); then, in this order,
+ *   top_k   keeps the top_k largest logits (ties to the lower id); 0 or less, or V and
+ *           more: all
+ *   min_p   keeps those with w_i >= min_p (1 at most); 0 or less, or NaN: all
+ *   top_p   keeps the shortest prefix, in descending order (ties to the lower id), whose
+ *           weights sum to at least top_p of what the first two left, one token at
+ *           least; 1 and more, or NaN: all
+ * and the token is the first one, in ascending order of ids, whose running sum over the
+ * kept ones exceeds u times their sum. t of 0 or less, or NaN: the first of the largest
+ * logits. Logits of -inf and NaN are never drawn; those of +inf share all weight. A row
+ * with nothing to draw gets token -1 and logprob -inf.
+ *   logits   [T][V] of dtype MISA_BF16, MISA_FP16 or MISA_FP32, rows row_stride elements apart
+ *   temperature, top_p, min_p  fp32 [T], top_k  int32 [T]: each may be NULL (1, 1, 0, 0)
+ *   u        fp32 [T], in [0, 1) (clamped to it; NaN counts as 0)
+ *   token    int32 [T] out;  logprob  fp32 [T] out, may be NULL: the logarithm of the
+ *            token's share of the kept weights (0 where t picks the largest)
+ * Weights are multiples of 2^-42 of the row's largest one (worked out in fp64; below
+ * 2^-43 they are 0), and their sums exact, so the result depends on no order.
+ * 1 <= V <= 2^20.
+ *   ws: misa_sample_workspace_bytes(T, V)
+ * Errors: MISA_ERR_ARG, MISA_ERR_ALIGN, MISA_ERR_WORKSPACE.
+ */
+#define MISA_FP32 3
+MISA_API int32_t misa_sample(const void* logits, int32_t dtype, int64_t row_stride, int64_t T, int32_t V,
+                             const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                             const float* u, int32_t* token, float* logprob, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of one misa_sample call (0: none needed, or sizes out of range). */
+MISA_API size_t misa_sample_workspace_bytes(int64_t T, int32_t V);
 
 /*
  * Full score rows of the routed scoring step (a diagnostic of step 3 above):

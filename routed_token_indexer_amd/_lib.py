@@ -33,9 +33,12 @@ OP_PIVOT_INDEXER = 9
 OP_ATTEND = 10
 OP_ATTEND_SELECTED = 11
 OP_ATTEND_SHARED = 12
+OP_ATTEND_MASS = 13
+OP_CACHE_EVICT = 14
 
 BF16 = 1
 FP16 = 2
+FP32 = 3
 
 KERNEL_SCORE = 1
 KERNEL_TOPK = 2
@@ -94,6 +97,13 @@ _SIGNATURES = {
                                     _SZ, _P]),
     "misa_attend_shared": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _F32, _F32, _P,
                                   _P, _P, _P, _SZ, _P]),
+    "misa_attend_mass": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _P, _P, _I64, _I32, _F32, _F32, _P, _I32, _P, _P, _P, _SZ,
+                                _P]),
+    "misa_cache_evict": (_I32, [_P, _P, _P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "misa_cache_move": (_I32, [_P, _P, _I32, _I64, _P]),
+    "misa_cache_workspace_bytes": (_SZ, [_I32, _P, _I64, _I32, _I32, _I64]),
+    "misa_sample": (_I32, [_P, _I32, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "misa_sample_workspace_bytes": (_SZ, [_I64, _I32]),
     "misa_timing_begin": (_I32, [_I32, _I32, _P]),
     "misa_timing_end": (_I32, [_P, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int32)]),
 }
@@ -543,10 +553,14 @@ def _attend_common(q, k_cache, v_cache, table, q_seq, q_len, q_pos, scale, slope
 
 
 def _attend_ws(ws, op, T, Hq, c, dev, stream, npre=0):
-    need = attend_workspace_bytes(op, T, Hq, c.heads, c.d, c.nseq, npre)
+    return _scratch(ws, attend_workspace_bytes(op, T, Hq, c.heads, c.d, c.nseq, npre), dev, stream)
+
+
+def _scratch(ws, need, dev, stream):
+    """The given workspace if it is large enough, or one from the stream's memory."""
     if ws is not None:
         if ws.device != dev:
-            raise ValueError(f"ws: on {ws.device}, the cache on {dev}")
+            raise ValueError(f"ws: on {ws.device}, the call on {dev}")
         if ws.dtype is not torch.uint8 or not ws.is_contiguous():
             raise TypeError("ws: expected a contiguous torch.uint8 tensor")
         if ws.numel() >= need:
@@ -605,6 +619,165 @@ def attend_shared(q, k_cache, v_cache, q_seq, q_len, pre, pre_len, table=None, p
           None if pre_table is None else _vec(pre_table, "pre_table", torch.int32, (npre, cols), dev), cols, npre, T, Hq,
           scale, cap, p[3], p[4], p[5], ws.data_ptr(), ws.numel(), _on(dev, stream))
     return out, lse
+
+
+def cache_workspace_bytes(op: int, k_cache, table=None, T: int = 0, Hq: int = 0, lists: int = 1, budget: int = 0) -> int:
+    """Workspace bytes of ``attend_mass`` (OP_ATTEND_MASS: T, Hq, lists) or ``cache_evict`` (OP_CACHE_EVICT: lists, budget)."""
+    return int(lib().misa_cache_workspace_bytes(op, ctypes.byref(_kv_cache(k_cache, None, table)), T, Hq, lists, budget))
+
+
+def _cache_ws(ws, op, c, T, Hq, lists, budget, dev, stream):
+    return _scratch(ws, int(lib().misa_cache_workspace_bytes(op, ctypes.byref(c), T, Hq, lists, budget)), dev, stream)
+
+
+def _addressed(c) -> int:
+    """Tokens that a sequence of the cache can address."""
+    return c.table_cols * c.page if c.table else c.page
+
+
+def _lists(x, name: str, dtype, c, G, dev):
+    """[nseq, lists, tokens] tensor, lists 1 or the cache's heads (G: as another tensor has); its pointer and lists."""
+    if x is None:
+        return None, G
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dim() != 3 or (x.shape[1] not in (1, c.heads) if G is None else x.shape[1] != G):
+        raise ValueError(f"{name}: got shape {tuple(x.shape)}, expected [{c.nseq}, {f'1 or {c.heads}' if G is None else G}, "
+                         f"{_addressed(c)}]")
+    return _vec(x, name, dtype, (c.nseq, x.shape[1], _addressed(c)), dev), x.shape[1]
+
+
+def attend_mass(q, k_cache, lse, q_seq, q_len, table=None, q_start=None, q_pos=None, scale=None, cap=0.0, slopes=None,
+                mass=None, out=None, per_head=True, ws=None, stream=None):
+    """Attention weight that each cached token got, summed over queries and heads.
+
+    Arguments as in ``attend``, whose log-sums ``lse`` [T, Hq] it needs; no values.
+    Returns ``out`` [nseq, heads, tokens] fp32 (tokens: as many as a sequence can
+    address), or [nseq, 1, tokens] for one sum over all heads, which is what the
+    shape of ``mass`` or ``out`` says, or else ``per_head``. ``mass`` is what earlier
+    calls gave (None: zeros); ``out`` may be ``mass`` itself.
+    """
+    c = _kv_cache(k_cache, None, table)
+    dev = k_cache.device
+    q_ts, q_hs = _rows(q, "q", k_cache)
+    T, Hq, d = q.shape
+    in_ptr, G = _lists(mass, "mass", torch.float32, c, None, dev)
+    out_ptr, G = _lists(out, "out", torch.float32, c, G, dev)
+    if G is None:
+        G = c.heads if per_head else 1
+    if out is None:
+        out = _empty((c.nseq, G, _addressed(c)), torch.float32, dev, stream)
+        out_ptr = out.data_ptr()
+    ptrs = (_vec(lse, "lse", torch.float32, (T, Hq), dev), _vec(q_seq, "q_seq", torch.int32, (T,), dev),
+            _vec(q_start, "q_start", torch.int32, (T,), dev), _vec(q_len, "q_len", torch.int32, (T,), dev),
+            _vec(q_pos, "q_pos", torch.int32, (T,), dev))
+    slopes_ptr = _vec(slopes, "slopes", torch.float32, (Hq,), dev)
+    ws = _cache_ws(ws, OP_ATTEND_MASS, c, T, Hq, G, 0, dev, stream)
+    _call(dev, "misa_attend_mass", ctypes.byref(c), q.data_ptr(), q_ts, q_hs, *ptrs, T, Hq,
+          float(d ** -0.5 if scale is None else scale), cap, slopes_ptr, G, in_ptr, out_ptr, ws.data_ptr(), ws.numel(),
+          _on(dev, stream))
+    return out
+
+
+def cache_evict(k_cache, v_cache, mass, lens, budget: int, sinks: int = 0, recent: int = 0, pos=None, table=None,
+                mass_out=None, pos_out=None, src=None, new_len=None, ws=None, stream=None):
+    """Keeps at most ``budget`` tokens of each sequence and makes them its first rows, in place.
+
+    ``mass`` [nseq, heads, tokens] fp32 (each kv head keeps its own tokens) or
+    [nseq, 1, tokens] (all heads the same), ``lens`` [nseq] int32 tokens there are,
+    ``pos`` [nseq, lists, tokens] int32 their positions (None: the row numbers). The
+    first ``sinks`` positions and the ``recent`` latest ones stay, then the tokens of
+    most mass, ties to the lower row. Rows of dropped tokens take the kept rows from
+    behind, so rows are in no order afterwards. Returns ``new_len`` [nseq], ``src``
+    [nseq, lists, budget] (the row each row came from, -1 behind the last),
+    ``mass_out`` and ``pos_out``, where rows have moved along (0 and -1 behind the
+    kept ones; they may be ``mass`` and ``pos``). ``v_cache`` may be None.
+    """
+    c = _kv_cache(k_cache, v_cache, table)
+    dev = k_cache.device
+    if mass is None:
+        raise TypeError("mass: expected a torch.Tensor")
+    mass_ptr, G = _lists(mass, "mass", torch.float32, c, None, dev)
+    pos_ptr, _ = _lists(pos, "pos", torch.int32, c, G, dev)
+    if mass_out is None:
+        mass_out = _empty(mass.shape, torch.float32, dev, stream)
+    if pos_out is None:
+        pos_out = _empty(mass.shape, torch.int32, dev, stream)
+    if budget < 1:
+        raise ValueError(f"budget: {budget} < 1")
+    if src is None:
+        src = _empty((c.nseq, G, budget), torch.int32, dev, stream)
+    if new_len is None:
+        new_len = _empty((c.nseq,), torch.int32, dev, stream)
+    ws = _cache_ws(ws, OP_CACHE_EVICT, c, 0, 0, G, budget, dev, stream)
+    _call(dev, "misa_cache_evict", ctypes.byref(c), mass_ptr, pos_ptr, _vec(lens, "lens", torch.int32, (c.nseq,), dev), G,
+          budget, sinks, recent, _lists(mass_out, "mass_out", torch.float32, c, G, dev)[0],
+          _lists(pos_out, "pos_out", torch.int32, c, G, dev)[0],
+          _vec(src, "src", torch.int32, (c.nseq, G, budget), dev), _vec(new_len, "new_len", torch.int32, (c.nseq,), dev),
+          ws.data_ptr(), ws.numel(), _on(dev, stream))
+    return new_len, src, mass_out, pos_out
+
+
+def cache_move(k_cache, v_cache, src, table=None, stream=None):
+    """The moves ``src`` [nseq, lists, n] of a ``cache_evict`` in another cache of the same
+    sequences, in place: row i takes row src[i] (lists: 1 for all heads, or the cache's
+    heads). Entries outside the sequence move nothing."""
+    c = _kv_cache(k_cache, v_cache, table)
+    dev = k_cache.device
+    if not isinstance(src, torch.Tensor):
+        raise TypeError("src: expected a torch.Tensor")
+    if src.dim() != 3 or src.shape[0] != c.nseq or src.shape[1] not in (1, c.heads):
+        raise ValueError(f"src: got shape {tuple(src.shape)}, expected [{c.nseq}, 1 or {c.heads}, rows]")
+    _call(dev, "misa_cache_move", ctypes.byref(c), _vec(src, "src", torch.int32, src.shape, dev), src.shape[1],
+          src.shape[2], _on(dev, stream))
+
+
+_LOGIT_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32}
+
+
+def sample_workspace_bytes(T: int, V: int) -> int:
+    return int(lib().misa_sample_workspace_bytes(T, V))
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, token=None, logprob=None, want_logprob=False,
+           ws=None, stream=None):
+    """Next tokens of logits [T, V] (bf16, fp16 or fp32; rows may be strided) from random
+    numbers ``u`` [T] in [0, 1): token [T] int32 and its log-probability [T] (None unless wanted).
+
+    Per row, each [T] or None: ``temperature`` (not above 0: the first largest logit),
+    then ``top_k`` (not above 0: all), ``min_p`` (of the largest probability), ``top_p``
+    (of what the others left). The token is the first one in ascending order whose
+    running sum exceeds u times the kept weights' sum; -1 for rows without a finite logit.
+    """
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a torch.Tensor")
+    dtype = _LOGIT_DTYPES.get(logits.dtype)
+    if dtype is None:
+        raise TypeError(f"logits: expected bfloat16, float16 or float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits: expected 2 dims, got shape {tuple(logits.shape)}")
+    if not logits.is_cuda:
+        raise ValueError("logits: must be a device tensor")
+    dev = logits.device
+    T, V = logits.shape
+    rs, es = logits.stride()
+    if es != 1 and V > 1:
+        raise ValueError("logits: rows must be contiguous")
+    f32 = torch.float32
+    ptrs = [_vec(x, name, dt, (T,), dev) for x, name, dt in
+            ((temperature, "temperature", f32), (top_k, "top_k", torch.int32), (top_p, "top_p", f32), (min_p, "min_p", f32))]
+    if u is None:
+        raise TypeError("u: expected a torch.Tensor")
+    u_ptr = _vec(u, "u", f32, (T,), dev)
+    if token is None:
+        token = _empty((T,), torch.int32, dev, stream)
+    if logprob is None and want_logprob:
+        logprob = _empty((T,), f32, dev, stream)
+    ws = _scratch(ws, sample_workspace_bytes(T, V), dev, stream)
+    _call(dev, "misa_sample", logits.data_ptr(), dtype, rs if T > 1 else V, T, V, *ptrs, u_ptr,
+          _vec(token, "token", torch.int32, (T,), dev), _vec(logprob, "logprob", f32, (T,), dev), ws.data_ptr(), ws.numel(),
+          _on(dev, stream))
+    return token, logprob
 
 
 def timing_begin(kernel: int, capacity: int = 4096, stream=None):

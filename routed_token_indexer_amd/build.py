@@ -15,7 +15,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libmisa.so")
 SOURCES = ["abi.hip", "pool.hip", "route.hip", "score.hip", "topk.hip", "topk_split.hip", "block.hip", "pivot.hip",
-           "append.hip", "attend.hip", "attend_d64.hip", "attend_d128.hip", "attend_d256.hip"]
+           "append.hip", "attend.hip", "attend_d64.hip", "attend_d128.hip", "attend_d256.hip", "mass.hip", "evict.hip",
+           "sample.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -10,6 +10,7 @@
 
 #include "misa.h"
 #include "misa_attend.hpp"
+#include "misa_evict.hpp"
 #include "misa_internal.hpp"
 
 namespace {
@@ -1201,6 +1202,198 @@ int32_t misa_attend_shared(const misa_kv_cache* cache, const void* q, int64_t q_
   if (e == hipSuccess) e = misa::launch_attend(a, Ra, half, st);
   if (e == hipSuccess) e = misa::launch_attend_join(b, Rb, &a, Ra, static_cast<uint16_t*>(out), lse, half, st);
   return hip_status(e, fn);
+}
+
+namespace {
+
+// lists of a sequence: one a kv head, or one for all heads
+int32_t check_lists(const char* fn, const misa_kv_cache* c, int32_t lists) {
+  if (lists != 1 && lists != c->heads)
+    return fail(MISA_ERR_ARG, "%s: lists = %d neither 1 nor heads = %d", fn, lists, c->heads);
+  return MISA_OK;
+}
+
+int32_t check_rows(const char* fn, const misa_kv_cache* c) {
+  if (c->d < 8 || c->d > 1024 || c->d % 8) return fail(MISA_ERR_ARG, "%s: d = %d not a multiple of 8 in [8, 1024]", fn, c->d);
+  return MISA_OK;
+}
+
+// Tokens that a sequence of the cache can address; 0 for sizes out of range.
+int64_t addressed(const misa_kv_cache* c) {
+  if (!c || c->page < 1 || c->page > kMaxTokens || c->nseq < 1 || c->nseq >= (int64_t(1) << 31) || c->heads < 1) return 0;
+  if (!c->table) return c->page;
+  return c->table_cols < 1 || c->table_cols > kMaxTokens / c->page ? 0 : c->table_cols * c->page;
+}
+
+// Workgroups of the accumulated weights' launch before it is split (each takes 128 keys).
+__int128 mass_tiles(const misa_kv_cache* c, int64_t L) { return (__int128)((L + 127) / 128) * c->nseq * c->heads; }
+
+}  // namespace
+
+size_t misa_cache_workspace_bytes(int32_t op, const misa_kv_cache* cache, int64_t T, int32_t Hq, int32_t lists,
+                                  int64_t budget) {
+  const int64_t L = addressed(cache);
+  if (L == 0 || lists < 1) return 0;
+  if (op == MISA_OP_ATTEND_MASS) {
+    if (T < 0 || T >= (int64_t(1) << 31) || Hq < cache->heads || Hq % cache->heads) return 0;
+    if (mass_tiles(cache, L) >= (1 << 24)) return 0;
+    const int splits = misa::mass_splits(T, cache->nseq, cache->heads, Hq / cache->heads, L, cache->d);
+    if (splits == 1 && lists == cache->heads) return 0;
+    return round_up((size_t)splits * (size_t)cache->nseq * cache->heads * (size_t)L * sizeof(float));
+  }
+  if (op == MISA_OP_CACHE_EVICT) {
+    if (budget < 1 || (__int128)cache->nseq * lists >= (1 << 22)) return 0;
+    return round_up((size_t)cache->nseq * lists * (size_t)(budget < L ? budget : L) * sizeof(int32_t));
+  }
+  return 0;
+}
+
+int32_t misa_attend_mass(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs, const float* lse,
+                         const int32_t* q_seq, const int32_t* q_start, const int32_t* q_len, const int32_t* q_pos,
+                         int64_t T, int32_t Hq, float scale, float cap, const float* slopes, int32_t lists,
+                         const float* in, float* out, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "misa_attend_mass";
+  misa::MassArgs a{};
+  int32_t rc = check_cache(fn, cache, &a.kv);
+  if (rc) return rc;
+  if (!(cache->d == 64 || cache->d == 128 || cache->d == 256))
+    return fail(MISA_ERR_ARG, "%s: d = %d not in {64, 128, 256}", fn, cache->d);
+  if (T < 0 || T >= (int64_t(1) << 31)) return fail(MISA_ERR_ARG, "%s: T = %lld out of range", fn, (long long)T);
+  if (Hq < 1 || Hq % cache->heads || Hq > 65536)
+    return fail(MISA_ERR_ARG, "%s: Hq = %d not a multiple of heads = %d", fn, Hq, cache->heads);
+  if (!(scale >= 1e-30f) || scale > 1e4f) return fail(MISA_ERR_ARG, "%s: scale = %g not in [1e-30, 1e4]", fn, scale);
+  if (!(cap == 0.f || (cap >= 1e-6f && cap <= 1e30f)))
+    return fail(MISA_ERR_ARG, "%s: cap = %g neither 0 nor in [1e-6, 1e30]", fn, cap);
+  if ((rc = check_lists(fn, cache, lists))) return rc;
+  if (!out || (T > 0 && (!q || !lse || !q_seq || !q_len))) return fail(MISA_ERR_ARG, "%s: null pointer", fn);
+  if (!stride_ok(q_ts) || !stride_ok(q_hs)) return fail(MISA_ERR_ALIGN, "%s: q strides must be positive multiples of 8", fn);
+  if (!aligned(q, 16)) return fail(MISA_ERR_ALIGN, "%s: q must be 16-byte aligned", fn);
+  if (!aligned(lse, 4) || !aligned(q_seq, 4) || !aligned(q_start, 4) || !aligned(q_len, 4) || !aligned(q_pos, 4) ||
+      !aligned(slopes, 4) || !aligned(in, 4) || !aligned(out, 4))
+    return fail(MISA_ERR_ALIGN, "%s: lse, q_seq, q_start, q_len, q_pos, slopes, in and out must be 4-byte aligned", fn);
+  a.group = Hq / cache->heads;
+  if (T * (int64_t)a.group >= (int64_t(1) << 31) - 64)
+    return fail(MISA_ERR_ARG, "%s: T * Hq / heads = %lld out of range", fn, (long long)(T * a.group));
+  if (mass_tiles(cache, a.kv.Lmax) >= (1 << 24)) return fail(MISA_ERR_ARG, "%s: grid too large", fn);
+  rc = check_ws(fn, ws, ws_bytes, misa_cache_workspace_bytes(MISA_OP_ATTEND_MASS, cache, T, Hq, lists, 0));
+  if (rc) return rc;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_ts = q_ts;
+  a.q_hs = q_hs;
+  a.lse = lse;
+  a.q_seq = q_seq;
+  a.q_start = q_start;
+  a.q_len = q_len;
+  a.q_pos = q_pos;
+  a.T = T;
+  a.d = cache->d;
+  a.Hq = Hq;
+  a.Hkv = cache->heads;
+  a.by_group = misa::fast_div((uint32_t)a.group);
+  a.scale = scale;
+  a.cap = cap;
+  a.slopes = slopes;
+  a.in = in;
+  a.out = out;
+  a.G = lists;
+  a.splits = misa::mass_splits(T, a.kv.nseq, a.Hkv, a.group, a.kv.Lmax, a.d);
+  a.part = a.splits > 1 || lists != cache->heads ? static_cast<float*>(ws) : nullptr;
+  if (misa::mass_blocks(a) >= (int64_t(1) << 24)) return fail(MISA_ERR_ARG, "%s: grid too large", fn);
+  return hip_status(misa::launch_mass(a, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);
+}
+
+int32_t misa_cache_evict(const misa_kv_cache* cache, const float* mass, const int32_t* pos, const int32_t* lens,
+                         int32_t lists, int64_t budget, int64_t sinks, int64_t recent, float* mass_out,
+                         int32_t* pos_out, int32_t* src, int32_t* new_len, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "misa_cache_evict";
+  misa::EvictArgs a{};
+  int32_t rc = check_cache(fn, cache, &a.kv);
+  if (rc || (rc = check_rows(fn, cache)) || (rc = check_lists(fn, cache, lists))) return rc;
+  if (budget < 1 || budget > kMaxTokens) return fail(MISA_ERR_ARG, "%s: budget = %lld out of range", fn, (long long)budget);
+  if (sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
+    return fail(MISA_ERR_ARG, "%s: sinks = %lld and recent = %lld must be at least 0 and at most budget = %lld together", fn,
+                (long long)sinks, (long long)recent, (long long)budget);
+  if (!mass || !lens || !src || !new_len) return fail(MISA_ERR_ARG, "%s: null pointer", fn);
+  if (!aligned(mass, 4) || !aligned(pos, 4) || !aligned(lens, 4) || !aligned(mass_out, 4) || !aligned(pos_out, 4) ||
+      !aligned(src, 4) || !aligned(new_len, 4))
+    return fail(MISA_ERR_ALIGN, "%s: mass, pos, lens, mass_out, pos_out, src and new_len must be 4-byte aligned", fn);
+  misa::MoveArgs b{};
+  b.kv = a.kv;
+  b.Hkv = a.Hkv = cache->heads;
+  b.d = a.d = cache->d;
+  b.G = a.G = lists;
+  b.src = a.src = src;
+  b.n = a.budget = budget;
+  // 1024 threads a list, and a launch holds fewer than 2^32
+  if ((__int128)a.kv.nseq * lists >= (1 << 22) || misa::move_blocks(b) >= (int64_t(1) << 24))
+    return fail(MISA_ERR_ARG, "%s: grid too large", fn);
+  rc = check_ws(fn, ws, ws_bytes, misa_cache_workspace_bytes(MISA_OP_CACHE_EVICT, cache, 0, 0, lists, budget));
+  if (rc) return rc;
+  a.mass = mass;
+  a.pos = pos;
+  a.lens = lens;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.mass_out = mass_out;
+  a.pos_out = pos_out;
+  a.new_len = new_len;
+  a.movers = static_cast<int32_t*>(ws);
+  hipStream_t st = (hipStream_t)stream;
+  hipError_t e = misa::launch_evict_select(a, st);
+  if (e == hipSuccess) e = misa::launch_move(b, st);
+  return hip_status(e, fn);
+}
+
+int32_t misa_cache_move(const misa_kv_cache* cache, const int32_t* src, int32_t lists, int64_t n_src, void* stream) {
+  const char* fn = "misa_cache_move";
+  misa::MoveArgs a{};
+  int32_t rc = check_cache(fn, cache, &a.kv);
+  if (rc || (rc = check_rows(fn, cache)) || (rc = check_lists(fn, cache, lists))) return rc;
+  if (n_src < 0 || n_src > kMaxTokens) return fail(MISA_ERR_ARG, "%s: n_src = %lld out of range", fn, (long long)n_src);
+  if (n_src == 0) return ok();
+  if (!src) return fail(MISA_ERR_ARG, "%s: null src", fn);
+  if (!aligned(src, 4)) return fail(MISA_ERR_ALIGN, "%s: src must be 4-byte aligned", fn);
+  a.Hkv = cache->heads;
+  a.d = cache->d;
+  a.src = src;
+  a.G = lists;
+  a.n = n_src;
+  if ((__int128)a.kv.nseq * lists >= (1 << 24) || misa::move_blocks(a) >= (int64_t(1) << 24))
+    return fail(MISA_ERR_ARG, "%s: grid too large", fn);
+  return hip_status(misa::launch_move(a, (hipStream_t)stream), fn);
+}
+
+size_t misa_sample_workspace_bytes(int64_t T, int32_t V) { return 0; }
+
+int32_t misa_sample(const void* logits, int32_t dtype, int64_t row_stride, int64_t T, int32_t V,
+                    const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                    const float* u, int32_t* token, float* logprob, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "misa_sample";
+  if (dtype != MISA_BF16 && dtype != MISA_FP16 && dtype != MISA_FP32) return fail(MISA_ERR_ARG, "%s: dtype = %d", fn, dtype);
+  if (T < 0 || T >= (int64_t(1) << 22)) return fail(MISA_ERR_ARG, "%s: T = %lld out of range", fn, (long long)T);
+  if (V < 1 || V > misa::kMaxVocab) return fail(MISA_ERR_ARG, "%s: V = %d not in [1, 2^20]", fn, V);
+  if (row_stride < 0 || row_stride >= (int64_t(1) << 38)) return fail(MISA_ERR_ARG, "%s: row_stride = %lld out of range", fn, (long long)row_stride);
+  if (T == 0) return ok();
+  if (!logits || !u || !token) return fail(MISA_ERR_ARG, "%s: null logits, u or token", fn);
+  if (!aligned(logits, dtype == MISA_FP32 ? 4 : 2)) return fail(MISA_ERR_ALIGN, "%s: logits must be aligned to their type", fn);
+  if (!aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) || !aligned(u, 4) ||
+      !aligned(token, 4) || !aligned(logprob, 4))
+    return fail(MISA_ERR_ALIGN, "%s: temperature, top_k, top_p, min_p, u, token and logprob must be 4-byte aligned", fn);
+  const int32_t rc = check_ws(fn, ws, ws_bytes, misa_sample_workspace_bytes(T, V));
+  if (rc) return rc;
+  misa::SampleArgs a{};
+  a.logits = logits;
+  a.row_stride = row_stride;
+  a.T = T;
+  a.V = V;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.u = u;
+  a.token = token;
+  a.logprob = logprob;
+  return hip_status(misa::launch_sample(a, dtype, (hipStream_t)stream), fn);
 }
 
 int32_t misa_debug_scores(const void* q, const float* w, const void* k, const int32_t* heads, int32_t h,

@@ -1,0 +1,201 @@
+"""Sampling against the fp64 oracle: the same token, every filter, rows of every length, equal
+logits, masked rows, odd numbers."""
+import math
+
+import pytest
+import torch
+
+import evict_oracle as O
+from routed_token_indexer_amd import _lib as M
+
+pytestmark = pytest.mark.gpu
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+def both(logits, u, t=None, k=None, p=None, m=None, strict=True):
+    """logits on the device; settings are lists or None. ``strict``: no comparison is too near to tell."""
+    T, V = logits.shape
+    dev = lambda x, dt=torch.float32: None if x is None else torch.tensor(x, dtype=dt, device="cuda")   # noqa: E731
+    token, logprob = M.sample(logits, dev(u), dev(t), dev(k, torch.int32), dev(p), dev(m), want_logprob=True)
+    torch.cuda.synchronize()
+    f = lambda x: torch.tensor(x, dtype=torch.float32).item()   # noqa: E731
+    for i in range(T):
+        one = dict(t=1.0 if t is None else f(t[i]), k=0 if k is None else k[i], p=1.0 if p is None or p[i] != p[i] else f(p[i]),
+                   m=0.0 if m is None or m[i] != m[i] else f(m[i]))
+        may, logs = O.sample_row(logits[i], f(u[i]), **one)
+        got = int(token[i])
+        assert got in may, (i, got, may, one, u[i])
+        assert not strict or len(may) == 1, (i, may)
+        want = logs[got]
+        # rounded to fp32 once; the sum of weights is off by V 2^-43 of it, the exponent by a few 2^-53 of itself
+        tol = 2.0 ** -24 * abs(want) + V * 2.0 ** -42 + 2.0 ** -40 + 2.0 ** -149
+        assert float(logprob[i]) == want or abs(float(logprob[i]) - want) <= tol, (i, float(logprob[i]), want)
+    return token
+
+
+def rows(T, V, dtype, seed, scale=2.0, pad=0):
+    g = torch.Generator().manual_seed(seed)
+    x = scale * torch.randn(T, V + pad, generator=g)
+    x[torch.arange(T), torch.randint(0, V, (T,), generator=g)] += 6.0
+    return x.to(TYPES[dtype]).cuda()[:, :V]
+
+
+def uniform(T, seed):
+    return torch.rand(T, generator=torch.Generator().manual_seed(seed)).tolist()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [1, 2, 7, 8, 9, 63, 64, 511, 512, 513, 1000, 4097, 32000, 100003])
+def test_lengths_and_filters(V, dtype):
+    T = 8
+    u = uniform(T, V)
+    x = rows(T, V, dtype, V)
+    t = [1.0, 0.7, 1.5, 0.3, 2.0, 1.0, 0.9, 1.1]
+    k = [0, 5, 1, V, 50, 3, -1, 40]
+    p = [1.0, 0.9, 0.5, 0.99, 0.8, 0.1, 0.95, 0.6]
+    m = [0.0, 0.01, 0.0, 0.05, 0.2, 0.0, 1e-4, 0.02]
+    both(x, u)
+    both(x, u, t=t)
+    both(x, u, t=t, k=k)
+    both(x, u, t=t, p=p)
+    both(x, u, t=t, m=m)
+    both(x, u, t=t, k=k, p=p, m=m)
+
+
+@pytest.mark.parametrize("dtype,pad", [("bf16", 1), ("bf16", 8), ("fp16", 3), ("fp32", 1), ("fp32", 5)])
+def test_rows_that_are_strided(dtype, pad):
+    x = rows(9, 777, dtype, 3, pad=pad)
+    both(x, uniform(9, 1), p=[0.9] * 9, k=[100] * 9)
+    both(x[:, 1:], uniform(9, 2), p=[0.9] * 9)
+    both(x[2:3, 5:], uniform(1, 3))
+    one = x[:1].expand(6, -1)                       # the same row six times
+    both(one, [0.0, 0.2, 0.4, 0.6, 0.8, 0.99], p=[0.95] * 6)
+
+
+@pytest.mark.parametrize("V", [600, 5000, 20000, 70001])
+def test_equal_logits(V):
+    """Flat rows: every token weighs the same, sums are whole numbers, and cuts fall among ties."""
+    x = torch.full((6, V), 3.25, device="cuda")
+    u = [0.0, 0.25, 0.5, 0.75, 0.999, 0.123]
+    n = V // 3
+    got = both(x, u, k=[n] * 6)
+    assert got.tolist() == [min(n - 1, int(torch.tensor(v, dtype=torch.float32).double() * n)) for v in u]
+    both(x, u, p=[0.5, 0.25, 0.125, 0.75, 1.0, 0.0])
+    both(x, u, k=[n, 1, 2, V - 1, V, V + 5], p=[0.5, 0.5, 0.5, 0.25, 0.25, 0.25])
+    both(x, u, m=[1.0, 0.5, 2.0, 0.0, -1.0, 1.0])
+
+
+@pytest.mark.parametrize("V", [5000, 40000])
+def test_few_values_and_narrow_rows(V):
+    """Many tokens in a bin: heavy ties, and rows whose logits hardly differ against the temperature."""
+    g = torch.Generator().manual_seed(V)
+    few = (torch.randn(6, V, generator=g) * 2).round().cuda()
+    u = uniform(6, V)
+    p = [0.9, 0.5, 0.99, 0.3, 0.7, 0.999]
+    both(few, u, p=p)
+    both(few, u, k=[V // 2, 10, 1, 2000, V - 1, 100], p=p)
+    narrow = (torch.randn(6, V, generator=g) * 1e-3).cuda()
+    both(narrow, u, p=p)
+    both(narrow, u, t=[1.0, 10.0, 0.01, 1e6, 0.1, 3.0], k=[V // 2, 10, 1, 2000, V - 1, 100], p=p, m=[0.0, 0.5, 0.9, 0.0, 0.1, 0.0])
+    both(narrow.bfloat16(), u, k=[V // 2, 10, 1, 2000, V - 1, 100])
+
+
+def test_temperatures():
+    x = rows(10, 3000, "fp32", 21)
+    x[1, 17] = x[1, 2000] = 40.0                     # the first of two equal ones
+    t = [0.0, -1.0, math.nan, 1e-30, 1e-4, 1e4, 1e30, math.inf, -0.0, 1.0]
+    got = both(x, uniform(10, 5), t=t)
+    assert int(got[1]) == 17
+    both(x, uniform(10, 6), t=t, k=[3] * 10, p=[0.9] * 10, m=[0.1] * 10)
+
+
+def test_rows_that_are_masked():
+    x = rows(8, 2000, "fp32", 22)
+    none = -math.inf
+    x[0] = none
+    x[1] = math.nan
+    x[2, :1990] = none
+    x[3, 5:] = math.nan
+    x[4, [3, 500, 1999]] = math.inf
+    x[5, 1::2] = none
+    x[6, :] = torch.finfo(torch.float32).min         # the lowest number masks nothing on its own
+    x[7, :1999] = torch.finfo(torch.float32).min
+    u = [0.5, 0.5, 0.3, 0.7, 0.4, 0.9, 0.25, 0.99]
+    got = both(x, u)
+    assert got[:2].tolist() == [-1, -1] and int(got[4]) == 500 and int(got[6]) == 500 and int(got[7]) == 1999
+    both(x, u, k=[3] * 8, p=[0.9] * 8)
+    both(x, u, t=[0.0] * 8)
+    both(x.half().float().bfloat16(), u, p=[0.5] * 8)
+
+
+def test_odd_settings():
+    x = rows(8, 500, "bf16", 23)
+    u = [0.0, 1.0, 2.0, -1.0, math.nan, math.inf, 0.5, 1.0 - 2.0 ** -24]
+    both(x, u, strict=False)
+    both(x, u, k=[-5, 0, 500, 501, 2 ** 31 - 1, -2 ** 31, 1, 2], strict=False)
+    v = uniform(8, 9)
+    both(x, v, p=[0.0, -1.0, 1.0, 2.0, math.nan, math.inf, 1e-30, 1.0 - 2.0 ** -24], strict=False)
+    both(x, v, m=[0.0, -1.0, 1.0, 2.0, math.nan, 1e-30, 0.5, 1.0 - 2.0 ** -24])
+
+
+@pytest.mark.parametrize("V", [(1 << 20) - 3, 1 << 20])
+def test_largest_vocabulary(V):
+    x = rows(3, V, "fp32", 24, scale=1.0)
+    both(x, uniform(3, 24), k=[0, 1000, 500000], p=[0.9, 0.99, 1.0], strict=False)
+    both(torch.zeros(2, V, device="cuda"), [0.5, 0.999], p=[0.5, 1.0])
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 17, 64, 300, 1000])
+def test_batches(T):
+    """The same row of a batch whatever the batch: the same token."""
+    V = 3001
+    x = rows(T, V, "bf16", 25)
+    u = torch.rand(T, generator=torch.Generator().manual_seed(T)).cuda()
+    p = torch.linspace(0.3, 1.0, T).cuda()
+    k = torch.arange(T, dtype=torch.int32).cuda()
+    token, logprob = M.sample(x, u, top_p=p, top_k=k, want_logprob=True)
+    for i in sorted({0, 1, T // 2, T - 1} & set(range(T))):
+        one, lp = M.sample(x[i:i + 1], u[i:i + 1], top_p=p[i:i + 1], top_k=k[i:i + 1], want_logprob=True)
+        assert int(one) == int(token[i]) and float(lp) == float(logprob[i])
+    few = min(T, 20)
+    both(x[:few], u[:few].tolist(), p=p[:few].tolist(), k=k[:few].tolist())
+    assert M.sample(x, u)[1] is None and M.sample(x[:0], u[:0])[0].shape == (0,)
+
+
+def test_frequencies():
+    """Tokens come as often as their probabilities say: 65536 evenly spaced numbers, each token's count within one."""
+    x = torch.tensor([[0.0, 1.0, -1.0, 2.0, -math.inf, 0.5]]).cuda()
+    n = 1 << 16
+    u = ((torch.arange(n, dtype=torch.float64) + 0.5) / n).float().cuda()
+    got = torch.bincount(M.sample(x.expand(n, -1), u)[0].long(), minlength=6).cpu()
+    want = torch.softmax(x[0].double().cpu(), 0) * n
+    assert bool(((got - want).abs() <= 1.01).all())
+
+
+@pytest.mark.parametrize("T,V", [(3, 50000), (40, 5000), (300, 2000)])
+def test_graphs_and_streams(T, V):
+    x = rows(T, V, "bf16", 26)
+    u = torch.rand(T, generator=torch.Generator().manual_seed(2)).cuda()
+    k = torch.full((T,), 50, dtype=torch.int32).cuda()
+    p = torch.full((T,), 0.9).cuda()
+    p[0] = 1.0
+    k[T // 2] = 0
+    first = M.sample(x, u, top_k=k, top_p=p, want_logprob=True)
+    ws = torch.full((max(256, M.sample_workspace_bytes(T, V)),), 0xAB, dtype=torch.uint8, device="cuda")
+    token, logprob = torch.empty_like(first[0]), torch.empty_like(first[1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        M.sample(x, u, top_k=k, top_p=p, token=token, logprob=logprob, ws=ws)
+    for i in range(3):
+        token.fill_(-9)
+        ws.fill_(0xCD)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(token, first[0]) and torch.equal(logprob, first[1])
+        again = M.sample(x, u, top_k=k, top_p=p, want_logprob=True)
+        assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+    given = M.sample(x, u, top_k=k, top_p=p, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(given[0], first[0])
