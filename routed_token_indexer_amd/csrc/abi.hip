@@ -1237,7 +1237,8 @@ size_t misa_cache_workspace_bytes(int32_t op, const misa_kv_cache* cache, int64_
   if (op == MISA_OP_ATTEND_MASS) {
     if (T < 0 || T >= (int64_t(1) << 31) || Hq < cache->heads || Hq % cache->heads) return 0;
     if (mass_tiles(cache, L) >= (1 << 24)) return 0;
-    const int splits = misa::mass_splits(T, cache->nseq, cache->heads, Hq / cache->heads, L, cache->d);
+    const int group = Hq / cache->heads;
+    const int splits = misa::mass_few(T, cache->nseq, group, 0, 0) ? 1 : misa::mass_splits(T, cache->nseq, cache->heads, group, L, cache->d);
     if (splits == 1 && lists == cache->heads) return 0;
     return round_up((size_t)splits * (size_t)cache->nseq * cache->heads * (size_t)L * sizeof(float));
   }
@@ -1296,7 +1297,8 @@ int32_t misa_attend_mass(const misa_kv_cache* cache, const void* q, int64_t q_ts
   a.in = in;
   a.out = out;
   a.G = lists;
-  a.splits = misa::mass_splits(T, a.kv.nseq, a.Hkv, a.group, a.kv.Lmax, a.d);
+  a.few = misa::mass_few(T, a.kv.nseq, a.group, q_ts, q_hs);
+  a.splits = a.few ? 1 : misa::mass_splits(T, a.kv.nseq, a.Hkv, a.group, a.kv.Lmax, a.d);
   a.part = a.splits > 1 || lists != cache->heads ? static_cast<float*>(ws) : nullptr;
   if (misa::mass_blocks(a) >= (int64_t(1) << 24)) return fail(MISA_ERR_ARG, "%s: grid too large", fn);
   return hip_status(misa::launch_mass(a, cache->dtype == MISA_FP16, (hipStream_t)stream), fn);

@@ -20,7 +20,6 @@ namespace {
 using namespace attend;
 
 constexpr int kThreads = 256;
-constexpr int kKeys = 128;      // keys of a workgroup
 
 // What a lane knows of its row.
 struct Row {
@@ -30,14 +29,11 @@ struct Row {
   float slope2;
 };
 
-// Row r of the rows (query, head) of kv head g, queries from t0 on.
+// Row of query t and a head; `is`: there is such a row.
 template <int MODE>
-__device__ __forceinline__ Row row_info(const MassArgs& a, int n, int g, int64_t t0, uint32_t r, uint32_t rows) {
+__device__ __forceinline__ Row row_info(const MassArgs& a, int n, int64_t t, int head, bool is) {
   Row x{0, 0, 0, 0.f, 0.f};
-  if (r >= rows) return x;
-  const uint32_t qi = fast_quot(a.by_group, r);
-  const int64_t t = t0 + qi;
-  const int head = g * a.group + (int)(r - qi * a.group);
+  if (!is) return x;
   const int seq = a.q_seq[t], len = a.q_len[t];
   const int start = a.q_start ? a.q_start[t] : 0;
   const float lse = a.lse[t * a.Hq + head];
@@ -48,20 +44,46 @@ __device__ __forceinline__ Row row_info(const MassArgs& a, int n, int g, int64_t
   x.lse2 = lse * kLog2e;
   x.hi = clamp_len(len, a.kv.Lmax);
   x.lo = start < 0 ? 0 : start;
-  if (seq != n || lse == -__builtin_inff()) x.lo = x.hi = 0;
+  if (seq != n || lse == -__builtin_inff() || x.lo > x.hi) x.lo = x.hi = 0;
   return x;
 }
 
-// The queries that see some of the keys [k0, k0 + kKeys), of [t_lo, t_hi): from the
+// The same by 32-bit offsets behind query t and a head: query t + qi, head + h.
+template <int MODE>
+__device__ __forceinline__ Row row_behind(const MassArgs& a, int n, int64_t t, int head, int qi, int h, bool is) {
+  const int o = is ? 4 * qi : 0;
+  auto load = [&](const int32_t* p) {
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(buffer_view(p + t, 0xfffffff0u), o, 0, 0);
+  };
+  const int seq = load(a.q_seq), len = load(a.q_len), start = a.q_start ? load(a.q_start) : 0;
+  const float lse = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_view(a.lse + t * a.Hq + head, 0xfffffff0u),
+                                                                         is ? 4 * (qi * a.Hq + h) : 0, 0, 0));
+  Row x;
+  x.pos = 0;
+  x.slope2 = 0.f;
+  if constexpr (MODE == kBias) {
+    x.pos = a.q_pos ? load(a.q_pos) : len - 1;
+    x.slope2 = a.slopes ? a.slopes[is ? head + h : 0] * kLog2e : 0.f;
+  }
+  x.lse2 = lse * kLog2e;
+  x.lo = max(start, 0);
+  x.hi = min(len, (int)a.kv.Lmax);
+  if (!is || seq != n || lse == -__builtin_inff() || x.lo >= x.hi) x.lo = x.hi = 0;
+  return x;
+}
+
+// The queries that see some of the keys [k0, k0 + KEYS), of [t_lo, t_hi): from the
 // first to the last one. All threads of the workgroup call it.
+template <int KEYS>
 __device__ __forceinline__ void seeing(const MassArgs& a, int n, int k0, int64_t t_lo, int64_t t_hi, int64_t& t0,
                                        int64_t& t1) {
   __shared__ int first[kThreads / 64], last[kThreads / 64];
   int lo = 0x7fffffff, hi = -1;
+#pragma unroll 4
   for (int64_t t = t_lo + threadIdx.x; t < t_hi; t += kThreads) {
     const int len = clamp_len(a.q_len[t], a.kv.Lmax);
     const int start = a.q_start ? a.q_start[t] : 0;
-    if (a.q_seq[t] == n && start < len && len > k0 && start < k0 + kKeys) {
+    if (a.q_seq[t] == n && start < len && len > k0 && start < k0 + KEYS) {
       lo = min(lo, (int)t);
       hi = max(hi, (int)t);
     }
@@ -92,26 +114,32 @@ __device__ __forceinline__ const uint16_t* key_row(const MassArgs& a, int n, int
   return a.kv.k + page * a.kv.page_stride + (int64_t)(s - (int)col * a.kv.page) * a.kv.tok_stride + g * a.kv.head_stride;
 }
 
-// Weights of MR rows and MR keys (one accumulator tile) added to the keys' sums.
-// off: the first key that the lane's registers hold, relative to the row's numbers.
-template <int MR, int MODE, bool MASK, typename Acc>
-__device__ __forceinline__ void add_weights(const Acc& s, Acc& sum, const Row& r, int key, uint64_t have, float c,
-                                            const FarCap& cap) {
-  constexpr int AR = MR * MR / 64;
+// Scores of MR rows and MR keys (one accumulator tile), less the rows' log-sums, in units
+// of log2. key: the first key that the lane's registers hold.
+template <int MR, int MODE, typename Acc>
+__device__ __forceinline__ void finish_scores(Acc& s, const Row& r, int key, float c, const FarCap& cap) {
 #pragma unroll
-  for (int j = 0; j < AR; ++j) {
-    const int o = MR == 32 ? 8 * (j >> 2) + (j & 3) : j;
-    float x;
+  for (int j = 0; j < MR * MR / 64; ++j) {
     if constexpr (MODE == kPlain) {
-      x = s[j] * c - r.lse2;
+      s[j] = s[j] * c - r.lse2;
     } else {
+      const int o = MR == 32 ? 8 * (j >> 2) + (j & 3) : j;
       float off = r.lse2;
       if constexpr (MODE == kBias) off += r.slope2 * (float)abs(r.pos - (key + o));
-      x = cap.cap2 != 0.f ? cap.chosen(s[j], off) : s[j] * c - off;
+      s[j] = cap.cap2 != 0.f ? cap.chosen(s[j], off) : s[j] * c - off;
     }
-    float p = __builtin_amdgcn_exp2f(x);
-    if constexpr (MASK) p = (key + o >= r.lo && key + o < r.hi && (have >> o & 1)) ? p : 0.f;
-    sum[j] += p;
+  }
+}
+
+// What a row does not see adds nothing, whatever its score is.
+template <int MR, typename Acc>
+__device__ __forceinline__ void hide(Acc& s, const Row& r, int key) {
+  const int first = r.lo - key;
+  const uint32_t many = (uint32_t)(r.hi - r.lo);
+#pragma unroll
+  for (int j = 0; j < MR * MR / 64; ++j) {
+    const int o = MR == 32 ? 8 * (j >> 2) + (j & 3) : j;
+    s[j] = (uint32_t)(o - first) < many ? s[j] : -__builtin_inff();
   }
 }
 
@@ -126,10 +154,11 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-// Writes the sums of the keys [k0, k0 + kKeys), which lie in LDS.
+// Writes the sums of the keys [k0, k0 + KEYS), which lie in LDS.
+template <int KEYS>
 __device__ __forceinline__ void store_sums(const MassArgs& a, int n, int g, int split, int k0, const float* sums) {
   const int s = k0 + (int)threadIdx.x;
-  if (threadIdx.x >= kKeys || s >= a.kv.Lmax) return;
+  if (threadIdx.x >= KEYS || s >= a.kv.Lmax) return;
   const float v = sums ? sums[threadIdx.x] : 0.f;
   if (a.part) {
     a.part[(((int64_t)split * a.kv.nseq + n) * a.Hkv + g) * a.kv.Lmax + s] = v;
@@ -139,172 +168,258 @@ __device__ __forceinline__ void store_sums(const MassArgs& a, int n, int g, int 
   }
 }
 
-// Few rows a sequence (decode steps): each wave takes 32 keys and all rows, 16 at a time.
+// Few rows a sequence (decode steps): memory-bound, so each wave is on its own. It takes
+// 64 keys of one kv head, all under way at once, and all rows, 16 at a time. The look-up
+// of the keys' pages goes beside the search for the queries. Neighbouring waves take the
+// kv heads of the same keys, then the next keys, one sequence after the other: 8 x 32768 tokens
+// of 8 heads of 128 in 87 us, 4.5 TB/s (the sequences side by side 101; runs of 2 to 8 such
+// pieces a wave, the next one under way, 88 to 108; keys through LDS, whole rows an
+// instruction, 107).
+constexpr int kFewTiles = 4, kFewKeys = 16 * kFewTiles;
+
 template <bool HALF, int D, int MODE>
-__global__ __launch_bounds__(kThreads) void mass_few_kernel(MassArgs a) {
-  constexpr int KF = D / 32;
-  __shared__ float sums[kKeys];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int lists = (int)a.kv.nseq * a.Hkv;
-  const int tile = blockIdx.x / lists, list = blockIdx.x % lists;
-  const int n = list / a.Hkv, g = list % a.Hkv, k0 = tile * kKeys;
-  int64_t t0, t1;
-  seeing(a, n, k0, 0, a.T, t0, t1);
-  if (t0 >= t1) {
-    if (a.part || a.in != a.out) store_sums(a, n, g, 0, k0, nullptr);
-    return;
-  }
-  const int key0 = k0 + 32 * wave;
-  u32x4 kf[2][KF];
-  uint64_t have[2];
+__global__ __launch_bounds__(kThreads, 2) void mass_few_kernel(MassArgs a) {
+  constexpr int KF = D / 32, NT = kFewTiles;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + uniform((int)threadIdx.x >> 6);
+  const int64_t of_seq = (a.kv.Lmax + kFewKeys - 1) / kFewKeys * a.Hkv;
+  const int n = (int)(unit / of_seq);
+  if (n >= a.kv.nseq) return;
+  const int64_t rest = unit - n * of_seq;
+  const int g = (int)(rest % a.Hkv), key0 = (int)(rest / a.Hkv) * kFewKeys;
+  // lanes 0 .. 15 of each 16 take one key's sum each
+  const int mine = key0 + 16 * ((lane & 15) >> 2) + 4 * (lane >> 4) + (lane & 3);
+  const bool holds = mine < a.kv.Lmax;
+  const int64_t at = ((int64_t)n * a.Hkv + g) * a.kv.Lmax + mine;
+  const uint16_t* p[NT];
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint16_t* p = key_row(a, n, g, key0 + 16 * i + (lane & 15));
-    have[i] = __ballot(p != nullptr);
-#pragma unroll
-    for (int f = 0; f < KF; ++f)
-      kf[i][f] = p ? *reinterpret_cast<const u32x4*>(p + 32 * f + 8 * (lane >> 4)) : u32x4{0, 0, 0, 0};
-  }
-  const uint32_t rows = (uint32_t)(t1 - t0) * a.group;
-  const float c = a.scale * kLog2e;
-  const FarCap cap = a.cap != 0.f ? far_cap(a.cap, a.scale / a.cap) : FarCap{0.f, 0.f, 0.f, false};
-  floatx4 sum[2] = {};
-  for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
-    const uint32_t r = r0 + (lane & 15);
-    const Row x = row_info<MODE>(a, n, g, t0, r, rows);
-    const uint32_t rr = r < rows ? r : 0, qi = fast_quot(a.by_group, rr);
-    const uint16_t* q = a.q + (t0 + qi) * a.q_ts + (int64_t)(g * a.group + (int)(rr - qi * a.group)) * a.q_hs + 8 * (lane >> 4);
-    u32x4 qf[KF];
-#pragma unroll
-    for (int f = 0; f < KF; ++f) qf[f] = *reinterpret_cast<const u32x4*>(q + 32 * f);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      floatx4 s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int f = 0; f < KF; ++f) s = mfma16<HALF>(kf[i][f], qf[f], s);
-      const int key = key0 + 16 * i + 4 * (lane >> 4);
-      add_weights<16, MODE, true>(s, sum[i], x, key, have[i] >> (4 * (lane >> 4)), c, cap);
+  for (int i = 0; i < NT; ++i) p[i] = key_row(a, n, g, key0 + 16 * i + (lane & 15));
+  const float before = holds && !a.part && a.in ? a.in[at] : 0.f;
+  int lo = 0x7fffffff, hi = -1;
+#pragma unroll 4
+  for (int64_t t = lane; t < a.T; t += 64) {
+    const int seq = a.q_seq[t], len = clamp_len(a.q_len[t], a.kv.Lmax);
+    const int start = a.q_start ? a.q_start[t] : 0;
+    if (seq == n && start < len && len > key0 && start < key0 + kFewKeys) {
+      lo = min(lo, (int)t);
+      hi = max(hi, (int)t);
     }
   }
+  const int64_t t0 = wave_min_of(lo), t1 = (int64_t)wave_max_of(hi) + 1;
+  float total = 0.f;
+  if (t0 < t1) {
+    u32x4 kf[NT][KF];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v = sum_lanes<16>(sum[i][j]);
-      if ((lane & 15) == j) sums[32 * wave + 16 * i + 4 * (lane >> 4) + j] = v;
+      for (int f = 0; f < KF; ++f)
+        kf[i][f] = p[i] ? *reinterpret_cast<const u32x4*>(p[i] + 32 * f + 8 * (lane >> 4)) : u32x4{0, 0, 0, 0};
+    const uint32_t rows = (uint32_t)(t1 - t0) * a.group;
+    const float c = a.scale * kLog2e;
+    const FarCap cap = a.cap != 0.f ? far_cap(a.cap, a.scale / a.cap) : FarCap{0.f, 0.f, 0.f, false};
+    float sum[NT][4] = {};
+    for (uint32_t r0 = 0; r0 < rows; r0 += 16) {
+      const uint32_t r = r0 + (lane & 15), rr = r < rows ? r : 0, qi = fast_quot(a.by_group, rr);
+      const int head = g * a.group + (int)(rr - qi * a.group);
+      const Row x = row_info<MODE>(a, n, t0 + qi, head, r < rows);
+      const uint16_t* q = a.q + (t0 + qi) * a.q_ts + (int64_t)head * a.q_hs + 8 * (lane >> 4);
+      u32x4 qf[KF];
+#pragma unroll
+      for (int f = 0; f < KF; ++f) qf[f] = *reinterpret_cast<const u32x4*>(q + 32 * f);
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        floatx4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < KF; ++f) s = mfma16<HALF>(kf[i][f], qf[f], s);
+        const int key = key0 + 16 * i + 4 * (lane >> 4);
+        finish_scores<16, MODE>(s, x, key, c, cap);
+        hide<16>(s, x, key);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[i][j] += __builtin_amdgcn_exp2f(s[j]);
+      }
     }
-  __syncthreads();
-  store_sums(a, n, g, 0, k0, sums);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const uint64_t there = __ballot(p[i] != nullptr);     // a key without a page is given nothing
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float v = sum_lanes<16>(sum[i][j]);
+        if ((lane & 15) == 4 * i + j && there >> (4 * (lane >> 4) + j) & 1) total = v;
+      }
+    }
+  }
+  if (!holds) return;
+  if (a.part) a.part[at] = total;
+  else if (t0 < t1 || a.in != a.out) a.out[at] = before + total;
 }
 
-// Many rows (prompts, windows of queries): 64 rows at a time go through LDS, the next
-// ones under way in registers meanwhile. Two groups of waves hold 64 keys each, and the
-// two waves of a group take the first and the last 32 of the rows; at d = 256 four
-// waves hold 32 keys each and take the same 32 rows (64 keys would spill).
+// Many rows (prompts, windows of queries): steps of 64 (d = 256: 32) rows go through LDS,
+// the next ones under way in registers meanwhile. Each wave holds 64 (32) keys and takes
+// all rows.
 template <int D>
 struct ManyShape {
   static constexpr int NT = D == 256 ? 1 : 2;            // tiles of 32 keys a wave
-  static constexpr int KG = kKeys / (32 * NT);           // groups of keys
-  static constexpr int RG = kThreads / 64 / KG;          // groups of rows
-  static constexpr int ROWS = 32 * RG;
+  static constexpr int KEYS = 32 * NT * kThreads / 64;   // keys of a workgroup
+  static constexpr int RT = D == 256 ? 1 : 2;            // tiles of 32 rows a step
+  static constexpr int ROWS = 32 * RT;
 };
 
 template <bool HALF, int D, int MODE>
 __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
   using S = ManyShape<D>;
-  constexpr int KF = D / 16, PIECES = D / 8, NT = S::NT, ROWS = S::ROWS, NLD = ROWS * PIECES / kThreads;
+  constexpr int KF = D / 16, PIECES = D / 8, NT = S::NT, RT = S::RT, ROWS = S::ROWS, NLD = ROWS * PIECES / kThreads;
   __shared__ __align__(16) uint16_t stage[2][ROWS * D];
-  __shared__ float sums[S::RG][kKeys];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, kg = wave % S::KG, rg = wave / S::KG;
+  __shared__ float sums[S::KEYS];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lists = (int)a.kv.nseq * a.Hkv;
-  const int split = blockIdx.x % a.splits, rest = blockIdx.x / a.splits;
-  const int tile = rest / lists, list = rest % lists;
-  const int n = list / a.Hkv, g = list % a.Hkv, k0 = tile * kKeys;
+  // the lists next to each other (on XCDs of their own where there are eight), the first
+  // keys before later ones and the last queries before earlier ones: the most work first
+  const int list = blockIdx.x % lists, rest = blockIdx.x / lists;
+  const int tiles = (int)(gridDim.x / (unsigned)(lists * a.splits));
+  const int tile = rest % tiles, split = a.splits - 1 - rest / tiles;
+  const int n = list / a.Hkv, g = list % a.Hkv, k0 = tile * S::KEYS;
   int64_t t0, t1;
-  seeing(a, n, k0, a.T * split / a.splits, a.T * (split + 1) / a.splits, t0, t1);
+  seeing<S::KEYS>(a, n, k0, a.T * split / a.splits, a.T * (split + 1) / a.splits, t0, t1);
   if (t0 >= t1) {
-    if (a.part || a.in != a.out) store_sums(a, n, g, split, k0, nullptr);
+    if (a.part || a.in != a.out) store_sums<S::KEYS>(a, n, g, split, k0, nullptr);
     return;
   }
-  const int key0 = k0 + 32 * NT * kg;
+  const int key0 = k0 + 32 * NT * wave;
   u32x4 kf[NT][KF];
-  uint64_t have[NT];
-  bool all_there = true;
+  uint64_t there[NT];     // a key without a page is given nothing at the end
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const uint16_t* p = key_row(a, n, g, key0 + 32 * i + (lane & 31));
-    have[i] = __ballot(p != nullptr);
-    all_there &= have[i] == ~0ull;
+    there[i] = __ballot(p != nullptr);
 #pragma unroll
     for (int f = 0; f < KF; ++f)
       kf[i][f] = p ? *reinterpret_cast<const u32x4*>(p + 16 * f + 8 * (lane >> 5)) : u32x4{0, 0, 0, 0};
   }
-  const uint32_t rows = (uint32_t)(t1 - t0) * a.group;
   const float c = a.scale * kLog2e;
   const FarCap cap = a.cap != 0.f ? far_cap(a.cap, a.scale / a.cap) : FarCap{0.f, 0.f, 0.f, false};
 
-  u32x4 next[NLD];
-  Row row_next;
-  auto fetch = [&](uint32_t r0) {
+  // A step takes all heads of `per` queries, or up to ROWS heads of one query. A thread's
+  // place in a step is the same in all steps: 32-bit offsets behind a uniform base.
+  const int per = a.group < ROWS ? ROWS / a.group : 1;
+  const int piece = 16 * ((int)threadIdx.x % PIECES);
+  uint32_t off[NLD];
+  int mark[NLD];        // query of the step, or head where a step has one query
 #pragma unroll
-    for (int i = 0; i < NLD; ++i) {
-      const int at = (int)threadIdx.x + i * kThreads;
-      const uint32_t r = r0 + at / PIECES, rr = r < rows ? r : 0, qi = fast_quot(a.by_group, rr);
-      next[i] = *reinterpret_cast<const u32x4*>(a.q + (t0 + qi) * a.q_ts +
-                                                (int64_t)(g * a.group + (int)(rr - qi * a.group)) * a.q_hs + 8 * (at % PIECES));
+  for (int i = 0; i < NLD; ++i) {
+    const int r = ((int)threadIdx.x + i * kThreads) / PIECES;
+    const int qi = per > 1 ? min((int)fast_quot(a.by_group, (uint32_t)r), per - 1) : 0;
+    mark[i] = per > 1 ? qi : r;
+    off[i] = 2u * (uint32_t)(qi * (int)a.q_ts + (per > 1 ? min(r - qi * a.group, a.group - 1) : r) * (int)a.q_hs) + piece;
+  }
+  int my_q[RT], my_h[RT];     // the lane's rows
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int my = 32 * i + (lane & 31);
+    my_q[i] = per > 1 ? (int)fast_quot(a.by_group, (uint32_t)my) : 0;
+    my_h[i] = my - my_q[i] * a.group;
+  }
+  u32x4 next[NLD];
+  Row x[RT], row_next[RT];
+  int64_t t = t0;       // first query of the next step to fetch
+  int h0 = 0;           // and first of its heads
+  auto fetch = [&]() __attribute__((always_inline)) {
+    const int head = g * a.group + h0;
+    const int left = per > 1 ? (int)min(t1 - t, (int64_t)per) : a.group - h0;
+    // in the place of what lies behind the last query or head: a row that there is
+    const __amdgpu_buffer_rsrc_t q = buffer_view(a.q + t * a.q_ts + (int64_t)head * a.q_hs, 0xfffffff0u);
+#pragma unroll
+    for (int i = 0; i < NLD; ++i)
+      next[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q, (int)(mark[i] < left ? off[i] : piece), 0, 0));
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+      row_next[i] = row_behind<MODE>(a, n, t, head, my_q[i], my_h[i], (per > 1 ? my_q[i] : my_h[i]) < left && my_q[i] < per);
+    h0 += ROWS;
+    if (h0 >= a.group) {
+      h0 = 0;
+      t += per;
     }
-    row_next = row_info<MODE>(a, n, g, t0, r0 + 32 * rg + (lane & 31), rows);
   };
-  auto put = [&](int b) {
+  auto put = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NLD; ++i) {
       const int at = (int)threadIdx.x + i * kThreads, r = at / PIECES, p = at % PIECES;
       *reinterpret_cast<u32x4*>(&stage[b][r * D + 8 * (p ^ swizzle<D>(r))]) = next[i];
     }
   };
-  floatx16 sum[NT] = {};
-  fetch(0);
-  put(0);
-  Row x = row_next;
-  __syncthreads();
-  int b = 0;
-  for (uint32_t r0 = 0; r0 < rows; r0 += ROWS, b ^= 1) {
-    const bool more = r0 + ROWS < rows;
-    if (more) fetch(r0 + ROWS);
-    const bool sees = x.lo < x.hi && x.hi > key0 && x.lo < key0 + 32 * NT;
-    if (__ballot(sees)) {
-      const bool whole = all_there && __ballot(x.lo <= key0 && x.hi >= key0 + 32 * NT) == ~0ull;
-      floatx16 s[NT] = {};
-      const int r = 32 * rg + (lane & 31);
+  float sum[NT][16] = {};
+  // The scores of 32 rows go into s[u] while the weights of the 32 rows before, whose
+  // scores are finished, are added from s[1 - u].
+  floatx16 s[2][NT];
 #pragma unroll
-      for (int f = 0; f < KF; ++f) {
-        const u32x4 qf = *reinterpret_cast<const u32x4*>(&stage[b][r * D + 8 * ((2 * f + (lane >> 5)) ^ swizzle<D>(r))]);
+  for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int i = 0; i < NT; ++i) s[i] = mfma32<HALF>(kf[i][f], qf, s[i]);
+    for (int j = 0; j < 16; ++j) s[1][k][j] = -__builtin_inff();
+  auto add = [&](int u) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        sum[k][j] += __builtin_amdgcn_exp2f(s[u][k][j]);
+        asm volatile("" : "+v"(sum[k][j]));      // here, beside the products, not behind a later branch
       }
-      const int sh = 4 * (lane >> 5), key = key0 + sh;
+  };
+  // rows r .. r + 31 of stage[b]
+  auto rows32 = [&](int b, int u, int r, const Row& x) __attribute__((always_inline)) {
+    r += lane & 31;
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        if (whole) add_weights<32, MODE, false>(s[i], sum[i], x, key + 32 * i, 0, c, cap);
-        else add_weights<32, MODE, true>(s[i], sum[i], x, key + 32 * i, have[i] >> sh, c, cap);
-      }
+    for (int k = 0; k < NT; ++k) s[u][k] = floatx16{};
+#pragma unroll
+    for (int f = 0; f < KF; ++f) {
+      const u32x4 qf = *reinterpret_cast<const u32x4*>(&stage[b][r * D + 8 * ((2 * f + (lane >> 5)) ^ swizzle<D>(r))]);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) s[u][k] = mfma32<HALF>(kf[k][f], qf, s[u][k]);
+    }
+    add(u ^ 1);
+    const int key = key0 + 4 * (lane >> 5);
+#pragma unroll
+    for (int k = 0; k < NT; ++k) finish_scores<32, MODE>(s[u][k], x, key + 32 * k, c, cap);
+    if (__ballot(x.lo <= key0 && x.hi >= key0 + 32 * NT) != ~0ull) {
+#pragma unroll
+      for (int k = 0; k < NT; ++k) hide<32>(s[u][k], x, key + 32 * k);
+    }
+  };
+  auto turn = [&](auto which) __attribute__((always_inline)) {        // false: that was the last step
+    constexpr int b = decltype(which)::value;
+    const bool more = t < t1;
+    if (more) fetch();
+    if constexpr (RT == 1) {
+      rows32(b, b, 0, x[0]);
+    } else {
+      rows32(b, 0, 0, x[0]);
+      rows32(b, 1, 32, x[1]);
     }
     if (more) {
       put(b ^ 1);
-      x = row_next;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) x[i] = row_next[i];
+      __syncthreads();
+    } else {
+      add(RT == 1 ? b : 1);
     }
-    __syncthreads();
+    return more;
+  };
+  fetch();
+  put(0);
+#pragma unroll
+  for (int i = 0; i < RT; ++i) x[i] = row_next[i];
+  __syncthreads();
+  while (turn(std::integral_constant<int, 0>{}) && turn(std::integral_constant<int, 1>{})) {
   }
 #pragma unroll
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float v = sum_lanes<32>(sum[i][j]);
-      if ((lane & 31) == j) sums[rg][32 * NT * kg + 32 * i + 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3)] = v;
+      const int k = 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+      if ((lane & 31) == j) sums[32 * NT * wave + 32 * i + k] = there[i] >> k & 1 ? v : 0.f;
     }
   __syncthreads();
-  if (S::RG > 1 && threadIdx.x < kKeys) sums[0][threadIdx.x] += sums[S::RG - 1][threadIdx.x];
-  store_sums(a, n, g, split, k0, sums[0]);
+  store_sums<S::KEYS>(a, n, g, split, k0, sums);
 }
 
 // out = in + the sums of all query ranges (and, for G = 1, of all heads), in a fixed order.
@@ -314,19 +429,28 @@ __global__ __launch_bounds__(kThreads) void mass_join_kernel(MassArgs a) {
   const int64_t list = i / a.kv.Lmax, s = i - list * a.kv.Lmax;
   const int64_t n = list / a.G;
   const int heads = a.G == 1 ? a.Hkv : 1, g0 = a.G == 1 ? 0 : (int)(list - n * a.G);
+  const float* p = a.part + ((int64_t)n * a.Hkv + g0) * a.kv.Lmax + s;
+  const int64_t step = a.kv.nseq * a.Hkv * a.kv.Lmax;
   float v = 0.f;
-  for (int c = 0; c < a.splits; ++c)
-    for (int h = 0; h < heads; ++h) v += a.part[(((int64_t)c * a.kv.nseq + n) * a.Hkv + g0 + h) * a.kv.Lmax + s];
+  for (int c0 = 0; c0 < a.splits * heads; c0 += 8) {      // 8 of them on their way at a time
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + j, split = c / heads;
+      x[j] = c < a.splits * heads ? p[split * step + (int64_t)(c - split * heads) * a.kv.Lmax] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v += x[j];
+  }
   a.out[i] = (a.in ? a.in[i] : 0.f) + v;
 }
 
-bool few_rows(int64_t T, int64_t nseq, int group) { return (T + nseq - 1) / nseq * group <= 16; }
-
-int64_t key_tiles(const KvView& kv) { return (kv.Lmax + kKeys - 1) / kKeys; }
+// Keys of a workgroup of the kernel for many rows.
+int many_keys(int d) { return d == 256 ? ManyShape<256>::KEYS : ManyShape<128>::KEYS; }
 
 template <bool HALF, int D, int MODE>
 void launch_mode(const MassArgs& a, unsigned blocks, hipStream_t st) {
-  if (few_rows(a.T, a.kv.nseq, a.group))
+  if (a.few)
     hipLaunchKernelGGL((mass_few_kernel<HALF, D, MODE>), dim3(blocks), dim3(kThreads), 0, st, a);
   else
     hipLaunchKernelGGL((mass_many_kernel<HALF, D, MODE>), dim3(blocks), dim3(kThreads), 0, st, a);
@@ -346,16 +470,26 @@ void launch_type(const MassArgs& a, unsigned blocks, hipStream_t st) {
 
 }  // namespace
 
+// 16 rows a sequence on average and fewer, or queries whose rows lie further apart than the
+// other kernel's 32-bit offsets reach over a step of 64 rows.
+bool mass_few(int64_t T, int64_t nseq, int group, int64_t q_ts, int64_t q_hs) {
+  return (T + nseq - 1) / nseq * group <= 16 || q_ts >= (1 << 23) || q_hs >= (1 << 23);
+}
+
+// The chip holds some 512 workgroups. One takes some 4 us before its first product, the time
+// of 512 rows. So the queries are split until there are 1024 workgroups with 128 rows of a
+// sequence each on average, or 4096 with 256 (8192 causal tokens 791 us with 2048 workgroups, 707 with
+// 4096; windows of 64 queries behind 32K keys 107 us with one range, 159 with two).
 int mass_splits(int64_t T, int64_t nseq, int heads, int group, int64_t Lmax, int d) {
-  if (few_rows(T, nseq, group)) return 1;
-  const int64_t tiles = (Lmax + kKeys - 1) / kKeys * nseq * heads;
+  const int64_t tiles = (Lmax + many_keys(d) - 1) / many_keys(d) * nseq * heads, rows = T * group / nseq;
   int s = 1;
-  while (s < 16 && tiles * s < 2048 && T * group / (s * 2) >= 1024) s *= 2;
+  while (s < 64 && tiles * s < 4096 && rows > (tiles * s < 1024 ? 256 : 512) * s) s *= 2;
   return s;
 }
 
 int64_t mass_blocks(const MassArgs& a) {
-  return key_tiles(a.kv) * a.kv.nseq * a.Hkv * a.splits;
+  const int64_t keys = a.few ? kFewKeys : many_keys(a.d), units = (a.kv.Lmax + keys - 1) / keys * a.kv.nseq * a.Hkv;
+  return a.few ? (units + kThreads / 64 - 1) / (kThreads / 64) : units * a.splits;
 }
 
 hipError_t launch_mass(const MassArgs& a, bool half, hipStream_t st) {

@@ -24,11 +24,13 @@ struct MassArgs {
   const float* in;          // [nseq][G][Lmax] or null: zeros
   float* out;
   int32_t G;                // Hkv, or 1: summed over the heads
+  bool few;                 // few rows a sequence
   // sums of query range c of `splits` in part[c][nseq][Hkv][Lmax]; null: straight to out
   int32_t splits;
   float* part;
 };
-// Query ranges of a call (1: not split).
+bool mass_few(int64_t T, int64_t nseq, int group, int64_t q_ts, int64_t q_hs);
+// Query ranges of a call that has more (1: not split).
 int mass_splits(int64_t T, int64_t nseq, int heads, int group, int64_t Lmax, int d);
 int64_t mass_blocks(const MassArgs& a);   // workgroups (of 256 threads) of its largest launch
 hipError_t launch_mass(const MassArgs& a, bool half, hipStream_t st);
