@@ -1365,7 +1365,10 @@ int32_t misa_cache_move(const misa_kv_cache* cache, const int32_t* src, int32_t 
   return hip_status(misa::launch_move(a, (hipStream_t)stream), fn);
 }
 
-size_t misa_sample_workspace_bytes(int64_t T, int32_t V) { return 0; }
+size_t misa_sample_workspace_bytes(int64_t T, int32_t V) {
+  if (T < 1 || T >= (int64_t(1) << 22) || V < 1 || V > misa::kMaxVocab) return 0;
+  return misa::sample_ws_bytes(T, V);
+}
 
 int32_t misa_sample(const void* logits, int32_t dtype, int64_t row_stride, int64_t T, int32_t V,
                     const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
@@ -1395,7 +1398,7 @@ int32_t misa_sample(const void* logits, int32_t dtype, int64_t row_stride, int64
   a.u = u;
   a.token = token;
   a.logprob = logprob;
-  return hip_status(misa::launch_sample(a, dtype, (hipStream_t)stream), fn);
+  return hip_status(misa::launch_sample(a, dtype, ws, (hipStream_t)stream), fn);
 }
 
 int32_t misa_debug_scores(const void* q, const float* w, const void* k, const int32_t* heads, int32_t h,

@@ -75,7 +75,8 @@ struct SampleArgs {
   float* logprob;           // [T] or null
 };
 constexpr int32_t kMaxVocab = 1 << 20;
+size_t sample_ws_bytes(int64_t T, int32_t V);
 // type: 1 bf16, 2 fp16, 3 fp32
-hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st);
+hipError_t launch_sample(const SampleArgs& a, int type, void* ws, hipStream_t st);
 
 }  // namespace misa

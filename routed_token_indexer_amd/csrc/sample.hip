@@ -12,11 +12,19 @@
 // their sums are sums of 64-bit integers, exact (a row has at most 2^20 tokens) and the
 // same in any order.
 //
-// One workgroup a row. Its first pass finds the maximum. The second puts every weight
-// into a histogram over x, 64 bins to the unit, from which the running sums at the bins'
-// edges follow. The last one collects the tokens of the few bins in which a filter
-// cuts, sorts those, and sums what surely remains in segments of 512 tokens. A cut in
-// a bin of too many tokens (flat rows, many equal logits) is found by a radix descent.
+// The first pass over a row finds its maximum. The second puts every weight (or, for top-k
+// alone, every token) into a histogram over x, 64 bins to the unit, from which the
+// running sums at the bins' edges follow. The third collects the tokens of the few bins in
+// which a filter cuts, and sums what surely remains in segments of 512 tokens; the
+// collected ones are sorted, the cut found among them, and what remains of them is added
+// to the segments. A cut in a bin of too many tokens (flat rows, many equal logits) is
+// found by a radix descent over the row.
+//
+// Many rows: one workgroup each, all in one launch. Few: several workgroups each, a launch
+// a pass, the last one to finish the third pass drawing the token. The sums being exact,
+// both give the same bits.
+#include <algorithm>
+
 #include "misa_common.hpp"
 #include "misa_evict.hpp"
 
@@ -24,13 +32,12 @@ namespace misa {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048;             // of 1 / 64 each: all weights above e^-32
+constexpr int kBins = 2048;             // of 1 / 64 each: weights below e^-32 round to 0
 constexpr int kSeg = 512;               // tokens of a segment: 8 a lane
 constexpr int kMaxSegs = kMaxVocab / kSeg;
 static_assert(kMaxSegs == kBins && kBins == 2 * kThreads, "the running sums take two entries a thread");
-constexpr int kList = 4096;             // tokens that are sorted
+constexpr int kList = 4096;             // tokens of the bins with a cut, at most
 constexpr int kOne = 42;                // a weight of 1 is 2^kOne
-constexpr double kLeast = -29.8;        // e^x rounds to 0 below (2^-43)
 
 typedef unsigned long long u64;
 
@@ -45,77 +52,113 @@ __device__ __forceinline__ float logit_of(uint32_t bits) {   // 16 bits, or 32
 struct Row {
   const void* logits;
   int V;
-  float top;            // largest logit
+  float top;            // largest logit (0 where that is infinite, and all others -inf)
+  bool inf;             // it is infinite: such logits stand for 0, all others for -inf
+  float half, fine;     // top / 2; 128 / temperature
   double inv;           // log2(e) / temperature
-  double min_w;         // in units of 2^-kOne
+  double min_w;         // least weight, in units of 2^-kOne
+  int top_k;            // 0: all
+  bool by_sum;          // top-p cuts
+  double share;
+  __device__ __forceinline__ bool filtered() const { return top_k || by_sum; }
 };
-
-template <int TYPE>
-__device__ __forceinline__ float load_logit(const void* row, int i) {
-  if (TYPE == 3) return static_cast<const float*>(row)[i];
-  return logit_of<TYPE>(static_cast<const uint16_t*>(row)[i]);
-}
 
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 
-// Logits i .. i + 7 of a row; -inf behind its end.
+// Eight neighbouring logits of a row on their way.
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* row, int i, int V, float (&l)[8]) {
-  if (i + 8 <= V) {
+struct Raw {
+  u32x4 x[TYPE == 3 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* row, int i) {
     if (TYPE == 3) {
-      const u32x4 a = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(row) + i);
-      const u32x4 b = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(row) + i + 4);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        l[j] = __uint_as_float(a[j]);
-        l[4 + j] = __uint_as_float(b[j]);
-      }
+      x[0] = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(row) + i);
+      x[TYPE == 3] = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(row) + i + 4);
     } else {
-      const u32x4 a = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(row) + i);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        l[2 * j] = logit_of<TYPE>(a[j] & 0xffffu);
-        l[2 * j + 1] = logit_of<TYPE>(a[j] >> 16);
-      }
+      x[0] = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(row) + i);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) l[j] = i + j < V ? load_logit<TYPE>(row, i + j) : -__builtin_inff();
   }
+  __device__ __forceinline__ void get(float (&l)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      l[j] = TYPE == 3 ? __uint_as_float(x[j >> 2][j & 3])
+                       : logit_of<TYPE>(j & 1 ? x[0][j >> 1] >> 16 : x[0][j >> 1] & 0xffffu);
+  }
+};
+__device__ __forceinline__ float logit(const Row& r, float l) {
+  return r.inf ? (l == __builtin_inff() ? 0.f : -__builtin_inff()) : l;
 }
 
-// x log2(e), 0 for the largest logit also where it is infinite. NaN for NaN.
-__device__ __forceinline__ double exponent(const Row& r, float l) {
-  return l == r.top ? 0.0 : ((double)l - (double)r.top) * r.inv;
+// How far below the maximum, in bins. The order of logits is kept (every step rounds
+// monotonically), nothing overflows, and NaN and -inf give no number below kBins.
+__device__ __forceinline__ float depth_of(const Row& r, float l) { return __builtin_fmaf(l, -0.5f, r.half) * r.fine; }
+
+// a b + c with c in scalar registers (left to itself the compiler copies every c into
+// vector registers before it is used up there).
+__device__ __forceinline__ double fma_s(double a, double b, double c) {
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
 }
 
-// 2^t in units of 2^-kOne, to the nearest; t <= 0. 2^f of the rest |f| <= 1/2 by its
-// Taylor polynomial of degree 11 (6e-15 off).
+// 2^t in units of 2^-kOne; t <= 0. 2^f of the rest |f| <= 1/2 by its Taylor polynomial of
+// degree 11 (6e-15 off).
 __device__ __forceinline__ double weight_of(double t) {
-  const double n = __builtin_rint(t), f = t - n;
+  const double whole = t + 6755399441055744.0, f = t - (whole - 6755399441055744.0);   // 1.5 2^52: to the next integer
+  const int n = (int)__builtin_bit_cast(u64, whole);
   double p = 4.4455382718708110e-10;            // ln(2)^k / k!
-  p = __builtin_fma(p, f, 7.0549116208011225e-09);
-  p = __builtin_fma(p, f, 1.0178086009239699e-07);
-  p = __builtin_fma(p, f, 1.3215486790144309e-06);
-  p = __builtin_fma(p, f, 1.5252733804059841e-05);
-  p = __builtin_fma(p, f, 1.5403530393381608e-04);
-  p = __builtin_fma(p, f, 1.3333558146428443e-03);
-  p = __builtin_fma(p, f, 9.6181291076284770e-03);
-  p = __builtin_fma(p, f, 5.5504108664821580e-02);
-  p = __builtin_fma(p, f, 2.4022650695910072e-01);
-  p = __builtin_fma(p, f, 6.9314718055994531e-01);
+  p = fma_s(p, f, 7.0549116208011225e-09);
+  p = fma_s(p, f, 1.0178086009239699e-07);
+  p = fma_s(p, f, 1.3215486790144309e-06);
+  p = fma_s(p, f, 1.5252733804059841e-05);
+  p = fma_s(p, f, 1.5403530393381608e-04);
+  p = fma_s(p, f, 1.3333558146428443e-03);
+  p = fma_s(p, f, 9.6181291076284770e-03);
+  p = fma_s(p, f, 5.5504108664821580e-02);
+  p = fma_s(p, f, 2.4022650695910072e-01);
+  p = fma_s(p, f, 6.9314718055994531e-01);
   p = __builtin_fma(p, f, 1.0);
-  return p * __builtin_bit_cast(double, (u64)((int)n + kOne + 1023) << 52);
+  return p * __builtin_bit_cast(double, (u64)(uint32_t)(n + kOne + 1023) << 52);
 }
-// A weight as an integer; 0 where min_p drops it, below the least one, and for NaN.
-__device__ __forceinline__ u64 weight(const Row& r, double t) {
-  if (!(t > kLeast * 1.4426950408889634)) return 0;
-  const double w = weight_of(t);
+__device__ __forceinline__ double exponent(const Row& r, float l) { return ((double)l - (double)r.top) * r.inv; }
+// The weight of a logit that is less than kBins deep, to the nearest whole number; 0 where
+// min_p drops it. As a number in fp64, and as an integer.
+__device__ __forceinline__ double rounded(const Row& r, float l) {
+  const double w = weight_of(exponent(r, l));
+  const double y = (w + 4503599627370496.0) - 4503599627370496.0;     // 2^52
+  return w < r.min_w ? 0.0 : y;
+}
+__device__ __forceinline__ u64 weight(const Row& r, float l) {
+  const double w = weight_of(exponent(r, l));
   const u64 y = __builtin_bit_cast(u64, w + 4503599627370496.0) & 0xfffffffffffffull;   // 2^52
-  return w >= r.min_w ? y : 0;
+  return w < r.min_w ? 0 : y;
 }
-__device__ __forceinline__ int bin_of(double t) {      // t > kLeast log2(e)
-  return min((int)(t * (-64.0 / 1.4426950408889634)), kBins - 1);
+
+// Data-parallel moves within rows of 16 lanes (0x110 + n: from n lanes below) and from row to
+// row (0x142: lane 15 to the next row, 0x143: lane 31 to the upper half). Lanes without a source
+// get `none`. Sums and scans over a wave by these take a fifth of the time of shuffles
+// through LDS.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 dpp(u64 none, u64 v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)none, (int)(uint32_t)v, CTRL, ROWS, 0xf, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(none >> 32), (int)(v >> 32), CTRL, ROWS, 0xf, false);
+  return (u64)hi << 32 | lo;
+}
+// op(op(first lane, second), ...) up to and with each lane; of all in lane 63.
+template <typename Op>
+__device__ __forceinline__ u64 scan_wave(u64 none, u64 v, Op op) {
+  v = op(v, dpp<0x111, 0xf>(none, v));
+  v = op(v, dpp<0x112, 0xf>(none, v));
+  v = op(v, dpp<0x114, 0xf>(none, v));
+  v = op(v, dpp<0x118, 0xf>(none, v));
+  v = op(v, dpp<0x142, 0xa>(none, v));
+  return op(v, dpp<0x143, 0xc>(none, v));
+}
+// The sum of a whole number below 2^47 per lane, in lane 63.
+__device__ __forceinline__ double wave_total(double v) {
+  auto add = [](u64 x, u64 y) {
+    return __builtin_bit_cast(u64, __builtin_bit_cast(double, x) + __builtin_bit_cast(double, y));
+  };
+  return __builtin_bit_cast(double, scan_wave(0, __builtin_bit_cast(u64, v), add));
 }
 
 // Tokens in descending order: larger logit first, then the lower id. 0: none (NaN).
@@ -125,372 +168,674 @@ __device__ __forceinline__ u64 order_of(float l, int i) {
 __device__ __forceinline__ int id_of(u64 order) { return kMaxVocab - 1 - (int)(order & (kMaxVocab - 1)); }
 __device__ __forceinline__ float logit_of_order(u64 order) { return key_score((uint32_t)(order >> 20)); }
 
-template <typename T>
-__device__ __forceinline__ T scan_wave(T v) {     // inclusive
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const T x = __shfl_up(v, off, 64);
-    if (lane >= off) v += x;
-  }
-  return v;
+// A workgroup's share of LDS.
+struct Shared {
+  u64 bins[2][kBins];       // number and sum of weights of the tokens of a bin, then of the bins up to and with it
+  u64 list[kList];          // tokens of the bins with a cut
+  u64 seg[kMaxSegs];        // sums of the weights that remain, by segment
+  u64 near[64];
+  u64 slots[kWaves];
+  u64 found[3];
+  uint32_t n;
+  Row row;
+};
+__device__ __forceinline__ Shared& lds() {
+  __shared__ Shared s;
+  return s;
+}
+constexpr int kCount = 0, kMass = 1, kSegments = 2;
+__device__ __forceinline__ u64* bins_of(int which) {
+  return which == kSegments ? lds().seg : lds().bins[which];
 }
 
-struct Shared {
-  u64 mass[kBins];          // of a bin, then of the bins up to and with it
-  uint32_t count[kBins];
-  u64 list[kList];
-  u64 seg[kMaxSegs];
-  u64 slots[kWaves];
-  u64 found[4];
-  uint32_t n;
-};
+// What is done once a row stands in functions of its own: a row passes through it once, so
+// its instructions come from memory each time (inlined and unrolled the kernel had 45 KB of code, and
+// four rows of 32000 tokens took 41 us instead of 29).
+#define MISA_ONCE __attribute__((noinline))
 
 // Inclusive sum of a value per thread, in thread order.
-template <typename T>
-__device__ __forceinline__ T scan_block(T v, u64* slots) {
-  const T incl = scan_wave(v);
+__device__ MISA_ONCE u64 scan_block(u64 v) {
+  Shared& s = lds();
+  const int wave = threadIdx.x >> 6;
+  v = scan_wave(0, v, [](u64 x, u64 y) { return x + y; });
   __syncthreads();
-  if ((threadIdx.x & 63) == 63) slots[threadIdx.x >> 6] = (u64)incl;
+  if ((threadIdx.x & 63) == 63) s.slots[wave] = v;
   __syncthreads();
-  T before = 0;
+  u64 before = 0;
 #pragma unroll
-  for (int i = 0; i < kWaves; ++i) before += i < (int)(threadIdx.x >> 6) ? (T)slots[i] : (T)0;
-  return before + incl;
+  for (int i = 0; i < kWaves; ++i) before += i < wave ? s.slots[i] : 0;
+  return before + v;
 }
 
 // Running sums over the bins, in place: thread i owns bins 2 i and 2 i + 1.
-template <typename T>
-__device__ __forceinline__ void scan_bins(T* bins, u64* slots) {
-  const T a = bins[2 * threadIdx.x], b = bins[2 * threadIdx.x + 1];
-  const T incl = scan_block<T>(a + b, slots);
+__device__ MISA_ONCE void scan_bins(int which) {
+  u64* bins = bins_of(which);
+  __syncthreads();
+  const u64 a = bins[2 * threadIdx.x], b = bins[2 * threadIdx.x + 1];
+  const u64 incl = scan_block(a + b);
   bins[2 * threadIdx.x] = incl - b;
   bins[2 * threadIdx.x + 1] = incl;
   __syncthreads();
 }
 
 // First bin whose running sum is at least `target` (kBins: none).
-template <typename T>
-__device__ __forceinline__ int first_bin(const T* bins, T target, uint32_t* out) {
+__device__ MISA_ONCE int first_bin(int which, u64 target) {
+  Shared& s = lds();
+  const u64* bins = bins_of(which);
+  const u64 z = threadIdx.x ? bins[2 * threadIdx.x - 1] : 0, a = bins[2 * threadIdx.x], b = bins[2 * threadIdx.x + 1];
+  if (bins[kBins - 1] < target) return kBins;
+  if (z < target && b >= target) s.n = 2 * threadIdx.x + (a < target);
   __syncthreads();
-  if (threadIdx.x == 0) *out = kBins;
+  const int bin = __builtin_amdgcn_readfirstlane((int)s.n);
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int b = 2 * threadIdx.x + j;
-    if (bins[b] >= target && (b == 0 || bins[b - 1] < target)) *out = b;
-  }
-  __syncthreads();
-  return (int)*out;
+  return bin;
 }
+
+__device__ __forceinline__ u64 upto(int which, int bin) { return bin > 0 ? bins_of(which)[bin - 1] : 0; }
 
 __device__ __forceinline__ u64 share_of(double share, u64 total) {     // least sum that is `share` of the total
   const double x = __builtin_ceil(share * (double)total);
   return x < 1.0 ? 1 : (x >= (double)total ? total : (u64)x);
 }
 
-// The list, descending, padded with zeros to a power of two.
-__device__ __forceinline__ void sort_list(u64* list, int n) {
-  int m = 64;
-  while (m < n) m <<= 1;
-  for (int i = n + (int)threadIdx.x; i < m; i += kThreads) list[i] = 0;
+__device__ MISA_ONCE void clear_bins() {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < 2 * kBins; i += kThreads) lds().bins[0][i] = 0;
+}
+
+__device__ __forceinline__ bool in_bins(const Row& r, float l, int b0, int b1) {
+  const float d = depth_of(r, l);
+  return d >= (float)b0 && d < (float)(b1 + 1);
+}
+
+// Of the n listed tokens of bins [b0, b1] with an order in [lo, hi]: least and largest order in
+// found[0] and [1], their number is returned.
+__device__ MISA_ONCE uint32_t range_of(int n, int b0, int b1, u64 lo, u64 hi) {
+  Shared& s = lds();
+  const Row r = s.row;
   __syncthreads();
-  for (int k = 2; k <= m; k <<= 1)
-    for (int j = k >> 1; j; j >>= 1) {
-      for (int i = threadIdx.x; i < m / 2; i += kThreads) {
-        const int lo = ((i & ~(j - 1)) << 1) | (i & (j - 1)), hi = lo | j;
-        const u64 x = list[lo], y = list[hi];
-        if ((x < y) == ((lo & k) == 0)) {
-          list[lo] = y;
-          list[hi] = x;
-        }
-      }
-      __syncthreads();
+  if (threadIdx.x == 0) {
+    s.found[0] = ~0ull;
+    s.found[1] = 0;
+    s.n = 0;
+  }
+  __syncthreads();
+  u64 least = ~0ull, most = 0;
+  uint32_t here = 0;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const u64 o = s.list[i];
+    if (o >= lo && o <= hi && in_bins(r, logit_of_order(o), b0, b1)) {
+      least = min(least, o);
+      most = max(most, o);
+      ++here;
     }
+  }
+  if (__ballot(here != 0)) {
+    least = ~scan_wave(0, ~least, [](u64 x, u64 y) { return max(x, y); });
+    most = scan_wave(0, most, [](u64 x, u64 y) { return max(x, y); });
+    here = (uint32_t)scan_wave(0, here, [](u64 x, u64 y) { return x + y; });
+    if ((threadIdx.x & 63) == 63) {
+      atomicMin(&s.found[0], least);
+      atomicMax(&s.found[1], most);
+      atomicAdd(&s.n, here);
+    }
+  }
+  __syncthreads();
+  const uint32_t all = __builtin_amdgcn_readfirstlane(s.n);
+  __syncthreads();
+  return all;
+}
+
+__device__ __forceinline__ u64 lane_of(u64 v, int lane) {
+  return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, lane);
+}
+
+// The cut among the n listed tokens of bins [b0, b1]: the one, in the order, at which the
+// running count (or sum of weights), which starts at `base`, reaches `target`. found[2]
+// gets the running sum of weights there, from `sum` before those bins. The range of the tokens
+// in question is divided into 2048 equal parts, until at most 64 are left: once where
+// logits differ, twice where ids decide.
+__device__ MISA_ONCE u64 cut_list(int n, int b0, int b1, int by, u64 base, u64 target, u64 sum) {
+  Shared& s = lds();
+  const Row r = s.row;
+  uint32_t here = range_of(n, b0, b1, 0, ~0ull);
+  u64 least = s.found[0], most = s.found[1];
+  while (here > 64) {
+    clear_bins();
+    const int shift = max(0, 53 - __builtin_clzll(most - least));    // 2048 parts at most
+    __syncthreads();
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const u64 o = s.list[i];
+      if (o >= least && o <= most) {
+        const int part = (int)((most - o) >> shift);
+        atomicAdd(&s.bins[kCount][part], (u64)1);
+        atomicAdd(&s.bins[kMass][part], weight(r, logit_of_order(o)));
+      }
+    }
+    scan_bins(kCount);
+    scan_bins(kMass);
+    const int part = min(first_bin(by, target - base), kBins - 1);
+    base += upto(by, part);
+    sum += upto(kMass, part);
+    const u64 hi = most - ((u64)part << shift), width = (u64)1 << shift;
+    here = range_of(n, b0, b1, hi - least >= width ? hi - width + 1 : least, hi);
+    least = s.found[0];
+    most = s.found[1];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.n = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const u64 o = s.list[i];
+    if (o >= least && o <= most) s.near[atomicAdd(&s.n, 1u)] = o;
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {       // each lane sums what lies at or before its token
+    const u64 mine = threadIdx.x < here ? s.near[threadIdx.x] : 0;
+    const u64 w = weight(r, logit_of_order(mine));
+    u64 c = 0, m = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; i < here; ++i) {
+      const u64 other = lane_of(mine, (int)i), v = lane_of(w, (int)i);
+      if (other >= mine) {
+        ++c;
+        m += v;
+      }
+    }
+    const u64 at = base + (by == kMass ? m : c);
+    if (mine && at >= target && at - (by == kMass ? w : 1) < target) {
+      s.found[0] = mine;
+      s.found[2] = sum + m;
+    }
+  }
+  __syncthreads();
+  return s.found[0];
 }
 
 template <int TYPE>
 struct Sampler {
+  const SampleArgs& a;
+  int64_t row;
+  int g0, g1;               // segments of this workgroup
   Row r;
-  Shared& s;
-  int nseg;
 
-  // f(token, logit) for all tokens of a segment that a wave takes; 8 neighbours a lane
+  __device__ __forceinline__ Sampler(const SampleArgs& a_, int64_t row_, int part, int parts) : a(a_), row(row_) {
+    const int nseg = (a.V + kSeg - 1) / kSeg, per = (nseg + parts - 1) / parts;
+    g0 = min(part * per, nseg);
+    g1 = min(g0 + per, nseg);
+    r.logits = static_cast<const char*>(a.logits) + row * a.row_stride * (TYPE == 3 ? 4 : 2);
+    r.V = a.V;
+    r.inf = false;
+  }
+
+  __device__ __forceinline__ static float load1(const Row& r, int i) {
+    return TYPE == 3 ? static_cast<const float*>(r.logits)[i] : logit_of<TYPE>(static_cast<const uint16_t*>(r.logits)[i]);
+  }
+
+  // f(segment, token, logits as logit() has them) for 8 neighbouring tokens a lane, a segment a wave; the next
+  // segment on its way
   template <typename F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int g = threadIdx.x >> 6; g < nseg; g += kWaves) {
-      const int i = g * kSeg + 8 * (threadIdx.x & 63);
-      float l[8];
-      load8<TYPE>(r.logits, i, r.V, l);
-      f(g, i, l);
+  __device__ __forceinline__ static void each(const Row& r, int from, int to, F f) {
+    const int lane8 = 8 * (threadIdx.x & 63), full = min(to, r.V / kSeg);
+    int g = from + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    float l[8];
+    Raw<TYPE> now, next;
+    if (g < full) now.load(r.logits, g * kSeg + lane8);
+    for (; g < to; g += kWaves) {
+      if (g < full) {
+        next.load(r.logits, min(g + kWaves, full - 1) * kSeg + lane8);
+        now.get(l);
+        now = next;
+      } else {                        // the last segment of the row; -inf behind its end
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int i = g * kSeg + lane8 + j;
+          const float x = load1(r, min(i, r.V - 1));
+          l[j] = i < r.V ? x : -__builtin_inff();
+        }
+      }
+      if (r.inf) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) l[j] = logit(r, l[j]);
+      }
+      f(g, g * kSeg + lane8, l);
     }
   }
 
-  // The cut among the tokens of bins [b0, b1], found digit by digit: the token at which
-  // the running count (or sum of weights), which starts at `base`, reaches `target`.
-  __device__ u64 descend(int b0, int b1, bool by_mass, u64 base, u64 target) {
-    u64 prefix = 0;
-    for (int shift = 44; shift >= 0; shift -= 11) {       // 5 digits of 11 bits: 32 + 20 bits and a little
-      for (int i = threadIdx.x; i < kBins; i += kThreads) s.list[i] = 0;
-      __syncthreads();
-      each([&](int, int i, const float* l) {
+  // The largest logit of this workgroup's segments (-inf: none; NaN is passed over).
+  __device__ __forceinline__ float find_top() {
+    float top = -__builtin_inff();
+    each(r, g0, g1, [&](int, int, const float* l) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, l[j]);
+    });
+#pragma unroll
+    for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    Shared& s = lds();
+    if ((threadIdx.x & 63) == 0) s.slots[threadIdx.x >> 6] = __float_as_uint(top);
+    __syncthreads();
+    top = __uint_as_float((uint32_t)s.slots[threadIdx.x & (kWaves - 1)]);
+#pragma unroll
+    for (int off = kWaves / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+    __syncthreads();
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top)));
+  }
+
+  // What the row asks for. false: there is nothing to choose, and the token is written if
+  // this workgroup is to.
+  __device__ __forceinline__ bool set_up(float top, bool writes) {
+    const float temperature = a.temperature ? a.temperature[row] : 1.f;
+    if (top == -__builtin_inff() || !(temperature > 0.f)) {
+      if (writes) {             // the first of the largest logits, or -1
+        Shared& s = lds();
+        if (threadIdx.x == 0) s.n = 0xffffffffu;
+        __syncthreads();
+        if (top != -__builtin_inff()) {
+#pragma unroll 1
+          for (int i = threadIdx.x; i < r.V; i += kThreads)
+            if (load1(r, i) == top) {
+              atomicMin(&s.n, (uint32_t)i);
+              break;
+            }
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          a.token[row] = (int)s.n;
+          if (a.logprob) a.logprob[row] = s.n == 0xffffffffu ? -__builtin_inff() : 0.f;
+        }
+      }
+      return false;
+    }
+    r.inf = top == __builtin_inff();
+    r.top = r.inf ? 0.f : top;
+    r.half = 0.5f * r.top;
+    r.fine = fminf(128.f / temperature, 3e38f);
+    r.inv = 1.4426950408889634 / (double)temperature;
+    const float min_p = a.min_p ? a.min_p[row] : 0.f;
+    r.min_w = min_p > 0.f ? (double)fminf(min_p, 1.f) * (double)(1ull << kOne) : 0.0;
+    const int k = a.top_k ? a.top_k[row] : 0;
+    r.top_k = k > 0 && k < r.V ? k : 0;
+    const float p = a.top_p ? a.top_p[row] : 1.f;
+    r.by_sum = p < 1.f;
+    r.share = p > 0.f ? (double)p : 0.0;
+    if (threadIdx.x == 0) lds().row = r;
+    return true;
+  }
+
+  // The histogram of this workgroup's segments.
+  __device__ __forceinline__ void fill_bins() {
+    Shared& s = lds();
+    clear_bins();
+    __syncthreads();
+    each(r, g0, g1, [&](int, int, const float* l) __attribute__((always_inline)) {
+      float d[8];
+      u64 w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = depth_of(r, l[j]);
+      if (r.top_k) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (d[j] < (float)kBins) atomicAdd(&s.bins[kCount][(int)d[j]], (u64)1);
+      }
+      if (r.by_sum) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = weight(r, l[j]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (d[j] < (float)kBins) atomicAdd(&s.bins[kMass][(int)d[j]], w[j]);
+      }
+    });
+  }
+
+  int bk, p0, p1;           // the bin of the k-th token (kBins: none); the bins that may hold top-p's last one
+  // Running sums over the bins, and where the filters cut.
+  __device__ __forceinline__ void find_bins() {
+    bk = p0 = kBins;
+    p1 = -1;
+    if (r.top_k) {
+      scan_bins(kCount);
+      bk = first_bin(kCount, (u64)r.top_k);
+    }
+    if (r.by_sum) {
+      scan_bins(kMass);
+      const u64 most = upto(kMass, min(bk + 1, kBins)), least = bk < kBins ? upto(kMass, bk) : most;
+      p0 = min(bk, first_bin(kMass, share_of(r.share, max(least, (u64)1))));
+      p1 = least == most ? p0 : min(bk, first_bin(kMass, share_of(r.share, most)));
+    }
+  }
+
+  // The tokens of the bins with a cut into the list (s.n of them; those beyond kList are
+  // only counted), and the segments' sums of what lies above those bins.
+  __device__ __forceinline__ void collect() {
+    Shared& s = lds();
+    __syncthreads();
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    const float sure = (float)min(bk, p0);                   // bins below it remain whole
+    const float k0 = (float)bk, k1 = bk < kBins ? k0 + 1.f : k0, q0 = (float)p0, q1 = (float)(p1 + 1), last = fmaxf(k1, q1);
+    each(r, g0, g1, [&](int g, int i, const float* l) __attribute__((always_inline)) {
+      float d[8], least = __builtin_inff();
+      bool cut = false;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        d[j] = depth_of(r, l[j]);
+        least = fminf(least, d[j]);
+        cut |= d[j] >= sure && d[j] < last;
+      }
+      double sum = 0.0;            // whole numbers below 2^53
+      if (__ballot(least < sure)) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const double t = exponent(r, l[j]);
-          if (!(t > kLeast * 1.4426950408889634)) continue;
-          const int b = bin_of(t);
-          const u64 o = order_of(l[j], i + j);
-          if (b < b0 || b > b1 || o >> (shift + 11) != prefix) continue;
-          const u64 w = by_mass ? weight(r, t) : 1;
-          if (w) atomicAdd(&s.list[kBins - 1 - (int)(o >> shift & (kBins - 1))], w);
+          const double w = rounded(r, l[j]);
+          sum += d[j] < sure ? w : 0.0;
         }
-      });
+        sum = wave_total(sum);
+      }
+      if ((threadIdx.x & 63) == 63) s.seg[g] = (u64)sum;
+      if (__ballot(cut)) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const bool mine = (d[j] >= k0 && d[j] < k1) || (d[j] >= q0 && d[j] < q1);
+          if (__ballot(mine)) {
+            if (mine) {
+              const uint32_t at = atomicAdd(&s.n, 1u);
+              if (at < kList) s.list[at] = order_of(l[j], i + j);
+            }
+          }
+        }
+      }
+    });
+    __syncthreads();
+  }
+
+  // The last kept token's place in the order, among the n listed ones; what remains of them
+  // is added to the segments' sums.
+  __device__ __forceinline__ u64 cut_lists(int n) {
+    Shared& s = lds();
+    u64 total = r.by_sum ? s.bins[kMass][kBins - 1] : 0, cut = 0;
+    const u64 before_p = r.by_sum ? upto(kMass, p0) : 0;
+    if (bk < kBins) {
+      cut = cut_list(n, bk, bk, kCount, upto(kCount, bk), (u64)r.top_k, upto(kMass, bk));
+      total = s.found[2];
+    }
+    if (r.by_sum) cut = max(cut, cut_list(n, p0, p1, kMass, before_p, share_of(r.share, total), 0));
+#pragma unroll 1
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const u64 o = s.list[i];
+      if (o >= cut) atomicAdd(&s.seg[id_of(o) / kSeg], weight(r, logit_of_order(o)));
+    }
+    return cut;
+  }
+
+  // The cut among the tokens of bins [b0, b1] of the whole row, found digit by digit: the
+  // token at which the running count (or sum of weights), which starts at `base`, reaches
+  // `target`.
+  __device__ __forceinline__ static u64 descend(const Row& r, int b0, int b1, int by, u64 base, u64 target) {
+    Shared& s = lds();
+    u64 prefix = 0;
+#pragma unroll 1
+    for (int shift = 44; shift >= 0; shift -= 11) {       // 5 digits of 11 bits for 32 + 20 bits
       __syncthreads();
-      scan_bins<u64>(s.list, s.slots);
-      const int d = first_bin<u64>(s.list, target - base, &s.n);
-      const u64 before = d == 0 || d >= kBins ? 0 : s.list[d - 1];
+      clear_bins();
       __syncthreads();
-      base += before;
-      prefix = prefix << 11 | (u64)(kBins - 1 - min(d, kBins - 1));
+#pragma unroll 1
+      for (int i = threadIdx.x; i < r.V; i += kThreads) {
+        const float x = logit(r, load1(r, i));
+        const u64 o = order_of(x, i);
+        if (in_bins(r, x, b0, b1) && o >> (shift + 11) == prefix)
+          atomicAdd(&s.bins[by][kBins - 1 - (int)(o >> shift & (kBins - 1))], by == kMass ? weight(r, x) : (u64)1);
+      }
+      scan_bins(by);
+      const int d = min(first_bin(by, target - base), kBins - 1);
+      base += upto(by, d);
+      prefix = prefix << 11 | (u64)(kBins - 1 - d);
     }
     return prefix;
   }
 
-  // Sum of the weights of the tokens of bins [b0, b1] that lie at or before the cut.
-  __device__ u64 sum_to(int b0, int b1, u64 cut) {
+  // The segments' sums of the tokens at or before the cut, of bins from b0 on; their sum.
+  __device__ __forceinline__ static u64 sum_to(const Row& r, int b0, u64 cut) {
+    Shared& s = lds();
+    __syncthreads();
+#pragma unroll 1
+    for (int g = threadIdx.x; g < kMaxSegs; g += kThreads) s.seg[g] = 0;
+    __syncthreads();
     u64 sum = 0;
-    each([&](int, int i, const float* l) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double t = exponent(r, l[j]);
-        if (!(t > kLeast * 1.4426950408889634)) continue;
-        const int b = bin_of(t);
-        if (b >= b0 && b <= b1 && order_of(l[j], i + j) >= cut) sum += weight(r, t);
+#pragma unroll 1
+    for (int i = threadIdx.x; i < r.V; i += kThreads) {
+      const float x = logit(r, load1(r, i));
+      if (in_bins(r, x, b0, kBins - 1) && order_of(x, i) >= cut) {
+        const u64 w = weight(r, x);
+        atomicAdd(&s.seg[i / kSeg], w);
+        sum += w;
       }
-    });
-    const u64 incl = scan_block<u64>(sum, s.slots);
-    if (threadIdx.x == kThreads - 1) s.found[3] = incl;
+    }
+    const u64 incl = scan_block(sum);
     __syncthreads();
-    const u64 all = s.found[3];
+    if (threadIdx.x == kThreads - 1) s.found[2] = incl;
     __syncthreads();
-    return all;
+    return s.found[2];
+  }
+
+  // More tokens share the bins with a cut than the list holds.
+  __device__ MISA_ONCE static u64 cut_row(int bk) {
+    const Row r = lds().row;
+    u64 total = r.by_sum ? lds().bins[kMass][kBins - 1] : 0, cut = 0;
+    if (bk < kBins) {
+      const u64 upto_k = upto(kCount, bk), mass_k = upto(kMass, bk);
+      cut = descend(r, bk, bk, kCount, upto_k, (u64)r.top_k);
+      if (r.by_sum) total = mass_k + sum_to(r, bk, cut);
+    }
+    if (r.by_sum) cut = max(cut, descend(r, 0, kBins - 1, kMass, 0, share_of(r.share, total)));
+    sum_to(r, 0, cut);
+    return cut;
+  }
+
+  // The token, from the segments' sums of what remains.
+  __device__ __forceinline__ void draw(u64 cut) {
+    Shared& s = lds();
+    scan_bins(kSegments);
+    const u64 total = s.seg[kMaxSegs - 1];
+    const float u = a.u[row];
+    u64 drawn = u > 0.f ? (u64)((double)u * (double)total) : 0;
+    if (drawn >= total) drawn = total - 1;
+    const int g = first_bin(kSegments, drawn + 1), i = g * kSeg + (int)threadIdx.x;
+    const u64 before = upto(kSegments, g);
+    float x = 0.f;
+    u64 w = 0;
+    if (threadIdx.x < kSeg && i < r.V) {
+      x = logit(r, load1(r, i));
+      if (depth_of(r, x) < (float)kBins && order_of(x, i) >= cut) w = weight(r, x);
+    }
+    const u64 run = before + scan_block(w);
+    if (drawn < run && run - w <= drawn) {
+      a.token[row] = i;
+      if (a.logprob)
+        a.logprob[row] =
+            (float)(exponent(r, x) * 0.6931471805599453 - log((double)total * (1.0 / (double)(1ull << kOne))));
+    }
   }
 };
 
+// One workgroup a row.
 template <int TYPE>
 __global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a) {
-  __shared__ Shared s;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = blockIdx.x;
-  Sampler<TYPE> z{{}, s, (a.V + kSeg - 1) / kSeg};
-  Row& r = z.r;
-  r.logits = static_cast<const char*>(a.logits) + row * a.row_stride * (TYPE == 3 ? 4 : 2);
-  r.V = a.V;
-
-  // 1. the first of the largest logits
-  u64 best = 0;
-  z.each([&](int, int i, const float* l) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) best = i + j < r.V ? max(best, order_of(l[j], i + j)) : best;
-  });
-#pragma unroll
-  for (int off = 32; off; off >>= 1) best = max(best, (u64)__shfl_xor(best, off, 64));
-  if (lane == 0) s.slots[wave] = best;
-  for (int i = threadIdx.x; i < kBins; i += kThreads) {
-    s.mass[i] = 0;
-    s.count[i] = 0;
+  Shared& s = lds();
+  Sampler<TYPE> z(a, blockIdx.x, 0, 1);
+  if (!z.set_up(z.find_top(), true)) return;
+  for (int g = threadIdx.x; g < kMaxSegs; g += kThreads) s.seg[g] = 0;
+  z.bk = z.p0 = kBins;
+  z.p1 = -1;
+  if (z.r.filtered()) {
+    z.fill_bins();
+    z.find_bins();
   }
-  if (threadIdx.x == 0) s.n = 0;
+  z.collect();
+  u64 cut = 0;
+  if (z.r.filtered()) {
+    const uint32_t n = s.n;
+    cut = n <= kList ? z.cut_lists((int)n) : Sampler<TYPE>::cut_row(z.bk);
+  }
+  z.draw(cut);
+}
+
+// ---------------------------------------------------------------- several workgroups a row
+// Each takes a part of the segments. What they leave for the next launch, or for the last
+// of them to finish:
+struct Parts {
+  float* top;               // [T][parts]
+  uint32_t* listed;         // [T][parts] tokens of the bins with a cut
+  uint32_t* done;           // [T] workgroups that have finished the last launch
+  u64* seg;                 // [T][kMaxSegs]
+  u64* bins;                // [T][parts][2][kBins]
+  u64* list;                // [T][parts][kList]
+  int parts;
+};
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void top_kernel(SampleArgs a, Parts w) {
+  const int row = blockIdx.x / w.parts, part = blockIdx.x % w.parts;
+  Sampler<TYPE> z(a, row, part, w.parts);
+  const float top = z.find_top();
+  if (threadIdx.x == 0) {
+    w.top[blockIdx.x] = top;
+    if (part == 0) w.done[row] = 0;
+  }
+}
+
+__device__ __forceinline__ float top_of(const Parts& w, int row) {
+  float top = -__builtin_inff();
+  for (int i = 0; i < w.parts; ++i) top = fmaxf(top, w.top[(int64_t)row * w.parts + i]);
+  return top;
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void bins_kernel(SampleArgs a, Parts w) {
+  const int row = blockIdx.x / w.parts, part = blockIdx.x % w.parts;
+  Sampler<TYPE> z(a, row, part, w.parts);
+  if (!z.set_up(top_of(w, row), false) || !z.r.filtered()) return;
+  z.fill_bins();
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) best = max(best, s.slots[i]);
-  __syncthreads();
-  r.top = logit_of_order(best);
-  const float temperature = a.temperature ? a.temperature[row] : 1.f;
-  const bool none = best == 0 || r.top == -__builtin_inff();
-  if (none || !(temperature > 0.f)) {        // nothing to choose from, or the first largest
-    if (threadIdx.x == 0) {
-      a.token[row] = none ? -1 : id_of(best);
-      if (a.logprob) a.logprob[row] = none ? -__builtin_inff() : 0.f;
+  u64* out = w.bins + (int64_t)blockIdx.x * 2 * kBins;
+  for (int i = threadIdx.x; i < 2 * kBins; i += kThreads)
+    if (i < kBins ? z.r.top_k != 0 : z.r.by_sum) out[i] = lds().bins[0][i];
+}
+
+template <int TYPE>
+__global__ __launch_bounds__(kThreads) void draw_kernel(SampleArgs a, Parts w) {
+  Shared& s = lds();
+  const int row = blockIdx.x / w.parts, part = blockIdx.x % w.parts;
+  Sampler<TYPE> z(a, row, part, w.parts);
+  if (!z.set_up(top_of(w, row), part == 0)) return;
+  z.bk = z.p0 = kBins;
+  z.p1 = -1;
+  if (z.r.filtered()) {
+    const u64* in = w.bins + (int64_t)row * w.parts * 2 * kBins;
+    for (int i = threadIdx.x; i < 2 * kBins; i += kThreads) {
+      u64 v = 0;
+      if (i < kBins ? z.r.top_k != 0 : z.r.by_sum) {
+#pragma unroll 4
+        for (int j = 0; j < w.parts; ++j) v += in[(int64_t)j * 2 * kBins + i];
+      }
+      s.bins[0][i] = v;
     }
+    z.find_bins();
+  }
+  z.collect();
+  // hand over: sums of the segments, listed tokens, their number
+  u64* seg = w.seg + (int64_t)row * kMaxSegs;
+  u64* list = w.list + (int64_t)row * w.parts * kList;
+  const uint32_t mine = s.n;
+  for (int g = z.g0 + (int)threadIdx.x; g < z.g1; g += kThreads) store_coherent((uint64_t*)seg + g, (uint64_t)s.seg[g]);
+  for (int i = threadIdx.x; i < (int)min(mine, (uint32_t)kList); i += kThreads)
+    store_coherent((uint64_t*)list + (int64_t)part * kList + i, (uint64_t)s.list[i]);
+  if (threadIdx.x == 0) store_coherent(w.listed + blockIdx.x, mine);
+  wait_stores();
+  __syncthreads();
+  if (threadIdx.x == 0) s.n = atomic_add_coherent(w.done + row, 1u);
+  __syncthreads();
+  if (s.n + 1 != (uint32_t)w.parts) return;
+  // the last one has them all
+  const int nseg = (a.V + kSeg - 1) / kSeg;
+  for (int g = threadIdx.x; g < kMaxSegs; g += kThreads) s.seg[g] = g < nseg ? (u64)load_coherent((const uint64_t*)seg + g) : 0;
+  uint32_t n = 0;
+  for (int j = 0; j < w.parts; ++j) {
+    const uint32_t m = load_coherent(w.listed + (int64_t)row * w.parts + j);
+    if (n + m <= kList)
+      for (uint32_t i = threadIdx.x; i < m; i += kThreads)
+        s.list[n + i] = (u64)load_coherent((const uint64_t*)list + (int64_t)j * kList + i);
+    n += m;
+  }
+  __syncthreads();
+  u64 cut = 0;
+  if (z.r.filtered()) cut = n <= kList ? z.cut_lists((int)n) : Sampler<TYPE>::cut_row(z.bk);
+  z.draw(cut);
+}
+
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+// Workgroups a row: one where the rows fill the chip (64 rows of 128000 tokens with four each
+// 66 us, with one 97, with eight, whose workgroups then wait for each other, 92) or are short
+// (4 rows of 32000 tokens 29 us with one, 31 with four). A workgroup has 16 waves, and a wave
+// takes 512 tokens at a time.
+int parts_of(int64_t T, int32_t V) {
+  const int64_t room = 256 / T, most = (V + kSeg * kWaves - 1) / (kSeg * kWaves);
+  if (room < 2 || most < 8) return 1;
+  return (int)std::min<int64_t>({room, most, 32});
+}
+
+Parts carve(void* ws, int64_t T, int parts, size_t* bytes) {
+  char* p = static_cast<char*>(ws);
+  auto take = [&](size_t n) {
+    char* q = p;
+    p += round_up(n);
+    return q;
+  };
+  Parts w{};
+  w.parts = parts;
+  w.top = reinterpret_cast<float*>(take((size_t)T * parts * sizeof(float)));
+  w.listed = reinterpret_cast<uint32_t*>(take((size_t)T * parts * sizeof(uint32_t)));
+  w.done = reinterpret_cast<uint32_t*>(take((size_t)T * sizeof(uint32_t)));
+  w.seg = reinterpret_cast<u64*>(take((size_t)T * kMaxSegs * sizeof(u64)));
+  w.bins = reinterpret_cast<u64*>(take((size_t)T * parts * 2 * kBins * sizeof(u64)));
+  w.list = reinterpret_cast<u64*>(take((size_t)T * parts * kList * sizeof(u64)));
+  *bytes = (size_t)(p - static_cast<char*>(ws));
+  return w;
+}
+
+template <int TYPE>
+void launch_type(const SampleArgs& a, void* ws, hipStream_t st) {
+  const int parts = parts_of(a.T, a.V);
+  if (parts == 1) {
+    hipLaunchKernelGGL(sample_kernel<TYPE>, dim3((unsigned)a.T), dim3(kThreads), 0, st, a);
     return;
   }
-  r.inv = 1.4426950408889634 / (double)temperature;
-  const float min_p = a.min_p ? a.min_p[row] : 0.f;
-  r.min_w = min_p > 0.f ? (double)fminf(min_p, 1.f) * (double)(1ull << kOne) : 0.0;
-  const int top_k = a.top_k && a.top_k[row] > 0 && a.top_k[row] < r.V ? a.top_k[row] : 0;
-  const float top_p = a.top_p ? a.top_p[row] : 1.f;
-  const bool by_sum = top_p < 1.f;
-  const double share = top_p > 0.f ? (double)top_p : 0.0;
-
-  // 2. the histogram, and where the filters cut
-  u64 cut = 0;            // tokens at or before it remain
-  if (top_k || by_sum) {
-    z.each([&](int, int, const float* l) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const double t = exponent(r, l[j]);
-        if (!(t > kLeast * 1.4426950408889634)) continue;
-        const int b = bin_of(t);
-        if (top_k) atomicAdd(&s.count[b], 1u);
-        if (by_sum) {
-          const u64 w = weight(r, t);
-          if (w) atomicAdd(&s.mass[b], w);
-        }
-      }
-    });
-    __syncthreads();
-    int bk = kBins, p0 = kBins, p1 = -1;      // the bin of the k-th token, the bins that may hold top-p's last one
-    if (top_k) {
-      scan_bins<uint32_t>(s.count, s.slots);
-      bk = first_bin<uint32_t>(s.count, (uint32_t)top_k, &s.n);
-    }
-    if (by_sum) {
-      scan_bins<u64>(s.mass, s.slots);
-      const u64 most = s.mass[min(bk, kBins - 1)], least = bk < kBins ? (bk ? s.mass[bk - 1] : 0) : most;
-      p0 = first_bin<u64>(s.mass, share_of(share, max(least, (u64)1)), &s.n);
-      p1 = first_bin<u64>(s.mass, share_of(share, most), &s.n);
-      p0 = min(p0, bk);
-      p1 = min(p1, bk);
-    }
-    if (bk < kBins || by_sum) {
-      __syncthreads();
-      if (threadIdx.x == 0) s.n = 0;
-      __syncthreads();
-      z.each([&](int, int i, const float* l) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const double t = exponent(r, l[j]);
-          if (!(t > kLeast * 1.4426950408889634)) continue;
-          const int b = bin_of(t);
-          if (b == bk || (b >= p0 && b <= p1)) {
-            const uint32_t at = atomicAdd(&s.n, 1u);
-            if (at < kList) s.list[at] = order_of(l[j], i + j);
-          }
-        }
-      });
-      __syncthreads();
-      const uint32_t n = s.n;
-      __syncthreads();
-      const u64 upto_k = bk < kBins && bk ? s.count[bk - 1] : 0;
-      const u64 mass_k = bk < kBins && bk ? s.mass[bk - 1] : 0;
-      u64 total = by_sum ? s.mass[kBins - 1] : 0;
-      if (n <= kList) {
-        sort_list(s.list, (int)n);
-        // four tokens a thread, in order: those of a bin stand next to each other
-        u64 o[4], w[4];
-        int bin[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = 4 * (int)threadIdx.x + j;
-          o[j] = i < (int)n ? s.list[i] : 0;
-          const double t = exponent(r, logit_of_order(o[j]));
-          bin[j] = i < (int)n ? bin_of(t) : -1;
-          w[j] = i < (int)n && by_sum ? weight(r, t) : 0;
-        }
-        if (threadIdx.x < 3) s.found[threadIdx.x] = 0;
-        if (bk < kBins) {
-          uint32_t c = 0;
-          u64 m = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            c += bin[j] == bk;
-            m += bin[j] == bk ? w[j] : 0;
-          }
-          c = scan_block<uint32_t>(c, s.slots) - c + (uint32_t)upto_k;
-          m = scan_block<u64>(m, s.slots) - m + mass_k;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (bin[j] == bk) {
-              m += w[j];
-              if (++c == (uint32_t)top_k) {
-                s.found[0] = o[j];
-                s.found[1] = m;
-              }
-            }
-          __syncthreads();
-          cut = s.found[0];
-          total = s.found[1];
-        }
-        if (by_sum) {
-          const u64 target = share_of(share, total);
-          u64 m = 0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) m += bin[j] >= p0 && bin[j] <= p1 ? w[j] : 0;
-          m = scan_block<u64>(m, s.slots) - m + (p0 ? s.mass[p0 - 1] : 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (bin[j] >= p0 && bin[j] <= p1) {
-              if (m < target && m + w[j] >= target) s.found[2] = o[j];
-              m += w[j];
-            }
-          __syncthreads();
-          cut = max(cut, s.found[2]);
-        }
-      } else {
-        if (bk < kBins) {
-          cut = z.descend(bk, bk, false, upto_k, (u64)top_k);
-          if (by_sum) total = mass_k + z.sum_to(bk, bk, cut);
-        }
-        if (by_sum) cut = max(cut, z.descend(0, kBins - 1, true, 0, share_of(share, total)));
-      }
-    }
-  }
-
-  // 3. sums of what remains in segments, the segment of the drawn token, the token
-  for (int g = threadIdx.x; g < kMaxSegs; g += kThreads) s.seg[g] = 0;
-  __syncthreads();
-  z.each([&](int g, int i, const float* l) {
-    u64 sum = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const double t = exponent(r, l[j]);
-      if (!(t > kLeast * 1.4426950408889634)) continue;
-      if (order_of(l[j], i + j) >= cut) sum += weight(r, t);
-    }
-#pragma unroll
-    for (int off = 32; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-    if (lane == 0) s.seg[g] = sum;
-  });
-  __syncthreads();
-  scan_bins<u64>(s.seg, s.slots);
-  const u64 total = s.seg[kMaxSegs - 1];
-  const float u = a.u[row];
-  u64 drawn = u > 0.f ? (u64)((double)u * (double)total) : 0;
-  if (drawn >= total) drawn = total - 1;
-  const int g = first_bin<u64>(s.seg, drawn + 1, &s.n);
-  if (wave == 0 && g < z.nseg) {
-    const u64 before = g ? s.seg[g - 1] : 0;
-    const int i = g * kSeg + 8 * lane;
-    float l[8];
-    load8<TYPE>(r.logits, i, r.V, l);
-    u64 w[8], mine = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      w[j] = order_of(l[j], i + j) >= cut ? weight(r, exponent(r, l[j])) : 0;
-      mine += w[j];
-    }
-    u64 run = before + scan_wave(mine) - mine;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (run <= drawn && drawn < run + w[j]) {
-        a.token[row] = i + j;
-        if (a.logprob)
-          a.logprob[row] = (float)(exponent(r, l[j]) * 0.6931471805599453 -
-                                   log((double)total * (1.0 / (double)(1ull << kOne))));
-      }
-      run += w[j];
-    }
-  }
+  size_t bytes;
+  const Parts w = carve(ws, a.T, parts, &bytes);
+  const dim3 grid((unsigned)(a.T * parts));
+  hipLaunchKernelGGL(top_kernel<TYPE>, grid, dim3(kThreads), 0, st, a, w);
+  if (a.top_k || a.top_p) hipLaunchKernelGGL(bins_kernel<TYPE>, grid, dim3(kThreads), 0, st, a, w);
+  hipLaunchKernelGGL(draw_kernel<TYPE>, grid, dim3(kThreads), 0, st, a, w);
 }
 
 }  // namespace
 
-hipError_t launch_sample(const SampleArgs& a, int type, hipStream_t st) {
-  const dim3 grid((unsigned)a.T), block(kThreads);
-  if (type == 1) hipLaunchKernelGGL(sample_kernel<1>, grid, block, 0, st, a);
-  else if (type == 2) hipLaunchKernelGGL(sample_kernel<2>, grid, block, 0, st, a);
-  else hipLaunchKernelGGL(sample_kernel<3>, grid, block, 0, st, a);
+size_t sample_ws_bytes(int64_t T, int32_t V) {
+  const int parts = parts_of(T, V);
+  if (parts == 1) return 0;
+  size_t bytes;
+  carve(nullptr, T, parts, &bytes);
+  return bytes;
+}
+
+hipError_t launch_sample(const SampleArgs& a, int type, void* ws, hipStream_t st) {
+  if (type == 1) launch_type<1>(a, ws, st);
+  else if (type == 2) launch_type<2>(a, ws, st);
+  else launch_type<3>(a, ws, st);
   return hipGetLastError();
 }
 
