@@ -1244,7 +1244,7 @@ size_t misa_cache_workspace_bytes(int32_t op, const misa_kv_cache* cache, int64_
   }
   if (op == MISA_OP_CACHE_EVICT) {
     if (budget < 1 || (__int128)cache->nseq * lists >= (1 << 22)) return 0;
-    return round_up((size_t)cache->nseq * lists * (size_t)(budget < L ? budget : L) * sizeof(int32_t));
+    return round_up(2 * (size_t)cache->nseq * lists * (size_t)(budget < L ? budget : L) * sizeof(int32_t));
   }
   return 0;
 }
@@ -1339,7 +1339,7 @@ int32_t misa_cache_evict(const misa_kv_cache* cache, const float* mass, const in
   a.mass_out = mass_out;
   a.pos_out = pos_out;
   a.new_len = new_len;
-  a.movers = static_cast<int32_t*>(ws);
+  a.lists = static_cast<int32_t*>(ws);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = misa::launch_evict_select(a, st);
   if (e == hipSuccess) e = misa::launch_move(b, st);

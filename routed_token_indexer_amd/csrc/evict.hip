@@ -13,53 +13,104 @@ namespace misa {
 namespace {
 
 // ---------------------------------------------------------------- selection
-constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
-constexpr int kBins = 4096;
+typedef unsigned long long u64;
 
 constexpr uint32_t kProtected = 0xffffffffu;
 
-// Rank of a token as an unsigned number; 0 stands for no token. NaN ranks above all numbers.
-__device__ __forceinline__ uint32_t rank_key(float mass, int pos, int64_t first, int64_t latest) {
-  if (pos < first || pos >= latest) return kProtected;
-  if (mass != mass) return kProtected - 1;
-  return score_key(mass);      // of no number 0 or above the NaN's
+// Rank of a token as an unsigned number; 0 stands for no token. Positions from `first` on,
+// fewer than `open` of them, are not protected. NaN ranks above all numbers.
+__device__ __forceinline__ uint32_t rank_key(float mass, int pos, int first, uint32_t open) {
+  const uint32_t u = __float_as_uint(mass + 0.f);                      // -0 becomes 0
+  uint32_t k = u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);           // of no number 0 or above the NaN's
+  k = mass != mass ? kProtected - 1 : k;
+  return (uint32_t)pos - (uint32_t)first < open ? k : kProtected;
 }
 
-__device__ __forceinline__ int wave_scan(int v) {   // inclusive
-  const int lane = threadIdx.x & 63;
+// A wave's maximum or sum, in all lanes (data-parallel moves: rows of 16 lanes, then from row
+// to row).
+template <int CTRL, int ROWS, typename Op>
+__device__ __forceinline__ uint32_t dpp_step(uint32_t none, uint32_t v, Op op) {
+  return op(v, (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)v, CTRL, ROWS, 0xf, false));
+}
+template <typename Op>
+__device__ __forceinline__ uint32_t scan_wave(uint32_t none, uint32_t v, Op op) {   // up to and with each lane
+  v = dpp_step<0x111, 0xf>(none, v, op);
+  v = dpp_step<0x112, 0xf>(none, v, op);
+  v = dpp_step<0x114, 0xf>(none, v, op);
+  v = dpp_step<0x118, 0xf>(none, v, op);
+  v = dpp_step<0x142, 0xa>(none, v, op);
+  return dpp_step<0x143, 0xc>(none, v, op);
+}
+struct Add {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
+};
+
+// Entries e .. e + 3 of an array of n; behind its end the last one. (The array starts at
+// any multiple of 4 bytes.)
+typedef u32x4 __attribute__((aligned(4))) u32x4_any;
+template <typename T>
+__device__ __forceinline__ u32x4 four(const T* p, int e, int n) {
+  if (e + 4 <= n) return *reinterpret_cast<const u32x4_any*>(p + e);
+  u32x4 v;
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int x = __shfl_up(v, off, 64);
-    if (lane >= off) v += x;
-  }
+  for (int j = 0; j < 4; ++j) v[j] = __builtin_bit_cast(uint32_t, p[min(e + j, n - 1)]);
   return v;
 }
 
-// Exclusive sum over the workgroup's waves of a value per wave; total of all in `all`.
-__device__ __forceinline__ int waves_before(int v, int* slots, int& all) {
-  const int w = threadIdx.x >> 6;
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) slots[w] = v;
-  __syncthreads();
-  int before = 0;
-  all = 0;
-#pragma unroll
-  for (int i = 0; i < kSelWaves; ++i) {
-    const int x = slots[i];
-    before += i < w ? x : 0;
-    all += x;
+// What the workgroups of a list share.
+template <int THREADS>
+struct Select {
+  static constexpr int kWaves = THREADS / 64, kBins = 4 * THREADS, kBits = THREADS == 1024 ? 12 : 11;
+  static_assert(1 << kBits == kBins);
+  uint32_t bins[kBins];          // then holes and movers
+  uint32_t slots[2][kWaves];
+  u64 near[64];
+  u64 range[2];
+  u64 cut;
+  uint32_t n, part, above;
+
+  __device__ __forceinline__ static uint32_t last_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
   }
-  return before;
-}
+  // A value per wave: the sum over the waves before, and over all.
+  __device__ __forceinline__ uint32_t before(int which, uint32_t v, uint32_t& all) {
+    const int w = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) slots[which][w] = v;
+    __syncthreads();
+    uint32_t b = 0;
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      const uint32_t x = slots[which][i];
+      b += i < w ? x : 0;
+      all += x;
+    }
+    return b;
+  }
+};
 
 // One workgroup a list. Wave w owns the rows [w C, (w + 1) C), 64 at a time, so that
-// numbers in row order need one sum over the waves. N > 0: at most N runs of 64 rows a
-// wave, whose keys stay in registers; 0: any length, keys read again for each sweep.
-template <int N>
-__global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
-  __shared__ uint32_t hist[kBins];
-  __shared__ int slots[kSelWaves];
-  __shared__ int found[2];
+// numbers in row order need one sum over the waves. CAP > 0: at most CAP rows, whose keys
+// stay in LDS (in registers the sweeps had to be unrolled, and their code took longer to
+// arrive than to run); 0: any length, keys read again for each sweep.
+//
+// A token's place in the order is its key, then its row from behind: one 64-bit number.
+// The last kept one is found by dividing the range of the numbers in question into equal
+// parts and counting, until at most 64 are left: once where masses differ, twice where rows
+// decide.
+//
+// Bound by latency: one CU a list, and a list is read once. Of 4 lists of 32768 rows to 2048
+// (30 us; a MB read): latest position 2, keys 6, the division 8, last candidates 3.5, counts
+// and lists of moves 9, writes 5.5. Of 512 lists of 2112 rows (9 us): 2, 1, 2.5, 0.6, 1, 2.
+template <int THREADS, int CAP>
+__global__ __launch_bounds__(THREADS) void select_kernel(EvictArgs a) {
+  using S = Select<THREADS>;
+  constexpr int kBatch = 8;       // rows on their way a lane
+  __shared__ S s;
+  __shared__ __align__(16) uint32_t kept[CAP > 0 ? CAP : 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t list = blockIdx.x;
   const int64_t n = list / a.G;
@@ -69,149 +120,244 @@ __global__ __launch_bounds__(kSelThreads) void select_kernel(EvictArgs a) {
   const float* mass = a.mass + list * Lmax;
   const int32_t* pos = a.pos ? a.pos + list * Lmax : nullptr;
   int32_t* src = a.src + list * a.budget;
-  int32_t* movers = a.movers + list * min(a.budget, a.kv.Lmax);
-  const int runs = (len + kSelThreads - 1) / kSelThreads;   // of 64 rows, per wave
+  const int runs = (len + THREADS - 1) / THREADS;   // of 64 rows, per wave
   const int base = wave * runs * 64 + lane;
-
   // the latest position
   int newest = len - 1;
-  if (pos) {
-    newest = (int)0x80000000;
-    for (int i = 0; i < runs; ++i) {
-      const int e = base + 64 * i;
-      if (e < len) newest = max(newest, pos[e]);
-    }
+  if (pos && a.recent > 0) {
+    uint32_t top = 0;             // positions as unsigned numbers in the same order
+#pragma unroll 4
+    for (int e = 4 * (int)threadIdx.x; e < len; e += 4 * THREADS) {
+      const u32x4 p = four(pos, e, len);
 #pragma unroll
-    for (int off = 32; off; off >>= 1) newest = max(newest, __shfl_xor(newest, off, 64));
-    if (lane == 0) slots[wave] = newest;
+      for (int j = 0; j < 4; ++j) top = max(top, p[j] ^ 0x80000000u);
+    }
+    top = S::last_lane(scan_wave(0, top, Max()));
+    if (lane == 0) s.slots[0][wave] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kSelWaves; ++i) newest = max(newest, slots[i]);
+    for (int i = 0; i < S::kWaves; ++i) top = max(top, s.slots[0][i]);
+    newest = (int)(top ^ 0x80000000u);
+    __syncthreads();
   }
-  const int64_t first = a.sinks, latest = newest - a.recent + 1;
+  // open positions: from `sinks` up to the latest ones
+  const int first = (int)a.sinks;
+  const int64_t latest = a.recent > 0 ? newest - a.recent + 1 : (int64_t)1 << 31;
+  const uint32_t open = (uint32_t)max(latest - first, (int64_t)0);
 
-  uint32_t keys[N > 0 ? N : 1];
-  auto load = [&](int e) { return e < len ? rank_key(mass[e], pos ? pos[e] : e, first, latest) : 0u; };
-  if constexpr (N > 0) {
+  // keys of the wave's runs i0 .. i0 + 7 (no branch between the loads)
+  auto load = [&](int i0, uint32_t (&k)[kBatch]) __attribute__((always_inline)) {
+    float m[kBatch];
+    int p[kBatch];
 #pragma unroll
-    for (int i = 0; i < N; ++i) keys[i] = i < runs ? load(base + 64 * i) : 0u;
-  }
-  // f(row, key) for the wave's rows in order
-  auto sweep = [&](auto f) {
-    if constexpr (N > 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < runs) f(base + 64 * i, keys[i]);
-    } else {
-      for (int i = 0; i < runs; ++i) f(base + 64 * i, load(base + 64 * i));
+    for (int j = 0; j < kBatch; ++j) {
+      const int e = min(base + 64 * (i0 + j), len - 1);
+      m[j] = mass[e];
+      p[j] = pos ? pos[e] : e;
     }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      k[j] = i0 + j < runs && base + 64 * (i0 + j) < len ? rank_key(m[j], p[j], first, open) : 0u;
   };
-
-  // the key of the last kept token, and how many of its equals are kept
-  uint32_t least = 1;
-  int equals = 0x7fffffff;
-  if (len > size) {
-    int want = size;
-    uint32_t prefix = 0;
-    bool done = false;
+  // the protected ones, and the range of the others
+  uint32_t safe = 0, low = ~0u, high = 0;
+  auto note = [&](uint32_t k) __attribute__((always_inline)) {
+    safe += k == kProtected;
+    low = min(low, k - 1);        // of no token: the largest number
+    high = max(high, k + 1);      // of a protected one: 0
+  };
+  if constexpr (CAP > 0) {
+#pragma unroll 4
+    for (int e = 4 * (int)threadIdx.x; e < len; e += 4 * THREADS) {
+      const u32x4 m = four(mass, e, len), p = pos ? four(pos, e, len) : u32x4{};
+      u32x4 k;
 #pragma unroll
-    for (int step = 0; step < 3; ++step) {
-      const int shift = step == 0 ? 20 : (step == 1 ? 8 : 0), bits = step == 2 ? 8 : 12;
-      if (!done) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        sweep([&](int, uint32_t k) {
-          if (k && (step == 0 || k >> (shift + bits) == prefix)) atomicAdd(&hist[k >> shift & ((1u << bits) - 1)], 1u);
-        });
-        __syncthreads();
-        // from the highest bin down: thread i owns bins 4095 - 4 i .. 4092 - 4 i
-        int c[4], mine = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          c[j] = (int)hist[kBins - 1 - 4 * (int)threadIdx.x - j];
-          mine += c[j];
-        }
-        const int incl = wave_scan(mine);
-        int all;
-        int above = waves_before(__shfl(incl, 63, 64), slots, all) + incl - mine;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (above < want && above + c[j] >= want) {
-            found[0] = kBins - 1 - 4 * (int)threadIdx.x - j;
-            found[1] = want - above == c[j] ? -c[j] : want - above;
-          }
-          above += c[j];
-        }
-        __syncthreads();
-        prefix = prefix << bits | (uint32_t)found[0];
-        if (found[1] < 0) {        // the whole bin stays
-          done = true;
-          least = prefix << shift;
-        } else {
-          want = found[1];
-          least = prefix;
-          equals = want;
-        }
+      for (int j = 0; j < 4; ++j) {
+        k[j] = e + j < len ? rank_key(__uint_as_float(m[j]), pos ? (int)p[j] : e + j, first, open) : 0u;
+        note(k[j]);
       }
+      *reinterpret_cast<u32x4*>(kept + e) = k;
     }
-    if (done) equals = 0x7fffffff;
-    if (least == 0) least = 1;
-  }
-
-  // number of equals before the wave's rows
-  int seen = 0;
-  if (equals != 0x7fffffff) {
-    int ties = 0;
-    sweep([&](int, uint32_t k) { ties += __popcll(__ballot(k == least)); });
-    int all;
-    seen = waves_before(ties, slots, all);
-  }
-  const int seen0 = seen;
-  auto stays = [&](uint32_t k) {
-    bool s = k >= least;
-    if (equals != 0x7fffffff) {
-      const uint64_t m = __ballot(k == least);
-      if (k == least) s = seen + (int)lanes_below(m) < equals;
-      seen += __popcll(m);
+    for (int e = len + (int)threadIdx.x; e < min(runs * THREADS, CAP); e += THREADS)
+      if (e >= (len + 3) / 4 * 4) kept[e] = 0;
+    __syncthreads();
+  } else {
+    for (int i0 = 0; i0 < runs; i0 += kBatch) {
+      uint32_t k[kBatch];
+      load(i0, k);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) note(k[j]);
     }
-    return s;
+  }
+  // f(row, key) for the wave's runs in order
+  auto sweep = [&](auto f) __attribute__((always_inline)) {
+    for (int i0 = 0; i0 < runs; i0 += kBatch) {
+      uint32_t k[kBatch];
+      if constexpr (CAP > 0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) k[j] = kept[base + 64 * min(i0 + j, runs - 1)];
+      } else {
+        load(i0, k);
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (i0 + j < runs) f(base + 64 * (i0 + j), k[j]);
+    }
   };
-  int holes = 0, moves = 0;
-  sweep([&](int e, uint32_t k) {
-    const bool s = stays(k);
-    holes += __popcll(__ballot(!s && e < size));
-    moves += __popcll(__ballot(s && e >= size));
+  auto order = [](int e, uint32_t k) __attribute__((always_inline)) { return (u64)k << 32 | (uint32_t)~e; };
+
+  u64 cut = (u64)1 << 32;      // the last kept token's number: any token's
+  if (len > size) {
+    safe = S::last_lane(scan_wave(0, safe, Add()));
+    low = ~S::last_lane(scan_wave(0, ~low, Max()));
+    high = S::last_lane(scan_wave(0, high, Max()));
+    if (threadIdx.x == 0) {
+      s.range[0] = ~0ull;
+      s.range[1] = 0;
+    }
+    uint32_t all_safe;
+    s.before(0, safe, all_safe);
+    if (lane == 0) {              // a wave without tokens has low = 2^32 - 1, one of protected ones high = 0
+      if (low < kProtected - 1) atomicMin(&s.range[0], (u64)(low + 1));
+      if (high > 1) atomicMax(&s.range[1], (u64)(high - 1));
+    }
+    __syncthreads();
+    u64 lo = s.range[0] << 32, hi = s.range[1] << 32 | 0xffffffffu;
+    bool whole = true;                        // all rows of the keys from lo to hi
+    int want = size - (int)all_safe;          // of those in question
+    uint32_t here = (uint32_t)len - all_safe;
+    if (want <= 0) {                          // there is no room for all protected ones: the first rows stay
+      lo = (u64)kProtected << 32;
+      hi = ~0ull;
+      want = size;
+      here = all_safe;
+    }
+    while (here > 64) {
+      const int shift = max(0, 64 - __builtin_clzll(hi - lo) - S::kBits);   // kBins parts at most
+      for (int i = threadIdx.x; i < S::kBins; i += THREADS) s.bins[i] = 0;
+      __syncthreads();
+      if (whole && shift >= 32) {             // parts of whole keys
+        const uint32_t k0 = (uint32_t)(lo >> 32), k1 = (uint32_t)(hi >> 32);
+        sweep([&](int, uint32_t k) __attribute__((always_inline)) {
+          if (k >= k0 && k <= k1) atomicAdd(&s.bins[(k1 - k) >> (shift - 32)], 1u);
+        });
+      } else {
+        sweep([&](int e, uint32_t k) __attribute__((always_inline)) {
+          const u64 o = order(e, k);
+          if (o >= lo && o <= hi) atomicAdd(&s.bins[(int)((hi - o) >> shift)], 1u);
+        });
+      }
+      __syncthreads();
+      // from the highest part down: thread i owns four
+      uint32_t c[4], mine = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        c[j] = s.bins[4 * threadIdx.x + j];
+        mine += c[j];
+      }
+      const uint32_t incl = scan_wave(0, mine, Add());
+      uint32_t all;
+      uint32_t above = s.before(1, S::last_lane(incl), all) + incl - mine;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (above < (uint32_t)want && above + c[j] >= (uint32_t)want) {
+          s.part = 4 * threadIdx.x + j;
+          s.above = above;
+          s.n = c[j];
+        }
+        above += c[j];
+      }
+      __syncthreads();
+      hi -= (u64)s.part << shift;
+      const u64 width = (u64)1 << shift;
+      lo = hi - lo >= width ? hi - width + 1 : lo;
+      whole &= shift >= 32;
+      want -= (int)s.above;
+      here = s.n;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    const uint32_t k0 = (uint32_t)(lo >> 32), k1 = (uint32_t)(hi >> 32);
+    sweep([&](int e, uint32_t k) __attribute__((always_inline)) {
+      if (k >= k0 && k <= k1) {
+        const u64 o = order(e, k);
+        if (o >= lo && o <= hi) s.near[atomicAdd(&s.n, 1u)] = o;
+      }
+    });
+    __syncthreads();
+    if (threadIdx.x < 64) {
+      const u64 o = threadIdx.x < here ? s.near[threadIdx.x] : 0;
+      int rank = 0;
+      for (uint32_t i = 0; i < here; ++i) rank += s.near[i] >= o;
+      if (o && rank == want) s.cut = o;
+    }
+    __syncthreads();
+    cut = s.cut;
+  }
+  auto stays = [&](int e, uint32_t k) __attribute__((always_inline)) { return order(e, k) >= cut; };
+
+  uint32_t holes = 0, moves = 0;
+  sweep([&](int e, uint32_t k) __attribute__((always_inline)) {
+    const bool stay = stays(e, k);
+    const u64 here = __ballot(stay), front = __ballot(e < size);
+    holes += __popcll(front & ~here);
+    moves += __popcll(here & ~front);
   });
-  int all_holes, all_moves;
-  int hole = waves_before(holes, slots, all_holes);
-  int move = waves_before(moves, slots, all_moves);
-  seen = seen0;
-  sweep([&](int e, uint32_t k) {
-    const bool m = stays(k) && e >= size;
-    const uint64_t b = __ballot(m);
-    if (m) movers[move + lanes_below(b)] = e;
-    move += __popcll(b);
+  uint32_t all_holes, all_moves;
+  __syncthreads();
+  uint32_t hole = s.before(0, holes, all_holes);
+  uint32_t move = s.before(1, moves, all_moves);
+  // lists of both, in LDS where they fit
+  const bool fit = all_holes <= (uint32_t)S::kBins / 2;
+  const int64_t room = min(a.budget, a.kv.Lmax);
+  int32_t *const far_to = a.lists + 2 * list * room, *const far_from = far_to + room;
+  int32_t *const to = reinterpret_cast<int32_t*>(s.bins), *const from = to + S::kBins / 2;
+  sweep([&](int e, uint32_t k) __attribute__((always_inline)) {
+    const bool stay = stays(e, k), h = e < size && !stay, m = e >= size && stay;
+    const u64 bh = __ballot(h), bm = __ballot(m);
+    if (bh) {
+      const uint32_t i = hole + lanes_below(bh);
+      if (h && fit) to[i] = e;
+      if (h && !fit) far_to[i] = e;
+      hole += __popcll(bh);
+    }
+    if (bm) {
+      const uint32_t i = move + lanes_below(bm);
+      if (m && fit) from[i] = e;
+      if (m && !fit) far_from[i] = e;
+      move += __popcll(bm);
+    }
   });
-  __syncthreads();      // the movers are there, and every key has been read (the rows may be written in place)
-  seen = seen0;
+  __syncthreads();
+  // rows that stay, then holes; movers lie behind all of them, so that in place nothing is
+  // written that is still to be read
   float* mass_out = a.mass_out ? a.mass_out + list * Lmax : nullptr;
   int32_t* pos_out = a.pos_out ? a.pos_out + list * Lmax : nullptr;
-  auto place = [&](int e, uint32_t k) {
-    const bool h = !stays(k) && e < size;
-    const uint64_t b = __ballot(h);
-    if (e < size) {
-      const int s = h ? movers[hole + lanes_below(b)] : e;
-      src[e] = s;
-      if (mass_out) mass_out[e] = mass[s];
-      if (pos_out) pos_out[e] = pos ? pos[s] : s;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < size; e += THREADS) {
+    const float m = mass[e];
+    const int p = pos ? pos[e] : e;
+    uint32_t k;
+    if constexpr (CAP > 0) k = kept[e];
+    else k = rank_key(m, p, first, open);
+    if (stays(e, k)) {
+      src[e] = e;
+      if (mass_out) mass_out[e] = m;
+      if (pos_out) pos_out[e] = p;
     }
-    hole += __popcll(b);
-  };
-  sweep(place);     // a row whose key is read again here is written by the same thread afterwards
+  }
   __syncthreads();
-  for (int64_t i = size + (int)threadIdx.x; i < a.budget; i += kSelThreads) src[i] = -1;
-  for (int i = size + (int)threadIdx.x; i < Lmax; i += kSelThreads) {
+#pragma unroll 2
+  for (uint32_t i = threadIdx.x; i < all_holes; i += THREADS) {
+    const int e = fit ? to[i] : far_to[i], f = fit ? from[i] : far_from[i];
+    src[e] = f;
+    if (mass_out) mass_out[e] = mass[f];
+    if (pos_out) pos_out[e] = pos ? pos[f] : f;
+  }
+  __syncthreads();
+  for (int64_t i = size + (int)threadIdx.x; i < a.budget; i += THREADS) src[i] = -1;
+  for (int i = size + (int)threadIdx.x; i < Lmax; i += THREADS) {
     if (mass_out) mass_out[i] = 0.f;
     if (pos_out) pos_out[i] = -1;
   }
@@ -255,41 +401,43 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(MoveArgs a, int chun
     if (threadIdx.x == 0) count = __popcll(b);
   }
   __syncthreads();
-  const uint32_t pieces = (uint32_t)count * heads * units;
+  const uint32_t pieces = (uint32_t)count * heads * units, all = a.kv.v ? 2 * pieces : pieces;
   const int64_t head0 = a.G == 1 ? 0 : g * a.kv.head_stride;
-#pragma unroll 1
-  for (int tensor = 0; tensor < (a.kv.v ? 2 : 1); ++tensor) {
-    uint16_t* base = (tensor ? a.kv.v : a.kv.k) + head0;
-    for (uint32_t i0 = threadIdx.x; i0 < pieces; i0 += kMoveThreads * kMoveBatch) {
-      u32x4 x[kMoveBatch];
-      uint16_t* dst[kMoveBatch];
+  uint16_t *const k = a.kv.k + head0, *const v = a.kv.v + head0;
+  for (uint32_t i0 = threadIdx.x; i0 < all; i0 += kMoveThreads * kMoveBatch) {
+    u32x4 x[kMoveBatch];
+    uint16_t* dst[kMoveBatch];
 #pragma unroll
-      for (int j = 0; j < kMoveBatch; ++j) {
-        const uint32_t i = i0 + j * kMoveThreads;
-        dst[j] = nullptr;
-        if (i >= pieces) continue;
-        const uint32_t item = fast_quot(by_units, i), u = i - item * units;
-        const uint32_t r = fast_quot(by_heads, item), h = item - r * heads;
-        const int64_t off = h * a.kv.head_stride + 8 * u;
-        x[j] = *reinterpret_cast<const u32x4*>(base + from[r] + off);
-        dst[j] = base + to[r] + off;
-      }
-#pragma unroll
-      for (int j = 0; j < kMoveBatch; ++j)
-        if (dst[j]) *reinterpret_cast<u32x4*>(dst[j]) = x[j];
+    for (int j = 0; j < kMoveBatch; ++j) {
+      const uint32_t at = i0 + j * kMoveThreads, i = at < pieces ? at : at - pieces;
+      dst[j] = nullptr;
+      if (at >= all) continue;
+      const uint32_t item = fast_quot(by_units, i), u = i - item * units;
+      const uint32_t r = fast_quot(by_heads, item), h = item - r * heads;
+      const int64_t off = h * a.kv.head_stride + 8 * u;
+      uint16_t* base = at < pieces ? k : v;
+      x[j] = *reinterpret_cast<const u32x4*>(base + from[r] + off);
+      dst[j] = base + to[r] + off;
     }
+#pragma unroll
+    for (int j = 0; j < kMoveBatch; ++j)
+      if (dst[j]) *reinterpret_cast<u32x4*>(dst[j]) = x[j];
   }
 }
 
 }  // namespace
 
 hipError_t launch_evict_select(const EvictArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.kv.nseq * a.G)), block(kSelThreads);
-  const int64_t runs = (a.kv.Lmax + kSelThreads - 1) / kSelThreads;
-  if (runs <= 4) hipLaunchKernelGGL(select_kernel<4>, grid, block, 0, st, a);
-  else if (runs <= 16) hipLaunchKernelGGL(select_kernel<16>, grid, block, 0, st, a);
-  else if (runs <= 48) hipLaunchKernelGGL(select_kernel<48>, grid, block, 0, st, a);
-  else hipLaunchKernelGGL(select_kernel<0>, grid, block, 0, st, a);
+  const dim3 grid((unsigned)(a.kv.nseq * a.G));
+  const int64_t L = a.kv.Lmax;
+  // Short lists: half the waves and a sixth of the LDS, so that several lists share a CU (512
+  // lists of 2112 rows to 2048, moves included: 19.9 us, against 21.6 with the next shape and
+  // 22.9 with keys read again). Keys in LDS as long as they fit: 4 lists of 32768 rows to 2048
+  // 43.5 us against 55.8, 512 of 30000 109 against 130; a shape for 8192 rows gained nothing
+  // (512 lists 48.0 us, 48.4 with the one for 32768).
+  if (L <= 4096) hipLaunchKernelGGL((select_kernel<512, 4096>), grid, dim3(512), 0, st, a);
+  else if (L <= 32768) hipLaunchKernelGGL((select_kernel<1024, 32768>), grid, dim3(1024), 0, st, a);
+  else hipLaunchKernelGGL((select_kernel<1024, 0>), grid, dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

@@ -47,7 +47,7 @@ struct EvictArgs {
   int32_t* pos_out;         // may be pos, or null
   int32_t* src;             // [nseq][G][budget]
   int32_t* new_len;         // [nseq]
-  int32_t* movers;          // [nseq][G][min(budget, Lmax)] workspace
+  int32_t* lists;           // [nseq][G][2][min(budget, Lmax)] workspace
 };
 hipError_t launch_evict_select(const EvictArgs& a, hipStream_t st);
 

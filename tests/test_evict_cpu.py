@@ -129,8 +129,8 @@ def test_workspaces(B):   # noqa: F811
     assert size(B.OP_ATTEND_MASS, 0, 8, 1) == 4 * 2 * 128 * 4
     # a long prompt over few keys: at most 64 parts
     assert 0 < size(B.OP_ATTEND_MASS, 1 << 20, 8, 2) <= 64 * 4 * 2 * 128 * 4
-    assert size(B.OP_CACHE_EVICT, lists=2, budget=50) == 1792          # 4 x 2 x 50 x 4, to 256
-    assert size(B.OP_CACHE_EVICT, lists=2, budget=1 << 30) == 4 * 2 * 128 * 4
+    assert size(B.OP_CACHE_EVICT, lists=2, budget=50) == 3328          # 4 x 2 x 2 x 50 x 4, to 256
+    assert size(B.OP_CACHE_EVICT, lists=2, budget=1 << 30) == 4 * 2 * 2 * 128 * 4
     assert size(99, 4, 8, 2) == 0 and size(B.OP_ATTEND_MASS, 4, 7, 2) == 0
     for T, V in ((1, 1), (4, 32000), (64, 128000), (512, 1 << 20)):
         assert B.sample_workspace_bytes(T, V) <= 64 << 20

@@ -194,3 +194,48 @@ def test_graphs_and_streams():
     torch.cuda.current_stream().wait_stream(side)
     torch.cuda.synchronize()
     assert torch.equal(got[1].cpu(), want[1]) and torch.equal(O.bits(kc), O.bits(O.move(k, want[1], t)))
+
+
+@pytest.mark.parametrize("L,budget,sinks,recent", [
+    (700, 600, 300, 290),         # few rows left to rank, waves of protected ones, waves without rows
+    (3000, 2900, 1000, 1500),
+    (3000, 300, 200, 99),
+    (9000, 8000, 4500, 3000),
+    (20000, 15000, 9000, 5900),
+    (40000, 39990, 25000, 14980),
+    (40, 20, 0, 0),
+    (520, 510, 512 - 40, 30),
+])
+@pytest.mark.parametrize("alias", [False, True])
+def test_long_protected_runs(L, budget, sinks, recent, alias):
+    g = torch.Generator().manual_seed(L)
+    k, v, t = caches(2, L, 100, 1, 8, seed=3, values=False)
+    mass = torch.rand(2, 1, t.shape[1] * 100, generator=g)
+    both(k, v, t, mass, [L, L - 5], budget, sinks=sinks, recent=recent, alias=alias)
+
+
+@pytest.mark.parametrize("L", [4096, 8192, 32768, 40000])
+def test_every_row_moves(L):
+    """Mass in the rows behind: the most moves there can be, more than workgroup memory lists; in a graph as well."""
+    g = torch.Generator().manual_seed(L)
+    k, v, t = caches(2, L, 64, 2, 8, seed=4, values=False)
+    cap = t.shape[1] * 64
+    mass = torch.rand(2, 2, cap, generator=g)
+    mass[:, :, L // 2:] += 2
+    both(k, v, t, mass, [L, L - 11], L // 2, alias=True)
+    kc, tc = on(k), on(t)
+    mc, lens = mass.cuda(), torch.tensor([L, L - 11], dtype=torch.int32, device="cuda")
+    want = O.evict(mass, None, lens, L // 2, 0, 0)
+    ws = torch.empty(M.cache_workspace_bytes(M.OP_CACHE_EVICT, kc, tc, lists=2, budget=L // 2), dtype=torch.uint8, device="cuda")
+    src, new = torch.empty(2, 2, L // 2, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.cache_evict(kc, None, mc, lens, L // 2, table=tc, ws=ws, src=src, new_len=new, mass_out=mc)
+    for _ in range(3):
+        kc.copy_(k)
+        mc.copy_(mass)
+        ws.fill_(0x5A)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(src.cpu(), want[1]) and torch.equal(new.cpu(), want[0]) and torch.equal(mc.cpu(), want[2])
+        assert torch.equal(O.bits(kc), O.bits(O.move(k, want[1], t)))
