@@ -229,3 +229,44 @@ def test_graphs_and_repeats(nq, lists):
     given = M.attend_mass(q2, kc, lse, seq, ln, table=table, mass=before, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(given, first)
+
+
+@pytest.mark.parametrize("lists", [1, 2])
+@pytest.mark.parametrize("d,nseq,nq,group", [(64, 70, 1, 4), (128, 40, 5, 3), (128, 9, 33, 2), (256, 5, 20, 4)])
+def test_many_sequences(d, nseq, nq, group, lists):
+    """Batches of uneven sequences, in order and with every sequence's queries spread over the batch."""
+    for shuffle in (None, 7):
+        b = Batch(d, "bf16", nseq, nq, 150, 16, 2 * group, 2, seed=nseq)
+        both(b, lists=lists, shuffle=shuffle, before=torch.rand(nseq, lists, b.L, generator=torch.Generator().manual_seed(1)))
+
+
+@pytest.mark.parametrize("nq", [1, 50])
+def test_rows_far_apart(nq):
+    """Queries whose rows lie more than 2^23 elements apart."""
+    b = Batch(64, "bf16", 1, nq, 100, 16, 4, 2, seed=21)
+    wide = torch.zeros(nq, (1 << 23) + 64, dtype=torch.bfloat16, device="cuda")
+    q = wide[:, :256].view(nq, 4, 64)
+    q.copy_(b.q)
+    _, (_, kc), (seq, ln), table = b.cuda()
+    _, lse = M.attend(q, kc, _like(b, kc), seq, ln, table=table, want_lse=True)
+    got = M.attend_mass(q, kc, lse, seq, ln, table=table)
+    assert torch.equal(lse, M.attend(q.contiguous(), kc, _like(b, kc), seq, ln, table=table, want_lse=True)[1])
+    O.check_mass(got, O.mass(b.q, b.kc, lse, b.seq, b.len, table=b.table), "rows far apart")
+
+
+def test_same_sums_every_time():
+    """Split queries, a shared workspace, calls on two streams: the same bits."""
+    b = Batch(128, "bf16", 2, 900, 900, 64, 8, 2, seed=22)
+    _, (q, kc), (seq, ln), table = b.cuda()
+    _, lse = M.attend(q, kc, _like(b, kc), seq, ln, table=table, want_lse=True)
+    first = M.attend_mass(q, kc, lse, seq, ln, table=table)
+    ws = torch.empty(max(256, M.cache_workspace_bytes(M.OP_ATTEND_MASS, kc, table, T=1800, Hq=8, lists=2)), dtype=torch.uint8,
+                     device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(6):
+        ws.fill_(255)
+        assert torch.equal(M.attend_mass(q, kc, lse, seq, ln, table=table, ws=ws), first)
+    got = [M.attend_mass(q, kc, lse, seq, ln, table=table, stream=streams[i % 2]) for i in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, first) for x in got)

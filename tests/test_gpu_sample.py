@@ -199,3 +199,71 @@ def test_graphs_and_streams(T, V):
     given = M.sample(x, u, top_k=k, top_p=p, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(given[0], first[0])
+
+
+# Long rows in small batches, which several workgroups share.
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("V", [57343, 65535, 65536, 65537, 131072, 262145])
+def test_few_long_rows(V, dtype):
+    T = 3
+    x = rows(T, V, dtype, V, pad=V % 3)
+    u = uniform(T, V)
+    both(x, u, p=[0.9, 0.5, 0.99], strict=dtype == "fp32")
+    both(x, u, k=[0, 50, V // 2], p=[1.0, 0.9, 1.0], m=[0.01, 0.0, 0.0], t=[0.7, 1.0, 1.3], strict=dtype == "fp32")
+    both(x[:1], u[:1], k=[4097], strict=False)
+    both(x, u, t=[0.0, 0.0, -1.0])
+
+
+@pytest.mark.parametrize("V", [65536, 100001])
+def test_few_long_rows_of_ties(V):
+    """Cuts among more equal logits than a workgroup lists."""
+    g = torch.Generator().manual_seed(V)
+    flat = torch.full((4, V), -1.5, device="cuda")
+    both(flat, [0.0, 0.3, 0.77, 0.999], k=[V // 2, 5000, 1, V], p=[0.5, 0.25, 1.0, 0.125])
+    few = (torch.randn(4, V, generator=g) * 2).round().cuda()
+    both(few, uniform(4, 5), k=[V // 3, 20000, 0, 7], p=[0.9, 1.0, 0.6, 0.5])
+    few[0], few[1, 100:], few[2, ::2] = -math.inf, -math.inf, math.nan
+    few[3, [9, V - 1]] = math.inf
+    got = both(few, [0.5, 0.5, 0.5, 0.75], p=[0.9] * 4)
+    assert int(got[0]) == -1 and int(got[1]) < 100 and int(got[2]) % 2 and int(got[3]) == V - 1
+
+
+def test_few_long_rows_in_a_graph():
+    """Two captured calls that share a workspace, one behind the other, and eager calls between the replays."""
+    V = 151643
+    x, y = rows(2, V, "bf16", 41), rows(5, V, "bf16", 42)
+    ux, uy = torch.tensor(uniform(2, 3)).cuda(), torch.tensor(uniform(5, 4)).cuda()
+    p = torch.full((5,), 0.9).cuda()
+    k = torch.tensor([50, 0, 6000, 1, 100000], dtype=torch.int32).cuda()
+    want = M.sample(x, ux, top_p=p[:2], want_logprob=True), M.sample(y, uy, top_p=p, top_k=k, want_logprob=True)
+    ws = torch.empty(max(M.sample_workspace_bytes(2, V), M.sample_workspace_bytes(5, V)), dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty_like(a), torch.empty_like(b)] for a, b in want]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        M.sample(x, ux, top_p=p[:2], token=outs[0][0], logprob=outs[0][1], ws=ws)
+        M.sample(y, uy, top_p=p, top_k=k, token=outs[1][0], logprob=outs[1][1], ws=ws)
+    for i in range(4):
+        for a, b in outs:
+            a.fill_(-7)
+            b.fill_(7)
+        ws.fill_(0x11 * i)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, (a, b) in zip(outs, want):
+            assert torch.equal(got[0], a) and torch.equal(got[1], b)
+        assert torch.equal(M.sample(y, uy, top_p=p, top_k=k)[0], want[1][0])
+
+
+def test_many_streams_at_once():
+    """Calls on two streams, each with a workspace of its own."""
+    V = 100000
+    x = [rows(3, V, "bf16", 50 + i) for i in range(4)]
+    u = torch.tensor(uniform(3, 9)).cuda()
+    want = [M.sample(t, u, want_logprob=True) for t in x]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [M.sample(x[i % 4], u, want_logprob=True, stream=streams[i % 2]) for i in range(24)]
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(got):
+        assert torch.equal(a, want[i % 4][0]) and torch.equal(b, want[i % 4][1])
