@@ -4,13 +4,13 @@
 // x_s being attention's score (scaled, capped, biased) and lse its log-sum, so the
 // keys are read once and no value at all.
 //
-// The keys are what stays: a workgroup takes 128 keys of one kv head, holds them in
-// registers as the first operand of the matrix instructions, and walks the (query,
-// head) rows that see some of them: S^T [keys x rows] = K Q^T. A lane's scores are of
-// ONE row, so the row's interval and log-sum are a lane's own, and the sum over rows is
-// an addition into one register a key; lanes are summed once, at the end. No two
-// workgroups add to the same sum and the order is fixed: results do not depend on
-// when workgroups run.
+// The keys are what stays: a workgroup takes 256 keys of one kv head (128 of d = 256; a wave
+// of its own 64, for few rows), holds them in registers as the first operand of the matrix
+// instructions, and walks the (query, head) rows that see some of them: S^T [keys x rows] =
+// K Q^T. A lane's scores are of ONE row, so the row's interval and log-sum are a lane's own,
+// and the sum over rows is an addition into one register a key; lanes are summed once, at the
+// end. No two workgroups add to the same sum and the order is fixed: results do not depend on
+// when workgroups run. Sums are fp32, scores as the attention kernels have them.
 #include "attend_kernel.hpp"
 #include "misa_evict.hpp"
 
@@ -20,6 +20,10 @@ namespace {
 using namespace attend;
 
 constexpr int kThreads = 256;
+
+// What a score goes through, as a kernel's MODE. (A branch on the cap beside the bias, taken for
+// each score, cost more than the rest of it: 83 -> 75 us for two prompts of 2000 tokens, d = 256.)
+constexpr int kCapped = 1, kBiased = 2;
 
 // What a lane knows of its row.
 struct Row {
@@ -37,7 +41,7 @@ __device__ __forceinline__ Row row_info(const MassArgs& a, int n, int64_t t, int
   const int seq = a.q_seq[t], len = a.q_len[t];
   const int start = a.q_start ? a.q_start[t] : 0;
   const float lse = a.lse[t * a.Hq + head];
-  if constexpr (MODE == kBias) {
+  if constexpr (MODE & kBiased) {
     x.pos = a.q_pos ? a.q_pos[t] : len - 1;
     x.slope2 = a.slopes ? a.slopes[head] * kLog2e : 0.f;
   }
@@ -48,46 +52,79 @@ __device__ __forceinline__ Row row_info(const MassArgs& a, int n, int64_t t, int
   return x;
 }
 
-// The same by 32-bit offsets behind query t and a head: query t + qi, head + h.
+// The same in two parts, loads alone (by 32-bit offsets behind query t and a head: query t + qi,
+// head + h; no branch, nothing looked at: what there is no array of is read from another one) and
+// the rest. A wait between them at the loads' place held every step up by a trip to memory.
+struct RawRow {
+  int seq, len, start, pos;
+  float lse, slope;
+};
 template <int MODE>
-__device__ __forceinline__ Row row_behind(const MassArgs& a, int n, int64_t t, int head, int qi, int h, bool is) {
+__device__ __forceinline__ RawRow row_behind(const MassArgs& a, int64_t t, int head, int qi, int h, bool is) {
   const int o = is ? 4 * qi : 0;
-  auto load = [&](const int32_t* p) {
-    return (int)__builtin_amdgcn_raw_buffer_load_b32(buffer_view(p + t, 0xfffffff0u), o, 0, 0);
+  auto load = [](const void* p, int o) __attribute__((always_inline)) {
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(buffer_view(p, 0xfffffff0u), o, 0, 0);
   };
-  const int seq = load(a.q_seq), len = load(a.q_len), start = a.q_start ? load(a.q_start) : 0;
-  const float lse = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(buffer_view(a.lse + t * a.Hq + head, 0xfffffff0u),
-                                                                         is ? 4 * (qi * a.Hq + h) : 0, 0, 0));
+  RawRow x;
+  x.seq = load(a.q_seq + t, o);
+  x.len = load(a.q_len + t, o);
+  x.start = load((a.q_start ? a.q_start : a.q_len) + t, o);
+  x.lse = __int_as_float(load(a.lse + t * a.Hq + head, is ? 4 * (qi * a.Hq + h) : 0));
+  if constexpr (MODE & kBiased) {
+    x.pos = load((a.q_pos ? a.q_pos : a.q_len) + t, o);
+    x.slope = __int_as_float(load(a.slopes + head, is ? 4 * h : 0));
+  }
+  return x;
+}
+template <int MODE>
+__device__ __forceinline__ Row row_of(const MassArgs& a, int n, const RawRow& r, bool is) {
   Row x;
   x.pos = 0;
   x.slope2 = 0.f;
-  if constexpr (MODE == kBias) {
-    x.pos = a.q_pos ? load(a.q_pos) : len - 1;
-    x.slope2 = a.slopes ? a.slopes[is ? head + h : 0] * kLog2e : 0.f;
+  if constexpr (MODE & kBiased) {
+    x.pos = r.pos - (a.q_pos ? 0 : 1);
+    x.slope2 = r.slope * kLog2e;
   }
-  x.lse2 = lse * kLog2e;
-  x.lo = max(start, 0);
-  x.hi = min(len, (int)a.kv.Lmax);
-  if (!is || seq != n || lse == -__builtin_inff() || x.lo >= x.hi) x.lo = x.hi = 0;
+  x.lse2 = r.lse * kLog2e;
+  x.lo = a.q_start ? max(r.start, 0) : 0;
+  x.hi = min(r.len, (int)a.kv.Lmax);
+  if (!is || r.seq != n || r.lse == -__builtin_inff() || x.lo >= x.hi) x.lo = x.hi = 0;
   return x;
 }
 
-// The queries that see some of the keys [k0, k0 + KEYS), of [t_lo, t_hi): from the
-// first to the last one. All threads of the workgroup call it.
-template <int KEYS>
-__device__ __forceinline__ void seeing(const MassArgs& a, int n, int k0, int64_t t_lo, int64_t t_hi, int64_t& t0,
-                                       int64_t& t1) {
-  __shared__ int first[kThreads / 64], last[kThreads / 64];
-  int lo = 0x7fffffff, hi = -1;
-#pragma unroll 4
-  for (int64_t t = t_lo + threadIdx.x; t < t_hi; t += kThreads) {
-    const int len = clamp_len(a.q_len[t], a.kv.Lmax);
-    const int start = a.q_start ? a.q_start[t] : 0;
-    if (a.q_seq[t] == n && start < len && len > k0 && start < k0 + KEYS) {
+// The first and the last of T queries that see some of the keys [k0, k0 + KEYS), as thread i of
+// THREADS finds them: four of them a load, 16 under way.
+typedef int32_t int32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+template <int KEYS, int THREADS>
+__device__ __forceinline__ void look(const MassArgs& a, int n, int k0, int i, int& lo, int& hi) {
+  lo = 0x7fffffff;
+  hi = -1;
+  auto one = [&](int64_t t, int seq, int len, int start) __attribute__((always_inline)) {
+    len = clamp_len(len, a.kv.Lmax);
+    if (seq == n && start < len && len > k0 && start < k0 + KEYS) {
       lo = min(lo, (int)t);
       hi = max(hi, (int)t);
     }
+  };
+#pragma unroll 4
+  for (int64_t t = 4 * i; t + 4 <= a.T; t += 4 * THREADS) {
+    const int32x4_any seq = *reinterpret_cast<const int32x4_any*>(a.q_seq + t);
+    const int32x4_any len = *reinterpret_cast<const int32x4_any*>(a.q_len + t);
+    const int32x4_any start = a.q_start ? *reinterpret_cast<const int32x4_any*>(a.q_start + t) : int32x4_any{};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) one(t + j, seq[j], len[j], start[j]);
   }
+  const int64_t t = (a.T & ~(int64_t)3) + i;
+  if (t < a.T) one(t, a.q_seq[t], a.q_len[t], a.q_start ? a.q_start[t] : 0);
+}
+
+// From the first to behind the last query that sees some of the keys [k0, k0 + KEYS). All
+// threads of the workgroup call it.
+template <int KEYS>
+__device__ __forceinline__ void seeing(const MassArgs& a, int n, int k0, int& t0, int& t1) {
+  __shared__ int first[kThreads / 64], last[kThreads / 64];
+  int lo, hi;
+  look<KEYS, kThreads>(a, n, k0, (int)threadIdx.x, lo, hi);
   lo = wave_min_of(lo);
   hi = wave_max_of(hi);
   const int w = threadIdx.x >> 6;
@@ -102,7 +139,7 @@ __device__ __forceinline__ void seeing(const MassArgs& a, int n, int k0, int64_t
     hi = max(hi, last[i]);
   }
   t0 = uniform(lo);
-  t1 = (int64_t)uniform(hi) + 1;
+  t1 = uniform(hi) + 1;
 }
 
 // Address of key s of sequence n, or null.
@@ -120,14 +157,10 @@ template <int MR, int MODE, typename Acc>
 __device__ __forceinline__ void finish_scores(Acc& s, const Row& r, int key, float c, const FarCap& cap) {
 #pragma unroll
   for (int j = 0; j < MR * MR / 64; ++j) {
-    if constexpr (MODE == kPlain) {
-      s[j] = s[j] * c - r.lse2;
-    } else {
-      const int o = MR == 32 ? 8 * (j >> 2) + (j & 3) : j;
-      float off = r.lse2;
-      if constexpr (MODE == kBias) off += r.slope2 * (float)abs(r.pos - (key + o));
-      s[j] = cap.cap2 != 0.f ? cap.chosen(s[j], off) : s[j] * c - off;
-    }
+    const int o = MR == 32 ? 8 * (j >> 2) + (j & 3) : j;
+    float off = r.lse2;
+    if constexpr (MODE & kBiased) off += r.slope2 * (float)abs(r.pos - (key + o));
+    s[j] = MODE & kCapped ? cap.chosen(s[j], off) : s[j] * c - off;
   }
 }
 
@@ -195,16 +228,8 @@ __global__ __launch_bounds__(kThreads, 2) void mass_few_kernel(MassArgs a) {
 #pragma unroll
   for (int i = 0; i < NT; ++i) p[i] = key_row(a, n, g, key0 + 16 * i + (lane & 15));
   const float before = holds && !a.part && a.in ? a.in[at] : 0.f;
-  int lo = 0x7fffffff, hi = -1;
-#pragma unroll 4
-  for (int64_t t = lane; t < a.T; t += 64) {
-    const int seq = a.q_seq[t], len = clamp_len(a.q_len[t], a.kv.Lmax);
-    const int start = a.q_start ? a.q_start[t] : 0;
-    if (seq == n && start < len && len > key0 && start < key0 + kFewKeys) {
-      lo = min(lo, (int)t);
-      hi = max(hi, (int)t);
-    }
-  }
+  int lo, hi;
+  look<kFewKeys, 64>(a, n, key0, lane, lo, hi);
   const int64_t t0 = wave_min_of(lo), t1 = (int64_t)wave_max_of(hi) + 1;
   float total = 0.f;
   if (t0 < t1) {
@@ -255,7 +280,11 @@ __global__ __launch_bounds__(kThreads, 2) void mass_few_kernel(MassArgs a) {
 
 // Many rows (prompts, windows of queries): steps of 64 (d = 256: 32) rows go through LDS,
 // the next ones under way in registers meanwhile. Each wave holds 64 (32) keys and takes
-// all rows.
+// all rows. 8192 causal tokens of 64 heads of 128 over 8 kv heads: 620 us, 0.89 PFLOP/s of the
+// products that somebody sees, beside one exponential (8 cycles a wave), one multiply-add and
+// one addition a score, which bound it with the products; a wave's products go beside the
+// weights of its 32 rows before. (128 keys a workgroup, products and weights in turn, a step's
+// intervals waited for: 1640.)
 template <int D>
 struct ManyShape {
   static constexpr int NT = D == 256 ? 1 : 2;            // tiles of 32 keys a wave
@@ -273,13 +302,20 @@ __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int lists = (int)a.kv.nseq * a.Hkv;
   // the lists next to each other (on XCDs of their own where there are eight), the first
-  // keys before later ones and the last queries before earlier ones: the most work first
+  // keys before later ones: the most work first
   const int list = blockIdx.x % lists, rest = blockIdx.x / lists;
-  const int tiles = (int)(gridDim.x / (unsigned)(lists * a.splits));
-  const int tile = rest % tiles, split = a.splits - 1 - rest / tiles;
+  const int split = rest % a.splits, tile = rest / a.splits;
   const int n = list / a.Hkv, g = list % a.Hkv, k0 = tile * S::KEYS;
-  int64_t t0, t1;
-  seeing<S::KEYS>(a, n, k0, a.T * split / a.splits, a.T * (split + 1) / a.splits, t0, t1);
+  // a step takes all heads of `per` queries, or up to ROWS heads of one query
+  const int per = a.group < ROWS ? ROWS / a.group : 1;
+  int t0, t1;                           // T is below 2^31
+  seeing<S::KEYS>(a, n, k0, t0, t1);
+  if (t0 < t1 && a.splits > 1) {        // the workgroup's part of them, in whole steps
+    const uint32_t all = (uint32_t)(t1 - t0), steps = (all + per - 1) / per;
+    const uint32_t part = (steps + a.splits - 1) / a.splits * per, from = min(part * split, all);
+    t1 = t0 + (int)min(from + part, all);
+    t0 += (int)from;
+  }
   if (t0 >= t1) {
     if (a.part || a.in != a.out) store_sums<S::KEYS>(a, n, g, split, k0, nullptr);
     return;
@@ -298,9 +334,7 @@ __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
   const float c = a.scale * kLog2e;
   const FarCap cap = a.cap != 0.f ? far_cap(a.cap, a.scale / a.cap) : FarCap{0.f, 0.f, 0.f, false};
 
-  // A step takes all heads of `per` queries, or up to ROWS heads of one query. A thread's
-  // place in a step is the same in all steps: 32-bit offsets behind a uniform base.
-  const int per = a.group < ROWS ? ROWS / a.group : 1;
+  // A thread's place in a step is the same in all steps: 32-bit offsets behind a uniform base.
   const int piece = 16 * ((int)threadIdx.x % PIECES);
   uint32_t off[NLD];
   int mark[NLD];        // query of the step, or head where a step has one query
@@ -319,20 +353,24 @@ __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
     my_h[i] = my - my_q[i] * a.group;
   }
   u32x4 next[NLD];
-  Row x[RT], row_next[RT];
-  int64_t t = t0;       // first query of the next step to fetch
+  RawRow raw[RT];
+  bool is[RT];
+  Row x[RT];
+  int t = t0;           // first query of the next step to fetch
   int h0 = 0;           // and first of its heads
   auto fetch = [&]() __attribute__((always_inline)) {
     const int head = g * a.group + h0;
-    const int left = per > 1 ? (int)min(t1 - t, (int64_t)per) : a.group - h0;
+    const int left = per > 1 ? min(t1 - t, per) : a.group - h0;
     // in the place of what lies behind the last query or head: a row that there is
-    const __amdgpu_buffer_rsrc_t q = buffer_view(a.q + t * a.q_ts + (int64_t)head * a.q_hs, 0xfffffff0u);
+    const __amdgpu_buffer_rsrc_t q = buffer_view(a.q + (int64_t)t * a.q_ts + (int64_t)head * a.q_hs, 0xfffffff0u);
 #pragma unroll
     for (int i = 0; i < NLD; ++i)
       next[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(q, (int)(mark[i] < left ? off[i] : piece), 0, 0));
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-      row_next[i] = row_behind<MODE>(a, n, t, head, my_q[i], my_h[i], (per > 1 ? my_q[i] : my_h[i]) < left && my_q[i] < per);
+    for (int i = 0; i < RT; ++i) {
+      is[i] = (per > 1 ? my_q[i] : my_h[i]) < left && my_q[i] < per;
+      raw[i] = row_behind<MODE>(a, t, head, my_q[i], my_h[i], is[i]);
+    }
     h0 += ROWS;
     if (h0 >= a.group) {
       h0 = 0;
@@ -383,9 +421,11 @@ __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
       for (int k = 0; k < NT; ++k) hide<32>(s[u][k], x, key + 32 * k);
     }
   };
+  uint32_t steps = (uint32_t)(t1 - t0);
+  steps = per > 1 ? (steps + per - 1) / per : steps * ((a.group + ROWS - 1) / ROWS);
   auto turn = [&](auto which) __attribute__((always_inline)) {        // false: that was the last step
     constexpr int b = decltype(which)::value;
-    const bool more = t < t1;
+    const bool more = --steps != 0;
     if (more) fetch();
     if constexpr (RT == 1) {
       rows32(b, b, 0, x[0]);
@@ -396,7 +436,7 @@ __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
     if (more) {
       put(b ^ 1);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) x[i] = row_next[i];
+      for (int i = 0; i < RT; ++i) x[i] = row_of<MODE>(a, n, raw[i], is[i]);
       __syncthreads();
     } else {
       add(RT == 1 ? b : 1);
@@ -406,7 +446,7 @@ __global__ __launch_bounds__(kThreads, 2) void mass_many_kernel(MassArgs a) {
   fetch();
   put(0);
 #pragma unroll
-  for (int i = 0; i < RT; ++i) x[i] = row_next[i];
+  for (int i = 0; i < RT; ++i) x[i] = row_of<MODE>(a, n, raw[i], is[i]);
   __syncthreads();
   while (turn(std::integral_constant<int, 0>{}) && turn(std::integral_constant<int, 1>{})) {
   }
@@ -457,9 +497,10 @@ void launch_mode(const MassArgs& a, unsigned blocks, hipStream_t st) {
 }
 template <bool HALF, int D>
 void launch_dim(const MassArgs& a, unsigned blocks, hipStream_t st) {
-  if (a.slopes) launch_mode<HALF, D, kBias>(a, blocks, st);
-  else if (a.cap != 0.f) launch_mode<HALF, D, kCap>(a, blocks, st);
-  else launch_mode<HALF, D, kPlain>(a, blocks, st);
+  if (a.slopes && a.cap != 0.f) launch_mode<HALF, D, kCapped | kBiased>(a, blocks, st);
+  else if (a.slopes) launch_mode<HALF, D, kBiased>(a, blocks, st);
+  else if (a.cap != 0.f) launch_mode<HALF, D, kCapped>(a, blocks, st);
+  else launch_mode<HALF, D, 0>(a, blocks, st);
 }
 template <bool HALF>
 void launch_type(const MassArgs& a, unsigned blocks, hipStream_t st) {
@@ -476,14 +517,16 @@ bool mass_few(int64_t T, int64_t nseq, int group, int64_t q_ts, int64_t q_hs) {
   return (T + nseq - 1) / nseq * group <= 16 || q_ts >= (1 << 23) || q_hs >= (1 << 23);
 }
 
-// The chip holds some 512 workgroups. One takes some 4 us before its first product, the time
-// of 512 rows. So the queries are split until there are 1024 workgroups with 128 rows of a
-// sequence each on average, or 4096 with 256 (8192 causal tokens 791 us with 2048 workgroups, 707 with
-// 4096; windows of 64 queries behind 32K keys 107 us with one range, 159 with two).
+// The chip holds some 512 workgroups. One takes some 6 us before its first product, the time
+// of a few hundred rows. So what sees a tile of keys is split until the workgroups fill the chip
+// once, with 128 rows of a sequence each and more, or four times, so that uneven ones even out,
+// with 2048 (two prompts of 2000 tokens of 7 documents, d = 256: 54 us whole, 34 with 512
+// workgroups, 40 with 1024; 8192 causal tokens: 1522 us whole, 669 with 1024, 634 with 2048, 654
+// with 4096; windows of 64 queries behind 32K keys, 2048 workgroups: 98 us whole, 124 in two).
 int mass_splits(int64_t T, int64_t nseq, int heads, int group, int64_t Lmax, int d) {
   const int64_t tiles = (Lmax + many_keys(d) - 1) / many_keys(d) * nseq * heads, rows = T * group / nseq;
   int s = 1;
-  while (s < 64 && tiles * s < 4096 && rows > (tiles * s < 1024 ? 256 : 512) * s) s *= 2;
+  while (s < 64 && ((tiles * s < 512 && rows > 256 * s) || (tiles * s < 2048 && rows > 4096 * s))) s *= 2;
   return s;
 }
 

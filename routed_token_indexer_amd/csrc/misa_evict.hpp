@@ -25,12 +25,12 @@ struct MassArgs {
   float* out;
   int32_t G;                // Hkv, or 1: summed over the heads
   bool few;                 // few rows a sequence
-  // sums of query range c of `splits` in part[c][nseq][Hkv][Lmax]; null: straight to out
+  // sums over part c of `splits` of what sees a tile of keys in part[c][nseq][Hkv][Lmax]; null: straight to out
   int32_t splits;
   float* part;
 };
 bool mass_few(int64_t T, int64_t nseq, int group, int64_t q_ts, int64_t q_hs);
-// Query ranges of a call that has more (1: not split).
+// Parts that a tile's queries are split into (1: not split), a power of two.
 int mass_splits(int64_t T, int64_t nseq, int heads, int group, int64_t Lmax, int d);
 int64_t mass_blocks(const MassArgs& a);   // workgroups (of 256 threads) of its largest launch
 hipError_t launch_mass(const MassArgs& a, bool half, hipStream_t st);
