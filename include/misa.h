@@ -513,7 +513,7 @@ MISA_API size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, i
  * What a query does not see may hold anything; tokens without a page get nothing.
  *   ws: misa_cache_workspace_bytes(MISA_OP_ATTEND_MASS, cache, T, Hq, lists, 0)
  * Errors: as misa_attend (d in {64, 128, 256}); MISA_ERR_ARG for lists neither 1 nor
- * cache->heads, T * Hq / heads of 2^31 and more, or nseq * heads * L too large for one launch.
+ * cache->heads, T * Hq / heads of 2^31 - 64 and more, or nseq * heads * L too large for one launch.
  */
 MISA_API int32_t misa_attend_mass(const misa_kv_cache* cache, const void* q, int64_t q_ts, int64_t q_hs,
                                   const float* lse, const int32_t* q_seq, const int32_t* q_start,
@@ -533,7 +533,9 @@ MISA_API int32_t misa_attend_mass(const misa_kv_cache* cache, const void* q, int
  * rows of dropped tokens below new_len take, both in ascending order, the kept rows from
  * behind. So the kept rows are in no order of position afterwards (attention over
  * [0, new_len) needs none; `pos` says which is which), few rows move, and no row that is
- * read is written. Rows from new_len on keep their contents in the cache.
+ * read is written. Rows from new_len on keep their contents in the cache. (Attention's
+ * intervals and distance bias go by row, so neither fits a cache whose rows have moved;
+ * rotations stay with the keys.)
  *   mass     fp32 [nseq][lists][L]; L = table_cols * page, or page without a table
  *   pos      int32 [nseq][lists][L] positions, or NULL: a row's number is its position
  *   lens     int32 [nseq], clamped to [0, L]

@@ -517,7 +517,7 @@ bool mass_few(int64_t T, int64_t nseq, int group, int64_t q_ts, int64_t q_hs) {
   return (T + nseq - 1) / nseq * group <= 16 || q_ts >= (1 << 23) || q_hs >= (1 << 23);
 }
 
-// The chip holds some 512 workgroups. One takes some 6 us before its first product, the time
+// The chip holds some 512 workgroups. One takes some 4 us before its first product, the time
 // of a few hundred rows. So what sees a tile of keys is split until the workgroups fill the chip
 // once, with 128 rows of a sequence each and more, or four times, so that uneven ones even out,
 // with 2048 (two prompts of 2000 tokens of 7 documents, d = 256: 54 us whole, 34 with 512
