@@ -92,45 +92,54 @@ __device__ __forceinline__ float logit(const Row& r, float l) {
 // monotonically), nothing overflows, and NaN and -inf give no number below kBins.
 __device__ __forceinline__ float depth_of(const Row& r, float l) { return __builtin_fmaf(l, -0.5f, r.half) * r.fine; }
 
-// a b + c with c in scalar registers (left to itself the compiler copies every c into
-// vector registers before it is used up there).
-__device__ __forceinline__ double fma_s(double a, double b, double c) {
-  double d;
-  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
-  return d;
-}
-
-// 2^t in units of 2^-kOne; t <= 0. 2^f of the rest |f| <= 1/2 by its Taylor polynomial of
-// degree 11 (6e-15 off).
-__device__ __forceinline__ double weight_of(double t) {
-  const double whole = t + 6755399441055744.0, f = t - (whole - 6755399441055744.0);   // 1.5 2^52: to the next integer
-  const int n = (int)__builtin_bit_cast(u64, whole);
-  double p = 4.4455382718708110e-10;            // ln(2)^k / k!
-  p = fma_s(p, f, 7.0549116208011225e-09);
-  p = fma_s(p, f, 1.0178086009239699e-07);
-  p = fma_s(p, f, 1.3215486790144309e-06);
-  p = fma_s(p, f, 1.5252733804059841e-05);
-  p = fma_s(p, f, 1.5403530393381608e-04);
-  p = fma_s(p, f, 1.3333558146428443e-03);
-  p = fma_s(p, f, 9.6181291076284770e-03);
-  p = fma_s(p, f, 5.5504108664821580e-02);
-  p = fma_s(p, f, 2.4022650695910072e-01);
-  p = fma_s(p, f, 6.9314718055994531e-01);
-  p = __builtin_fma(p, f, 1.0);
-  return p * __builtin_bit_cast(double, (u64)(uint32_t)(n + kOne + 1023) << 52);
+// 2^t in units of 2^-kOne, of two numbers t <= 0 at a time. 2^f of the rest |f| <= 1/2 is 1 + f
+// times the polynomial through (2^f - 1) / f at the zeros of a Chebyshev polynomial (degree 10
+// in all, 6e-16 off). The two run side by side, with the constants in scalar registers: left to
+// itself the compiler copies every constant into vector registers before it is used up there,
+// and does one number after the other, each step waiting for the one before.
+struct Two {
+  double a, b;
+};
+__device__ __forceinline__ Two weights_of(double t0, double t1) {
+  const double magic = 6755399441055744.0;     // 1.5 2^52: to the next integer
+  const double whole0 = t0 + magic, whole1 = t1 + magic, f0 = t0 - (whole0 - magic), f1 = t1 - (whole1 - magic);
+  double p0, p1;
+  asm("v_fma_f64 %0, %4, %2, %5\n\tv_fma_f64 %1, %4, %3, %5\n\t"
+      "v_fma_f64 %0, %0, %2, %6\n\tv_fma_f64 %1, %1, %3, %6\n\t"
+      "v_fma_f64 %0, %0, %2, %7\n\tv_fma_f64 %1, %1, %3, %7\n\t"
+      "v_fma_f64 %0, %0, %2, %8\n\tv_fma_f64 %1, %1, %3, %8\n\t"
+      "v_fma_f64 %0, %0, %2, %9\n\tv_fma_f64 %1, %1, %3, %9\n\t"
+      "v_fma_f64 %0, %0, %2, %10\n\tv_fma_f64 %1, %1, %3, %10\n\t"
+      "v_fma_f64 %0, %0, %2, %11\n\tv_fma_f64 %1, %1, %3, %11\n\t"
+      "v_fma_f64 %0, %0, %2, %12\n\tv_fma_f64 %1, %1, %3, %12\n\t"
+      "v_fma_f64 %0, %0, %2, %13\n\tv_fma_f64 %1, %1, %3, %13\n\t"
+      "v_fma_f64 %0, %0, %2, 1.0\n\tv_fma_f64 %1, %1, %3, 1.0"
+      : "=&v"(p0), "=&v"(p1)
+      : "v"(f0), "v"(f1), "v"(7.070976083807186e-09), "s"(1.0205905476607851e-07), "s"(1.3215451644483806e-06),
+        "s"(1.525267292453816e-05), "s"(0.00015403530424751012), "s"(0.0013333558200795041), "s"(0.00961812910761869),
+        "s"(0.05550410866465167), "s"(0.24022650695910075), "s"(0.6931471805599462));
+  const int n0 = (int)__builtin_bit_cast(u64, whole0), n1 = (int)__builtin_bit_cast(u64, whole1);
+  return {p0 * __builtin_bit_cast(double, (u64)(uint32_t)(n0 + kOne + 1023) << 52),
+          p1 * __builtin_bit_cast(double, (u64)(uint32_t)(n1 + kOne + 1023) << 52)};
 }
 __device__ __forceinline__ double exponent(const Row& r, float l) { return ((double)l - (double)r.top) * r.inv; }
-// The weight of a logit that is less than kBins deep, to the nearest whole number; 0 where
-// min_p drops it. As a number in fp64, and as an integer.
-__device__ __forceinline__ double rounded(const Row& r, float l) {
-  const double w = weight_of(exponent(r, l));
-  const double y = (w + 4503599627370496.0) - 4503599627370496.0;     // 2^52
-  return w < r.min_w ? 0.0 : y;
+// The weights of two logits that are less than kBins deep, to the nearest whole number; 0
+// where min_p drops them. As numbers in fp64, and as integers.
+__device__ __forceinline__ Two rounded(const Row& r, float l0, float l1) {
+  const Two w = weights_of(exponent(r, l0), exponent(r, l1));
+  const double magic = 4503599627370496.0;     // 2^52
+  const double y0 = (w.a + magic) - magic, y1 = (w.b + magic) - magic;
+  return {w.a < r.min_w ? 0.0 : y0, w.b < r.min_w ? 0.0 : y1};
+}
+__device__ __forceinline__ void weights(const Row& r, float l0, float l1, u64& y0, u64& y1) {
+  const Two w = weights_of(exponent(r, l0), exponent(r, l1));
+  y0 = w.a < r.min_w ? 0 : __builtin_bit_cast(u64, w.a + 4503599627370496.0) & 0xfffffffffffffull;
+  y1 = w.b < r.min_w ? 0 : __builtin_bit_cast(u64, w.b + 4503599627370496.0) & 0xfffffffffffffull;
 }
 __device__ __forceinline__ u64 weight(const Row& r, float l) {
-  const double w = weight_of(exponent(r, l));
-  const u64 y = __builtin_bit_cast(u64, w + 4503599627370496.0) & 0xfffffffffffffull;   // 2^52
-  return w < r.min_w ? 0 : y;
+  u64 y, same;
+  weights(r, l, l, y, same);
+  return y;
 }
 
 // Data-parallel moves within rows of 16 lanes (0x110 + n: from n lanes below) and from row to
@@ -483,7 +492,7 @@ struct Sampler {
       }
       if (r.by_sum) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = weight(r, l[j]);
+        for (int j = 0; j < 8; j += 2) weights(r, l[j], l[j + 1], w[j], w[j + 1]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           if (d[j] < (float)kBins) atomicAdd(&s.bins[kMass][(int)d[j]], w[j]);
@@ -516,36 +525,37 @@ struct Sampler {
     if (threadIdx.x == 0) s.n = 0;
     __syncthreads();
     const float sure = (float)min(bk, p0);                   // bins below it remain whole
-    const float k0 = (float)bk, k1 = bk < kBins ? k0 + 1.f : k0, q0 = (float)p0, q1 = (float)(p1 + 1), last = fmaxf(k1, q1);
+    const float k0 = (float)bk, k1 = bk < kBins ? k0 + 1.f : k0, q0 = (float)p0, q1 = (float)(p1 + 1);
     each(r, g0, g1, [&](int g, int i, const float* l) __attribute__((always_inline)) {
       float d[8], least = __builtin_inff();
-      bool cut = false;
+      uint32_t cut = 0;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         d[j] = depth_of(r, l[j]);
         least = fminf(least, d[j]);
-        cut |= d[j] >= sure && d[j] < last;
+        cut = (d[j] >= k0 && d[j] < k1) || (d[j] >= q0 && d[j] < q1) ? cut | 1u << j : cut;
       }
       double sum = 0.0;            // whole numbers below 2^53
       if (__ballot(least < sure)) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const double w = rounded(r, l[j]);
-          sum += d[j] < sure ? w : 0.0;
+        for (int j = 0; j < 8; j += 2) {
+          const Two w = rounded(r, l[j], l[j + 1]);
+          sum += (d[j] < sure ? w.a : 0.0) + (d[j + 1] < sure ? w.b : 0.0);
         }
         sum = wave_total(sum);
       }
       if ((threadIdx.x & 63) == 63) s.seg[g] = (u64)sum;
-      if (__ballot(cut)) {
+      // few of a segment's, one a lane at a time (a ballot and an atomic for each of the eight:
+      // 256 rows of 151643 tokens 127 us, like this 122; one place for a segment's, 136)
+      while (__ballot(cut != 0)) {
+        if (cut) {
+          const int j = __builtin_ctz(cut);
+          float x = l[0];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const bool mine = (d[j] >= k0 && d[j] < k1) || (d[j] >= q0 && d[j] < q1);
-          if (__ballot(mine)) {
-            if (mine) {
-              const uint32_t at = atomicAdd(&s.n, 1u);
-              if (at < kList) s.list[at] = order_of(l[j], i + j);
-            }
-          }
+          for (int q = 1; q < 8; ++q) x = q == j ? l[q] : x;
+          const uint32_t at = atomicAdd(&s.n, 1u);
+          if (at < kList) s.list[at] = order_of(x, i + j);
+          cut &= cut - 1;
         }
       }
     });
