@@ -239,3 +239,24 @@ def test_every_row_moves(L):
         torch.cuda.synchronize()
         assert torch.equal(src.cpu(), want[1]) and torch.equal(new.cpu(), want[0]) and torch.equal(mc.cpu(), want[2])
         assert torch.equal(O.bits(kc), O.bits(O.move(k, want[1], t)))
+
+
+@pytest.mark.parametrize("L,budget", [(777, 300), (5001, 1000), (33001, 2000)])
+def test_lists_that_start_anywhere(L, budget):
+    """Lists of an odd number of rows, in arrays four bytes behind a 16-byte boundary."""
+    g = torch.Generator().manual_seed(L)
+    k, _, _ = caches(2, L, L, 3, 8, seed=5, table=False, values=False)
+    mass, pos = torch.rand(2, 3, L, generator=g), torch.randperm(6 * L, generator=g).view(2, 3, L).to(torch.int32)
+
+    def shifted(x):
+        y = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+        return y.copy_(x)
+    m, p, kc = shifted(mass), shifted(pos), on(k)
+    lens = torch.tensor([L, L - 2], dtype=torch.int32)
+    want = O.evict(mass, pos, lens, budget, 3, 50)
+    got = M.cache_evict(kc, None, m, shifted(lens), budget, sinks=3, recent=50, pos=p, mass_out=m, pos_out=p,
+                        src=shifted(torch.zeros(2, 3, budget, dtype=torch.int32)))
+    torch.cuda.synchronize()
+    for x, y in zip(got, want):
+        assert torch.equal(x.cpu(), y)
+    assert torch.equal(O.bits(kc), O.bits(O.move(k, want[1])))

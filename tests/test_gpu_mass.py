@@ -270,3 +270,23 @@ def test_same_sums_every_time():
     got = [M.attend_mass(q, kc, lse, seq, ln, table=table, stream=streams[i % 2]) for i in range(8)]
     torch.cuda.synchronize()
     assert all(torch.equal(x, first) for x in got)
+
+
+@pytest.mark.parametrize("nq,T", [(1, 0), (1, 3), (7, 0), (40, 0), (41, 0)])
+def test_arrays_that_start_anywhere(nq, T):
+    """Every array four bytes behind a 16-byte boundary, batches that are no multiple of four; sums as from aligned ones."""
+    b = Batch(64, "bf16", 3, nq, 130, 10, 8, 2, seed=31)
+    n = T or len(b.seq)
+    _, (q, kc), (seq, ln), table = b.cuda()
+    start = (ln - 60).clamp(min=0)
+    _, lse = M.attend(q, kc, _like(b, kc), seq, ln, table=table, q_start=start, want_lse=True)
+
+    def shifted(x):
+        y = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")[1:].view(x.shape)
+        return y.copy_(x)
+    before = torch.rand(3, 2, b.L, device="cuda")
+    want = M.attend_mass(q[:n], kc, lse[:n], seq[:n], ln[:n], table=table, q_start=start[:n], mass=before)
+    got = M.attend_mass(q[:n], kc, shifted(lse[:n]), shifted(seq[:n]), shifted(ln[:n]), table=shifted(table),
+                        q_start=shifted(start[:n]), mass=shifted(before), out=shifted(torch.empty_like(before)))
+    assert torch.equal(got, want)
+    O.check_mass(got, O.mass(b.q[:n], b.kc, lse[:n], b.seq[:n], b.len[:n], table=b.table, q_start=start[:n], before=before), "shifted")
