@@ -15,10 +15,14 @@
 // The first pass over a row finds its maximum. The second puts every weight (or, for top-k
 // alone, every token) into a histogram over x, 64 bins to the unit, from which the
 // running sums at the bins' edges follow. The third collects the tokens of the few bins in
-// which a filter cuts, and sums what surely remains in segments of 512 tokens; the
-// collected ones are sorted, the cut found among them, and what remains of them is added
-// to the segments. A cut in a bin of too many tokens (flat rows, many equal logits) is
-// found by a radix descent over the row.
+// which a filter cuts, and sums what surely remains in segments of 512 tokens; the cut is
+// found among the collected ones by dividing the range of their places in the order, and what
+// remains of them is added to the segments. A cut in a bin of too many tokens (flat rows, many
+// equal logits) is found by a radix descent over the row.
+//
+// Long rows are bound by vector work: 256 rows of 151643 bf16 logits by top-p 118 us (maximum 14,
+// histogram 40, collection 45, cut and draw 17; their bytes once, 15). Short ones by the latency
+// of one pass behind the other: 4 rows of 32000 by all filters 29 us.
 //
 // Many rows: one workgroup each, all in one launch. Few: several workgroups each, a launch
 // a pass, the last one to finish the third pass drawing the token. The sums being exact,
