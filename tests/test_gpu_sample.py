@@ -267,3 +267,13 @@ def test_many_streams_at_once():
     torch.cuda.synchronize()
     for i, (a, b) in enumerate(got):
         assert torch.equal(a, want[i % 4][0]) and torch.equal(b, want[i % 4][1])
+
+
+@pytest.mark.parametrize("V", [1000, 70000])
+def test_rows_far_apart(V):
+    """Rows more than 2^32 elements apart."""
+    far = (1 << 32) + 8
+    buffer = torch.empty(2 * far + V, dtype=torch.bfloat16, device="cuda")
+    x = buffer.as_strided((3, V), (far, 1))
+    x.copy_(rows(3, V, "bf16", 60))
+    both(x, uniform(3, 60), k=[50, 0, V // 2], p=[0.9, 0.9, 1.0])
