@@ -543,7 +543,7 @@ MISA_API int32_t misa_attend_mass(const misa_kv_cache* cache, const void* q, int
  *            follow their tokens; behind new_len: 0 and -1.
  *   src      int32 [nseq][lists][budget] out: the row that each of the first rows came
  *            from, -1 from new_len on
- *   new_len  int32 [nseq] out
+ *   new_len  int32 [nseq] out; may be lens itself
  * No two rows that a sequence addresses below lens[n] may be one place of memory, and no
  * two sequences may share such rows (a prefix they share is to be kept apart, as
  * misa_attend_shared does). A row whose page, or whose source's page, does not exist is

@@ -691,7 +691,8 @@ def cache_evict(k_cache, v_cache, mass, lens, budget: int, sinks: int = 0, recen
     behind, so rows are in no order afterwards. Returns ``new_len`` [nseq], ``src``
     [nseq, lists, budget] (the row each row came from, -1 behind the last),
     ``mass_out`` and ``pos_out``, where rows have moved along (0 and -1 behind the
-    kept ones; they may be ``mass`` and ``pos``). ``v_cache`` may be None.
+    kept ones; they may be ``mass`` and ``pos``). ``new_len`` may be ``lens``,
+    ``v_cache`` may be None.
     """
     c = _kv_cache(k_cache, v_cache, table)
     dev = k_cache.device

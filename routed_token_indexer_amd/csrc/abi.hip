@@ -1338,7 +1338,8 @@ int32_t misa_cache_evict(const misa_kv_cache* cache, const float* mass, const in
   a.recent = recent;
   a.mass_out = mass_out;
   a.pos_out = pos_out;
-  a.new_len = new_len;
+  b.lens = lens;
+  b.new_len = new_len;
   a.lists = static_cast<int32_t*>(ws);
   hipStream_t st = (hipStream_t)stream;
   hipError_t e = misa::launch_evict_select(a, st);

@@ -361,7 +361,6 @@ __global__ __launch_bounds__(THREADS) void select_kernel(EvictArgs a) {
     if (mass_out) mass_out[i] = 0.f;
     if (pos_out) pos_out[i] = -1;
   }
-  if (threadIdx.x == 0 && list == n * a.G) a.new_len[n] = size;
 }
 
 // ---------------------------------------------------------------- moves
@@ -371,7 +370,8 @@ constexpr int kMoveBatch = 8;       // pieces on their way a thread
 
 // Bound by memory: 16-byte pieces of the rows that move, all heads of a row next to
 // each other. The first wave looks up which of the workgroup's rows move, and the pages
-// of both ends.
+// of both ends. New lengths are written here, one thread a sequence, and not by the selection:
+// several of its workgroups read a sequence's length, and the two may be one array.
 __global__ __launch_bounds__(kMoveThreads) void move_kernel(MoveArgs a, int chunks, int units, FastDiv by_units,
                                                             int heads, FastDiv by_heads) {
   __shared__ int64_t from[kMoveRows], to[kMoveRows];
@@ -399,6 +399,8 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(MoveArgs a, int chun
       to[at] = p1;
     }
     if (threadIdx.x == 0) count = __popcll(b);
+  } else if (threadIdx.x == kMoveRows && a.new_len && chunk == 0 && g == 0) {
+    a.new_len[n] = (int)min((int64_t)min(max(a.lens[n], 0), (int)a.kv.Lmax), a.n);
   }
   __syncthreads();
   const uint32_t pieces = (uint32_t)count * heads * units, all = a.kv.v ? 2 * pieces : pieces;

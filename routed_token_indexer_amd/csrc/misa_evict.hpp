@@ -46,7 +46,6 @@ struct EvictArgs {
   float* mass_out;          // may be mass, or null
   int32_t* pos_out;         // may be pos, or null
   int32_t* src;             // [nseq][G][budget]
-  int32_t* new_len;         // [nseq]
   int32_t* lists;           // [nseq][G][2][min(budget, Lmax)] workspace
 };
 hipError_t launch_evict_select(const EvictArgs& a, hipStream_t st);
@@ -57,6 +56,10 @@ struct MoveArgs {
   const int32_t* src;       // [nseq][G][n]
   int32_t G;
   int64_t n;
+  // behind an eviction (null otherwise): new_len[i] = lens[i], clamped to what a sequence can
+  // address, n at most; may be the same array
+  const int32_t* lens;
+  int32_t* new_len;
 };
 int64_t move_blocks(const MoveArgs& a);   // workgroups (of 256 threads)
 hipError_t launch_move(const MoveArgs& a, hipStream_t st);
