@@ -419,12 +419,13 @@ struct Sampler {
     }
   }
 
-  // The largest logit of this workgroup's segments (-inf: none; NaN is passed over).
+  // The largest logit of this workgroup's segments (-inf: none; NaN is passed over, and by
+  // comparisons: the maximum instruction gives NaN for a signalling one, and loses what came before).
   __device__ __forceinline__ float find_top() {
     float top = -__builtin_inff();
     each(r, g0, g1, [&](int, int, const float* l) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, l[j]);
+      for (int j = 0; j < 8; ++j) top = l[j] > top ? l[j] : top;
     });
 #pragma unroll
     for (int off = 32; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
