@@ -58,7 +58,8 @@ struct Row {
   int V;
   float top;            // largest logit (0 where that is infinite, and all others -inf)
   bool inf;             // it is infinite: such logits stand for 0, all others for -inf
-  float half, fine;     // top / 2; 128 / temperature
+  float lift;           // depth_of's first factor, and
+  float high, fine;     // top times it; 64 / temperature by it
   double inv;           // log2(e) / temperature
   double min_w;         // least weight, in units of 2^-kOne
   int top_k;            // 0: all
@@ -92,9 +93,11 @@ __device__ __forceinline__ float logit(const Row& r, float l) {
   return r.inf ? (l == __builtin_inff() ? 0.f : -__builtin_inff()) : l;
 }
 
-// How far below the maximum, in bins. The order of logits is kept (every step rounds
-// monotonically), nothing overflows, and NaN and -inf give no number below kBins.
-__device__ __forceinline__ float depth_of(const Row& r, float l) { return __builtin_fmaf(l, -0.5f, r.half) * r.fine; }
+// How far below the maximum, in bins: 64 (top - l) / temperature. The order of logits is kept
+// (every step rounds monotonically), no finite logit overflows, and NaN and -inf give no number
+// below kBins. What lies below kBins deep has an exponent above -47 in units of log2, which
+// weights_of relies on.
+__device__ __forceinline__ float depth_of(const Row& r, float l) { return __builtin_fmaf(l, -r.lift, r.high) * r.fine; }
 
 // 2^t in units of 2^-kOne, of two numbers t <= 0 at a time. 2^f of the rest |f| <= 1/2 is 1 + f
 // times the polynomial through (2^f - 1) / f at the zeros of a Chebyshev polynomial (degree 10
@@ -466,8 +469,14 @@ struct Sampler {
     }
     r.inf = top == __builtin_inff();
     r.top = r.inf ? 0.f : top;
-    r.half = 0.5f * r.top;
-    r.fine = fminf(128.f / temperature, 3e38f);
+    // Differences are halved, so that they do not overflow, and scaled. Temperatures below
+    // 2^-120 want a factor beyond fp32. Of a largest logit of 2^-40 and more all different
+    // ones are then far below it (2^-65 at least) by any factor; around smaller ones
+    // differences are lifted first: exact for the largest, and infinite only for logits far below.
+    const bool tiny = temperature < 0x1p-120f, near = tiny && fabsf(r.top) < 0x1p-40f;
+    r.lift = near ? 0x1p60f : 0.5f;
+    r.high = r.lift * r.top;
+    r.fine = near ? (float)(0x1p-54 / (double)temperature) : tiny ? 0x1p127f : 128.f / temperature;
     r.inv = 1.4426950408889634 / (double)temperature;
     const float min_p = a.min_p ? a.min_p[row] : 0.f;
     r.min_w = min_p > 0.f ? (double)fminf(min_p, 1.f) * (double)(1ull << kOne) : 0.0;
