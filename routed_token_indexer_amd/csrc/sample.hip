@@ -664,8 +664,8 @@ struct Sampler {
     Shared& s = lds();
     scan_bins(kSegments);
     const u64 total = s.seg[kMaxSegs - 1];
-    const float u = a.u[row];
-    u64 drawn = u > 0.f ? (u64)((double)u * (double)total) : 0;
+    const float u = a.u[row];          // a product beyond 64 bits has no defined value
+    u64 drawn = u > 0.f ? (u64)((double)fminf(u, 1.f) * (double)total) : 0;
     if (drawn >= total) drawn = total - 1;
     const int g = first_bin(kSegments, drawn + 1), i = g * kSeg + (int)threadIdx.x;
     const u64 before = upto(kSegments, g);

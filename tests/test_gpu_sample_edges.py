@@ -1,4 +1,4 @@
-"""Sampling at the edges of its numbers: the smallest temperatures, signalling NaN."""
+"""Sampling at the edges of its numbers: the smallest temperatures, signalling NaN, random numbers out of range."""
 import math
 
 import pytest
@@ -79,3 +79,14 @@ def test_signalling_nan(V, dtype, bits):
     both(x, u, t=[0.0] * 4)
     raw[:] = bits[0]
     assert M.sample(x, torch.tensor(u).cuda())[0].tolist() == [-1] * 4
+
+
+@pytest.mark.parametrize("V", [900, 70001])
+def test_random_numbers_out_of_range(V):
+    """1 and more pick the last kept token, 0 and less and NaN the first."""
+    u = [1.0, 1.5, 2.0 ** 22, 1e10, 1e30, 3.4e38, math.inf, 0.0, -0.0, -1e30, -math.inf, math.nan, -LEAST, LEAST]
+    x = torch.zeros(len(u), V).cuda()
+    x[:, ::2] = -1.0
+    for o in ({}, dict(k=[30] * len(u)), dict(p=[0.5] * len(u)), dict(m=[0.9] * len(u))):
+        got = both(x, u, strict=False, **o).tolist()
+        assert len(set(got[:7])) == 1 and len(set(got[7:])) == 1 and got[0] > got[7], got
