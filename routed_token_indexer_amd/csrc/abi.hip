@@ -1321,8 +1321,8 @@ int32_t misa_cache_evict(const misa_kv_cache* cache, const float* mass, const in
     return fail(MISA_ERR_ALIGN, "%s: mass, pos, lens, mass_out, pos_out, src and new_len must be 4-byte aligned", fn);
   misa::MoveArgs b{};
   b.kv = a.kv;
-  b.Hkv = a.Hkv = cache->heads;
-  b.d = a.d = cache->d;
+  b.Hkv = cache->heads;
+  b.d = cache->d;
   b.G = a.G = lists;
   b.src = a.src = src;
   b.n = a.budget = budget;

@@ -37,7 +37,6 @@ hipError_t launch_mass(const MassArgs& a, bool half, hipStream_t st);
 
 struct EvictArgs {
   KvView kv;
-  int32_t Hkv, d;
   const float* mass;        // [nseq][G][Lmax]
   const int32_t* pos;       // the same shape, or null: row numbers
   const int32_t* lens;      // [nseq]
