@@ -502,14 +502,19 @@ MISA_API size_t misa_attend_workspace_bytes(int32_t op, int64_t T, int32_t Hq, i
  *     out[n][g][s] = in[n][g][s] + sum over the queries t of sequence n that see s, and
  *                    the heads j of kv head g, of  exp(x_s - lse[t][j])
  * for every token s that a sequence can address (L = table_cols * page, or page without
- * a table). Keys are read once, values not at all (cache->v may be NULL).
- *   lse     fp32 [T][Hq]; a row of -inf (a query that sees nothing) gives nothing
+ * a table). Keys are read once for each part that their queries are split into (decode
+ * steps: once), values not at all (cache->v may be NULL).
+ *   lse     fp32 [T][Hq]; a row of -inf (a query that sees nothing) gives nothing. Of
+ *           misa_attend over the same interval: the log-sums of misa_attend_selected count
+ *           the selected tokens alone, and tokens that were not selected would still be given
+ *           weight here
  *   lists   cache->heads: a sum per kv head; 1: one sum over all heads
  *   in      fp32 [nseq][lists][L] or NULL (zeros);  out  the same shape, every element
  *           written; may be in itself
  * The queries of a call may stand in any order; those of a sequence next to each other
- * are fastest. The last queries of a prompt, all of them, or a decode step's make such a
- * sum alike. It is the same from run to run: nothing depends on the order of workgroups.
+ * are fastest. How many queries are taken at a time goes by T / nseq, so the table should
+ * hold the batch's sequences, not a whole pool's. The last queries of a prompt, all of them,
+ * or a decode step's make such a sum alike. It is the same from run to run: nothing depends on the order of workgroups.
  * What a query does not see may hold anything; tokens without a page get nothing.
  *   ws: misa_cache_workspace_bytes(MISA_OP_ATTEND_MASS, cache, T, Hq, lists, 0)
  * Errors: as misa_attend (d in {64, 128, 256}); MISA_ERR_ARG for lists neither 1 nor

@@ -102,9 +102,10 @@ struct Select {
 // parts and counting, until at most 64 are left: once where masses differ, twice where rows
 // decide.
 //
-// Bound by latency: one CU a list, and a list is read once. Of 4 lists of 32768 rows to 2048
-// (30 us; a MB read): latest position 2, keys 6, the division 8, last candidates 3.5, counts
-// and lists of moves 9, writes 5.5. Of 512 lists of 2112 rows (9 us): 2, 1, 2.5, 0.6, 1, 2.
+// Bound by latency: one CU a list, one sweep behind the other. Of 32 lists of up to 32768 rows
+// (4 sequences, 8 heads) to 2048, the longest list (29 us): latest position 2, keys 5, the
+// division 5, last candidates 3, counts and lists of moves 8.5, writes 5.5. Of 64 lists of 2112
+// rows (8.4 us): 0.8, 1.1, 1.9, 0.8, 1.6, 2.2.
 template <int THREADS, int CAP>
 __global__ __launch_bounds__(THREADS) void select_kernel(EvictArgs a) {
   using S = Select<THREADS>;
@@ -432,11 +433,14 @@ __global__ __launch_bounds__(kMoveThreads) void move_kernel(MoveArgs a, int chun
 hipError_t launch_evict_select(const EvictArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.kv.nseq * a.G));
   const int64_t L = a.kv.Lmax;
-  // Short lists: half the waves and a sixth of the LDS, so that several lists share a CU (512
-  // lists of 2112 rows to 2048, moves included: 19.9 us, against 21.6 with the next shape and
-  // 22.9 with keys read again). Keys in LDS as long as they fit: 4 lists of 32768 rows to 2048
-  // 43.5 us against 55.8, 512 of 30000 109 against 130; a shape for 8192 rows gained nothing
-  // (512 lists 48.0 us, 48.4 with the one for 32768).
+  // By the rows that a sequence can address: how many it holds is known on the device alone.
+  // (Times: selection and moves of rows of 8 elements, to a budget of 2048.) Short lists: half the
+  // waves and a sixth of the LDS, so that several lists share a CU: 512 lists of 2112 rows 28 us,
+  // against 37 with the next shape and 42 with keys read again; 64 lists, which have a CU each, 13.8
+  // against 14.8 and 17.8. Keys in LDS as long as they fit: 32 lists of 32768 rows 35 us against 48,
+  // 512 of 30000 131 against 163. A shape for 8192 rows gained nothing (512 lists 50 us either way).
+  // Few tokens in long rows cost what the rows do: 64 lists of 2112 tokens 14 us in rows of 4096, 19
+  // in rows of 32768, 25 in rows of 65536, whose ends are cleared by one workgroup a list.
   if (L <= 4096) hipLaunchKernelGGL((select_kernel<512, 4096>), grid, dim3(512), 0, st, a);
   else if (L <= 32768) hipLaunchKernelGGL((select_kernel<1024, 32768>), grid, dim3(1024), 0, st, a);
   else hipLaunchKernelGGL((select_kernel<1024, 0>), grid, dim3(1024), 0, st, a);

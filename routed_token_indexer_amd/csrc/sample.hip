@@ -22,7 +22,10 @@
 //
 // Long rows are bound by vector work: 256 rows of 151643 bf16 logits by top-p 118 us (maximum 14,
 // histogram 40, collection 45, cut and draw 17; their bytes once, 15). Short ones by the latency
-// of one pass behind the other: 4 rows of 32000 by all filters 29 us.
+// of one pass behind the other: 4 rows of 32000 by all filters 29 us. Rows that need the descent take
+// its passes over the row, by one workgroup each: nearly flat rows by top-p 130 us (4 of 32000), 450 (64
+// of 128000) and 620 (256 of 151643), by top-k and top-p 200, 750 and 1040; by temperature alone any row
+// takes two passes (19, 25 and 67 us).
 //
 // Many rows: one workgroup each, all in one launch. Few: several workgroups each, a launch
 // a pass, the last one to finish the third pass drawing the token. The sums being exact,
